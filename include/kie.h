@@ -272,6 +272,123 @@ int kie_create_moe_with_buffers(const kie_config *cfg, const kie_moe_config *moe
                                 void *kv_dev, size_t kv_bytes, void *workspace_dev, size_t workspace_bytes,
                                 kie_ctx **out);
 
+/* ---- a paged K/V cache for a batch of sequences --------------------------------------------------------
+ * No counterpart on the pages (they decode one request): operators for a program that serves several sequences
+ * next to the batch-1 decoder above. The K/V rows of one layer lie in n_blocks pages of block_size positions;
+ * block_table[seq][i] (int32) is the page of positions i * block_size .. of a sequence, and the slot of a position
+ * is page * block_size + offset. kie_paged_extend gives sequences the pages of their new tokens and lists the
+ * slot of each; kie_paged_append writes the tokens' K/V rows there (rotating q and k); kie_paged_attention attends
+ * over the pages; kie_paged_release takes finished sequences' pages back.
+ *
+ * For all of them: every pointer is a DEVICE pointer of the current device; the call enqueues on `stream` (NULL =
+ * the legacy default stream) and returns without synchronising; it allocates nothing, so it may be captured into a
+ * graph; the argument struct is read before it returns. Calls that share no output and no workspace may overlap.
+ * Errors: KIE_ERR_INVALID (message in kie_paged_last_error, per host thread) before anything is enqueued, or
+ * KIE_ERR_CUDA. Index and length arrays live on the device and are not checked by the host: the kernels ignore what
+ * is out of range, as said at each call. */
+enum { KIE_F16 = 0, KIE_BF16 = 1, KIE_F32 = 2, KIE_E4M3 = 3 };
+
+/* The pages of one layer. k and v: element (page, kv head, position in the page, i) at page * stride[0] +
+ * head * stride[1] + position * stride[2] + i, strides in elements, each a multiple of 16 bytes, as are the
+ * addresses. dtype KIE_F16, KIE_BF16 or KIE_E4M3. E4M3 codes (OCP "fn") have one fp32 scale per row, at
+ * k_scale / v_scale [page * scale_stride[0] + head * scale_stride[1] + position * scale_stride[2]], the value being
+ * code * scale, as in the FP8 experts' rows above; else the scales are not read (may be NULL). head_dim 64 or 128;
+ * block_size a multiple of 16; n_blocks * block_size < 2^31. */
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int64_t k_stride[3], v_stride[3], k_scale_stride[3], v_scale_stride[3];
+  int n_blocks, n_kv_heads, block_size, head_dim, dtype;
+} kie_pages;
+
+/* Pages and slots for new tokens. Request r holds lens[r] positions and brings new_lens[r] tokens; the tokens of
+ * all requests are packed in request order into n_rows rows. Requests are taken in order: request r is admitted if
+ * its table row has room (lens + new <= max_blocks * block_size), its rows end within n_rows, and the pages that it
+ * and all requests before it need do not exceed n_free (a request that needs none is admitted anyway). A request
+ * with a negative length is not admitted and counts no rows. Page j of the new ones (numbered over all requests in
+ * order) is free_blocks[n_free - 1 - j]: the list is a stack.
+ * Written: the new entries of block_table (the others stay), lens_out [n_seqs] (lens + new, or lens if not
+ * admitted), n_free_out [1], admitted [n_seqs] (bytes 0 / 1), row_start [n_seqs + 1] (the requests' first rows) and,
+ * per row, slots, positions and seqs [n_rows]: -1 for rows of requests not admitted and for rows behind the last.
+ * lens_out and n_free_out must not be lens and n_free. */
+typedef struct {
+  const int32_t *lens, *new_lens, *free_blocks, *n_free;
+  int32_t *block_table;
+  int64_t table_stride;
+  int32_t *lens_out, *n_free_out, *row_start, *slots, *positions, *seqs;
+  uint8_t *admitted;
+  int n_seqs, max_blocks, block_size, n_rows, free_capacity;
+} kie_paged_extend_args;
+int kie_paged_extend(const kie_paged_extend_args *a, void *stream);
+
+/* Pages of finished requests (done[r] != 0, bytes) go back on the free list: free_blocks[n_free ...] receives their
+ * block_table entries, requests in order, pages in order (those past free_capacity are dropped). lens_out: 0 for the
+ * finished, else lens; n_free_out [1]. The table rows stay as they were. lens_out and n_free_out must not be lens
+ * and n_free. */
+typedef struct {
+  const uint8_t *done;
+  const int32_t *lens, *n_free, *block_table;
+  int64_t table_stride;
+  int32_t *free_blocks, *lens_out, *n_free_out;
+  int n_seqs, max_blocks, block_size, free_capacity;
+} kie_paged_release_args;
+int kie_paged_release(const kie_paged_release_args *a, void *stream);
+
+/* K/V rows into their slots: row t of k and v ([n_rows] x [n_kv_heads] x [head_dim], strides {row, head} in
+ * elements, head_dim contiguous) goes to slot slots[t] of the pages, and q, if given, to q_out (the same type;
+ * q_out may be q with the same strides). All inputs are x_dtype (KIE_F16, KIE_BF16, KIE_F32). With a table
+ * rope [n_pos][head_dim / 2] of (cos, sin) fp32 pairs, k and q are rotated first at positions[t] (pairs
+ * (i, i + head_dim / 2), in fp32: x_i c - x_j s, x_j c + x_i s); v never. Rows are rounded to the cache's type once;
+ * an E4M3 row gets the scale max|x| / 448 (2^-126 for a zero row) and the codes of x / scale. A row whose slot lies
+ * outside the pages, or whose position lies outside the table, is padding: nothing is written for it. Slots must
+ * not repeat: of two rows with the same slot, each 16 bytes and each scale may come from either.
+ * k_pairs != 0: k rows hold each pair (i, i + head_dim / 2) in adjacent elements, as the K planes of a ctx's cache
+ * do ([n_layers][2][n_kv_heads][max_seq][head_dim], kie_buffer_sizes), so that a prompt that a ctx has prefilled can
+ * be copied into pages; the pages always hold plain order. */
+typedef struct {
+  kie_pages pages;
+  const void *k, *v, *q;
+  void *q_out;
+  int64_t k_stride[2], v_stride[2], q_stride[2], q_out_stride[2];
+  const int32_t *slots, *positions;
+  const float *rope;
+  int n_rows, n_heads, n_pos, x_dtype, k_pairs;
+} kie_paged_append_args;
+int kie_paged_append(const kie_paged_append_args *a, void *stream);
+
+/* Attention of one new token per sequence: for query head h of sequence b (kv head h / (n_heads / n_kv_heads), up
+ * to 8 query heads each), out = sum_j p_j V_j with p = softmax(scale * q . K_j) over the positions j in
+ * [max(0, lens[b] - window), lens[b]) (window 0: all), and lse (if not NULL) = ln sum exp(scale * q . K_j). The new
+ * token's own row is already in the pages (it is position lens[b] - 1). A sequence of length <= 0 gets zeros and an
+ * lse of -inf; lengths past max_blocks * block_size are cut there. Positions on a page outside [0, n_blocks) are
+ * left out. Rows behind a sequence's end are never read. q, out: q_dtype, strides {sequence, head} in elements,
+ * head_dim contiguous; lse [n_seqs][n_heads]. q_dtype is KIE_F32 (F16 and E4M3 pages), or the pages' own 16-bit
+ * type, or either 16-bit type for E4M3 pages. Sums and the softmax are fp32; fp32 queries and the weights p go
+ * through the tensor cores as two 16-bit parts.
+ * workspace: kie_paged_attention_workspace bytes, 256-byte aligned, contents arbitrary before and after; calls that
+ * may overlap need one each. */
+typedef struct {
+  kie_pages pages;
+  const void *q;
+  void *out;
+  float *lse;
+  int64_t q_stride[2], out_stride[2];
+  const int32_t *block_table, *lens;
+  int64_t table_stride;
+  void *workspace;
+  size_t workspace_bytes;
+  float scale;
+  int n_seqs, n_heads, max_blocks, window, q_dtype;
+} kie_paged_attention_args;
+int kie_paged_attention(const kie_paged_attention_args *a, void *stream);
+
+/* Bytes of kie_paged_attention's workspace on the current device, for any number of sequences (0: bad arguments or
+ * no device). */
+size_t kie_paged_attention_workspace(int n_heads, int n_kv_heads, int head_dim);
+
+/* Message of this host thread's last failed kie_paged_* call ("" before the first). */
+const char *kie_paged_last_error(void);
+
 /* Host-side layout query (no GPU needed): byte offset of code Q[r][c] inside a packed FP8 matrix [M, K]
  * (column blocks of 512 codes, each CTA's rows in tiles of up to 32 rows; within a full 512-code block the
  * 16-code chunk q of an odd row r is stored at chunk q ^ 4). M even, K a multiple of 16; -1 for bad

@@ -20,8 +20,9 @@ _CSRC = os.path.join(_HERE, "csrc")
 _INCLUDE = os.path.join(_ROOT, "include")
 _BUILD = os.path.join(_ROOT, "_build")
 LIB_PATH = os.path.join(_HERE, "libkie.so")
-SOURCES = ("kie_api.cu", "kie_decode.cu", "kie_gemv.cu", "kie_prefill.cu")
-HEADERS = ("kie_layout.h", "kie_device.cuh", "kie_decode.cuh", "kie_prefill.cuh", "kie_tcgemm.cuh", "kie_tcattn.cuh")
+SOURCES = ("kie_api.cu", "kie_decode.cu", "kie_gemv.cu", "kie_prefill.cu", "kie_paged.cu", "kie_paged_attn.cu")
+HEADERS = ("kie_layout.h", "kie_device.cuh", "kie_decode.cuh", "kie_prefill.cuh", "kie_tcgemm.cuh", "kie_tcattn.cuh",
+           "kie_paged.cuh")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 KIE_OK, KIE_ERR_INVALID, KIE_ERR_OOM, KIE_ERR_CAPACITY = 0, -1, -2, -3
@@ -122,6 +123,42 @@ class KieBarrierStats(ctypes.Structure):
                 ("mean_latency_ns", ctypes.c_double), ("total_ns", ctypes.c_double)]
 
 
+I64x2, I64x3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
+
+
+class KiePages(ctypes.Structure):
+    _fields_ = [("k", P), ("v", P), ("k_scale", P), ("v_scale", P), ("k_stride", I64x3), ("v_stride", I64x3),
+                ("k_scale_stride", I64x3), ("v_scale_stride", I64x3)] + \
+               [(n, ctypes.c_int) for n in ("n_blocks", "n_kv_heads", "block_size", "head_dim", "dtype")]
+
+
+class KiePagedExtendArgs(ctypes.Structure):
+    _fields_ = [(n, P) for n in ("lens", "new_lens", "free_blocks", "n_free", "block_table")] + \
+               [("table_stride", ctypes.c_int64)] + \
+               [(n, P) for n in ("lens_out", "n_free_out", "row_start", "slots", "positions", "seqs", "admitted")] + \
+               [(n, ctypes.c_int) for n in ("n_seqs", "max_blocks", "block_size", "n_rows", "free_capacity")]
+
+
+class KiePagedReleaseArgs(ctypes.Structure):
+    _fields_ = [(n, P) for n in ("done", "lens", "n_free", "block_table")] + [("table_stride", ctypes.c_int64)] + \
+               [(n, P) for n in ("free_blocks", "lens_out", "n_free_out")] + \
+               [(n, ctypes.c_int) for n in ("n_seqs", "max_blocks", "block_size", "free_capacity")]
+
+
+class KiePagedAppendArgs(ctypes.Structure):
+    _fields_ = [("pages", KiePages)] + [(n, P) for n in ("k", "v", "q", "q_out")] + \
+               [(n, I64x2) for n in ("k_stride", "v_stride", "q_stride", "q_out_stride")] + \
+               [(n, P) for n in ("slots", "positions", "rope")] + \
+               [(n, ctypes.c_int) for n in ("n_rows", "n_heads", "n_pos", "x_dtype", "k_pairs")]
+
+
+class KiePagedAttentionArgs(ctypes.Structure):
+    _fields_ = [("pages", KiePages), ("q", P), ("out", P), ("lse", P), ("q_stride", I64x2), ("out_stride", I64x2),
+                ("block_table", P), ("lens", P), ("table_stride", ctypes.c_int64), ("workspace", P),
+                ("workspace_bytes", ctypes.c_size_t), ("scale", ctypes.c_float)] + \
+               [(n, ctypes.c_int) for n in ("n_seqs", "n_heads", "max_blocks", "window", "q_dtype")]
+
+
 # Every entry point of include/kie.h with its ctypes signature.
 SIGNATURES = {
     "kie_query_buffers": ([P, ctypes.c_int, P], ctypes.c_int),
@@ -156,6 +193,12 @@ SIGNATURES = {
                                     ctypes.c_int),
     "kie_packed_offset_fp8": ([ctypes.c_int] * 5, ctypes.c_int64),
     "kie_tc_tile_offset": ([ctypes.c_int] * 4, ctypes.c_int64),
+    "kie_paged_extend": ([P, P], ctypes.c_int),
+    "kie_paged_release": ([P, P], ctypes.c_int),
+    "kie_paged_append": ([P, P], ctypes.c_int),
+    "kie_paged_attention": ([P, P], ctypes.c_int),
+    "kie_paged_attention_workspace": ([ctypes.c_int] * 3, ctypes.c_size_t),
+    "kie_paged_last_error": ([], ctypes.c_char_p),
 }
 
 _lib = None
@@ -436,3 +479,8 @@ def rows_of_cta(M: int, n_cta: int, cta: int):
     r0, r1 = ctypes.c_int(), ctypes.c_int()
     _check(lib().kie_rows_of_cta(M, n_cta, cta, ctypes.byref(r0), ctypes.byref(r1)))
     return r0.value, r1.value
+
+
+# ---- paged K/V cache for a batch of sequences ----------------------------------------------------------------
+from .paged import (PagedCache, PagedStep, paged_append, paged_attention, paged_extend,  # noqa: E402,F401
+                    paged_release, rope_table)

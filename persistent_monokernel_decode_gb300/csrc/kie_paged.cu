@@ -158,59 +158,6 @@ __global__ void __launch_bounds__(PX_THREADS) paged_release_kernel(const kie_pag
 
 // ---- append -------------------------------------------------------------------------------------------------
 
-// Eight consecutive elements at p + i as fp32; VEC: p + i is aligned for 16-byte accesses.
-template <bool VEC>
-__device__ __forceinline__ void load8(const void *p, int64_t i, int dtype, float (&v)[8]) {
-  if (!VEC) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = paged_load(p, i + e, dtype);
-    return;
-  }
-  if (dtype == KIE_F32) {
-    const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-    const float4 x = s[0], y = s[1];
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-    return;
-  }
-  const uint4 r = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (dtype == KIE_F16) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
-      v[2 * e] = f.x, v[2 * e + 1] = f.y;
-    } else {
-      v[2 * e] = __uint_as_float(w[e] << 16), v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
-  }
-}
-
-__device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
-  if (dtype == KIE_F16) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-  }
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-template <bool VEC>
-__device__ __forceinline__ void store8(void *p, int64_t i, int dtype, const float (&v)[8]) {
-  if (!VEC) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) paged_store(p, i + e, dtype, v[e]);
-    return;
-  }
-  if (dtype == KIE_F32) {
-    float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-    d[0] = make_float4(v[0], v[1], v[2], v[3]);
-    d[1] = make_float4(v[4], v[5], v[6], v[7]);
-    return;
-  }
-  *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) =
-      make_uint4(pack2(v[0], v[1], dtype), pack2(v[2], v[3], dtype), pack2(v[4], v[5], dtype), pack2(v[6], v[7], dtype));
-}
-
 // Maximum that keeps a NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -458,9 +405,10 @@ int kie_paged_attention(const kie_paged_attention_args *p, void *stream) {
   if (a.n_seqs == 0) return KIE_OK;
   if (!a.q || !a.out || !a.block_table || !a.lens) return refuse("q, out, block_table or lens is NULL");
   if (a.n_seqs > 1 && a.table_stride < a.max_blocks) return refuse("table_stride is below max_blocks");
-  const size_t need = kie_paged_attention_workspace(a.n_heads, a.pages.n_kv_heads, a.pages.head_dim);
-  if (need == 0) return finish(cudaErrorInvalidDevice, "device query");
+  int dev, sms;
+  if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
+  const size_t need = kie_paged_attention_workspace_bytes(a.n_heads, a.pages.n_kv_heads, a.pages.head_dim, sms);
   if (!a.workspace || a.workspace_bytes < need || !aligned(a.workspace, 256))
     return refuse("the workspace is NULL, unaligned (256 bytes) or smaller than kie_paged_attention_workspace");
-  return finish(kie_launch_paged_attention(a, (cudaStream_t)stream), "paged_attention");
+  return finish(kie_launch_paged_attention(a, sms, (cudaStream_t)stream), "paged_attention");
 }

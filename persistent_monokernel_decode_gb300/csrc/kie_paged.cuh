@@ -33,11 +33,74 @@ __device__ __forceinline__ void paged_store(void *p, int64_t i, int dtype, float
     static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
 }
 
-__device__ __forceinline__ float paged_from_e4m3(uint8_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+// Eight consecutive elements at p + i as fp32; VEC: p + i is aligned for 16-byte accesses.
+template <bool VEC>
+__device__ __forceinline__ void load8(const void *p, int64_t i, int dtype, float (&v)[8]) {
+  if (!VEC) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = paged_load(p, i + e, dtype);
+    return;
+  }
+  if (dtype == KIE_F32) {
+    const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+    const float4 x = s[0], y = s[1];
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    return;
+  }
+  const uint4 r = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (dtype == KIE_F16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+      v[2 * e] = f.x, v[2 * e + 1] = f.y;
+    } else {
+      v[2 * e] = __uint_as_float(w[e] << 16), v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
+  if (dtype == KIE_F16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(void *p, int64_t i, int dtype, const float (&v)[8]) {
+  if (!VEC) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) paged_store(p, i + e, dtype, v[e]);
+    return;
+  }
+  if (dtype == KIE_F32) {
+    float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
+    d[0] = make_float4(v[0], v[1], v[2], v[3]);
+    d[1] = make_float4(v[4], v[5], v[6], v[7]);
+    return;
+  }
+  *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) =
+      make_uint4(pack2(v[0], v[1], dtype), pack2(v[2], v[3], dtype), pack2(v[4], v[5], dtype), pack2(v[6], v[7], dtype));
+}
+
+// Four dimensions d .. d + 3 of a query head's output from its weighted sum, and its lse from the reference M (log2
+// units) and the sum of weights L: zeros and -inf where nothing was attended.
+__device__ __forceinline__ void paged_finish4(const kie_paged_attention_args &a, int b, int64_t head, int d, float4 acc,
+                                              float M, float L) {
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int64_t to = b * a.out_stride[0] + head * a.out_stride[1] + d;
+  paged_store(a.out, to, a.q_dtype, acc.x * inv);
+  paged_store(a.out, to + 1, a.q_dtype, acc.y * inv);
+  paged_store(a.out, to + 2, a.q_dtype, acc.z * inv);
+  paged_store(a.out, to + 3, a.q_dtype, acc.w * inv);
+  if (d == 0 && a.lse)
+    a.lse[(int64_t)b * a.n_heads + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
 }  // namespace kie
 
-cudaError_t kie_launch_paged_attention(const kie_paged_attention_args &a, cudaStream_t stream);
+cudaError_t kie_launch_paged_attention(const kie_paged_attention_args &a, int sms, cudaStream_t stream);
 size_t kie_paged_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim, int sms);

@@ -394,7 +394,7 @@ int kie_paged_attention(const kie_paged_attention_args *p, void *stream) {
   const kie_paged_attention_args &a = *p;
   if (const char *e = check_pages(a.pages)) return refuse(e);
   if (a.n_seqs < 0 || a.max_blocks < 1 || a.window < 0) return refuse("n_seqs and window must be >= 0 and max_blocks >= 1");
-  if ((int64_t)a.max_blocks * a.pages.block_size > INT_MAX) return refuse("max_blocks * block_size must be below 2^31");
+  if ((int64_t)a.max_blocks * a.pages.block_size > 1 << 30) return refuse("max_blocks * block_size must not pass 2^30");
   if (a.n_heads < 1 || a.n_heads % a.pages.n_kv_heads) return refuse("n_heads must be a multiple of n_kv_heads");
   if (a.n_heads / a.pages.n_kv_heads > PAGED_MAX_GROUP) return refuse("more than 8 query heads per KV head");
   if ((int64_t)a.n_seqs * a.n_heads > INT_MAX) return refuse("n_seqs * n_heads must be below 2^31");

@@ -5,11 +5,15 @@
 // the GPU alike; a block keeps the whole items of its run to itself and publishes the pieces of the (at most two)
 // items that it shares with its neighbours, which a second kernel joins.
 //
-// Inside a block each of four warps takes 16 positions of a unit. Both products run as mma.sync m16n8k16 with the
-// KV head's query heads (at most 8) as rows 0-7 of A and, where 16 bits do not hold a value exactly, its remainder
-// in rows 8-15: S = Q K^T, then O += P V with the weights P as two 16-bit parts, the accumulators' two row halves being
-// summed in the same lane. The running maximum, sum and output of a warp's positions stay in registers; a tile's
-// scores never leave the lanes that hold them (the accumulator of S is the A operand of P V).
+// Inside a block each of four warps takes a quarter of a unit, one tile. Both products run as mma.sync m16n8k16 in the
+// transposed form, so that no row of an instruction is wasted on the at most 8 query heads of a KV head: S^T = K Q^T
+// (16 positions x 8 heads) and O^T += V^T P^T (16 dimensions x 8 heads). K is the A operand as it lies in shared memory
+// (ldmatrix), V through ldmatrix.trans; the weights P pass from accumulator to B operand with movmatrix. Where 16 bits
+// do not hold a B value exactly (fp32 queries; the weights), its remainder goes through a second mma. The running sum
+// and output of a warp's positions stay in registers.
+//
+// The reference of the softmax is not the running maximum but a value that stays within 2^8 of it: weights up to 2^15
+// fit in fp16, so it is only moved (with the shuffles and the rescaling that this costs) when a weight passes that.
 #include <float.h>
 
 #include "kie_device.cuh"
@@ -20,37 +24,44 @@ namespace {
 
 constexpr int PA_WARPS = 4;
 constexpr int PA_THREADS = PA_WARPS * 32;
-constexpr int PA_TILE = 16;                 // positions of a warp's tile: the k of one P V step; pages are multiples
-constexpr int PA_UNIT = PA_WARPS * PA_TILE;
-constexpr int PA_BLOCKS_PER_SM = 2;
+constexpr int PA_BLOCKS_PER_SM = 3;
 constexpr int PA_ROWS = PAGED_MAX_GROUP;
-constexpr int PA_RING_BYTES = 24 * 1024;    // a warp's ring: 4 warps x 2 blocks x 24 KB = 192 KB of an SM
-constexpr int PA_MAX_SLOTS = 12;
+constexpr int PA_RING_BYTES = 16 * 1024;    // a warp's ring: 4 warps x 3 blocks x 16 KB = 192 KB of an SM
 constexpr float LOG2E = 1.4426950408889634f;
-// fp16 weights are kept as 2^14 p: an fp16 pair then holds them to 2^-39 of the largest instead of 2^-25.
-constexpr float P_BIAS = 14.f;
+// Weights are kept as 2^7 2^(v - ref): an fp16 pair holds them to 2^-25, which is 2^-32 of the largest.
+constexpr float P_BIAS = 7.f, P_LIMIT = 32768.f;
+// Scales of E4M3 value rows count into the reference down to this (log2), so that the plain weights stay finite.
+constexpr float MIN_LOG2_SCALE = -60.f;
 
 enum { PG_F16 = 0, PG_BF16 = 1, PG_E4M3 = 2 };
 
-__host__ __device__ constexpr int pa_half_bytes(int kind, int dh) { return PA_TILE * dh * (kind == PG_E4M3 ? 1 : 2); }
-__host__ __device__ constexpr int pa_slots(int kind, int dh) {
-  return PA_RING_BYTES / pa_half_bytes(kind, dh) < PA_MAX_SLOTS ? PA_RING_BYTES / pa_half_bytes(kind, dh) : PA_MAX_SLOTS;
-}
-
-// A block's shared memory: the warps' rings, the E4M3 scales of each ring entry, the joining of the four warps.
+// A warp's tile: 16 positions (32 of E4M3), as one half of K rows and one of V rows of 32 * DH bytes each.
 template <int KIND, int DH>
-struct PaSmem {
-  static constexpr int NS = pa_slots(KIND, DH), HALF = pa_half_bytes(KIND, DH);
-  uint8_t ring[PA_WARPS][NS][HALF];
-  float scale[PA_WARPS][KIND == PG_E4M3 ? NS : 1][PA_TILE];
-  float o[PA_WARPS][PA_ROWS][DH];
-  float m[PA_WARPS][PA_ROWS], l[PA_WARPS][PA_ROWS];
-  uint32_t live[PA_WARPS][NS / 2];
+struct PaTile {
+  static constexpr int ES = KIND == PG_E4M3 ? 1 : 2, SUBS = KIND == PG_E4M3 ? 2 : 1;  // 16-position parts
+  static constexpr int POS = 16 * SUBS, UNIT = POS * PA_WARPS;
+  static constexpr int ROW = DH * ES, CH = ROW / 16, HALF = POS * ROW;  // bytes; 16-byte chunks of a row
+  static constexpr int NS = PA_RING_BYTES / HALF;                       // ring slots, a half each
+  static constexpr int LOADS = HALF / 512;                              // chunks each lane copies
 };
 
-__device__ __forceinline__ void cp_async16(void *dst, const void *src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0)
-               : "memory");
+// A block's shared memory: the warps' rings (the slot last used also joins the four warps), the E4M3 scales of each
+// slot, which positions of it are live, and the warps' references and sums.
+template <int KIND, int DH>
+struct PaSmem {
+  using T = PaTile<KIND, DH>;
+  uint8_t ring[PA_WARPS][T::NS][T::HALF];
+  float scale[PA_WARPS][KIND == PG_E4M3 ? T::NS : 1][32];
+  float m[PA_WARPS][PA_ROWS], l[PA_WARPS][PA_ROWS];
+  uint32_t live[PA_WARPS][T::NS];
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The same where live, else 16 zero bytes (nothing is read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async4(void *dst, const void *src, bool live) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 4 : 0) : "memory");
@@ -60,17 +71,17 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// x = mant * 2^e with 1 <= |mant| < 2 (below 2^-126: e = -126 and |mant| < 1; an infinity or NaN is its own mant).
-__device__ __forceinline__ void split_exponent(float x, float *mant, float *e) {
-  const uint32_t bits = __float_as_uint(x), field = (bits >> 23) & 255u;
-  *mant = field == 0u ? x * 0x1p126f : field == 255u ? x : __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);
-  *e = (float)(field == 0u ? -126 : (int)field - 127);
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 template <int KIND>
@@ -83,6 +94,24 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at)
+               : "memory");
+}
+// The transpose of an 8 x 8 matrix of 16-bit elements held as two neighbours per lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
 template <int KIND>
@@ -109,21 +138,23 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
 
 // ---- the list of units --------------------------------------------------------------------------------------
 
-// One sequence's span: positions [lo, len), its tiles from tile0 on, in n units (at least one, so that a sequence of
-// no positions still writes its zeros).
+// One sequence's span: positions [lo, len), in n units of UNIT positions from `from` on, a multiple of 16 (at least one
+// unit, so that a sequence of no positions still writes its zeros).
 struct Span {
-  int lo, len, tile0, n;
+  int lo, len, from, n;
 };
+template <int UNIT>
 __device__ __forceinline__ Span span_of(const kie_paged_attention_args &a, int b) {
   Span s;
-  s.len = (int)min((int64_t)max(a.lens[b], 0), (int64_t)a.max_blocks * a.pages.block_size);
+  s.len = min(max(a.lens[b], 0), a.max_blocks * a.pages.block_size);
   s.lo = a.window > 0 ? max(0, s.len - a.window) : 0;
-  s.tile0 = s.lo / PA_TILE;
-  s.n = max(1, (s.len - s.tile0 * PA_TILE + PA_UNIT - 1) / PA_UNIT);
+  s.from = s.lo & ~15;
+  s.n = max(1, (int)((unsigned)(s.len - s.from + UNIT - 1) / UNIT));
   return s;
 }
 
 // A place in the list: unit `unit` of item (b, h).
+template <int UNIT>
 struct Cursor {
   Span s;
   int b, h, unit;
@@ -132,13 +163,14 @@ struct Cursor {
     unit = 0;
     if (++h < a.pages.n_kv_heads) return;
     h = 0;
-    if (++b < a.n_seqs) s = span_of(a, b);
+    if (++b < a.n_seqs) s = span_of<UNIT>(a, b);
   }
 };
 
 // This block's run of units: the cursor at its first unit, and how many there are; total units of the list and units
 // per block. Every thread gets the same; two block barriers.
-__device__ __forceinline__ int locate(const kie_paged_attention_args &a, Cursor *c, long long *total, long long *per_block) {
+template <int UNIT>
+__device__ __forceinline__ int locate(const kie_paged_attention_args &a, Cursor<UNIT> *c, long long *total, long long *per_block) {
   __shared__ long long s_warp[PA_WARPS];
   __shared__ int s_b;
   __shared__ long long s_off;
@@ -146,7 +178,7 @@ __device__ __forceinline__ int locate(const kie_paged_attention_args &a, Cursor 
   const int per = (a.n_seqs + PA_THREADS - 1) / PA_THREADS;
   const int b0 = min(tid * per, a.n_seqs), b1 = min(b0 + per, a.n_seqs);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += span_of(a, b).n;
+  for (int b = b0; b < b1; ++b) mine += span_of<UNIT>(a, b).n;
   long long up = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -171,7 +203,7 @@ __device__ __forceinline__ int locate(const kie_paged_attention_args &a, Cursor 
     long long at = before;
     int b = b0;
     for (;; ++b) {
-      const long long n = (long long)span_of(a, b).n * heads;
+      const long long n = (long long)span_of<UNIT>(a, b).n * heads;
       if (u0 < at + n) break;
       at += n;
     }
@@ -181,7 +213,7 @@ __device__ __forceinline__ int locate(const kie_paged_attention_args &a, Cursor 
   __syncthreads();
   if (u0 >= all) return 0;
   c->b = s_b;
-  c->s = span_of(a, s_b);
+  c->s = span_of<UNIT>(a, s_b);
   c->h = (int)(s_off / c->s.n);
   c->unit = (int)(s_off % c->s.n);
   return (int)min(*per_block, all - u0);
@@ -202,320 +234,360 @@ __device__ __forceinline__ float *pa_piece(const kie_paged_attention_args &a, in
 
 // ---- the kernel ---------------------------------------------------------------------------------------------
 
+// Two consecutive elements at p + i as fp32; pair: p + i is aligned for one access.
+__device__ __forceinline__ float2 load_pair(const void *p, int64_t i, int dtype, bool pair) {
+  if (!pair) return make_float2(paged_load(p, i, dtype), paged_load(p, i + 1, dtype));
+  if (dtype == KIE_F32) return *reinterpret_cast<const float2 *>(static_cast<const float *>(p) + i);
+  const uint32_t w = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + i);
+  if (dtype == KIE_F16) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// Where column d of a warp's output row r lies in the joining area: the accumulators' four column pairs of a lane
+// quad go to different banks.
+template <int KIND>
+__device__ __forceinline__ int join_col(int r, int d) {
+  return d ^ (((r >> 1) & 3) << (KIND == PG_E4M3 ? 4 : 3));
+}
+
 template <int KIND, int DH, bool SPLIT>
 __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS_PER_SM) paged_attn_kernel(const kie_paged_attention_args a) {
+  using T = PaTile<KIND, DH>;
   using Sm = PaSmem<KIND, DH>;
-  constexpr int NS = Sm::NS, ES = KIND == PG_E4M3 ? 1 : 2;
-  constexpr int CH = DH * ES / 16;        // 16-byte chunks of a row
-  constexpr int LOADS = PA_TILE * CH / 32;  // chunks each lane copies of a half
-  constexpr int KSTEPS = DH / 16, NT = DH / 8, EC = 16 / ES;  // EC: elements of a chunk
-  extern __shared__ __align__(128) uint8_t pa_raw[];
+  constexpr int NS = T::NS, CH = T::CH, ROW = T::ROW, ES = T::ES, SUBS = T::SUBS, LOADS = T::LOADS;
+  constexpr int KSTEPS = DH / 16, MT = DH / 16;
+  constexpr uint32_t FULL = SUBS == 2 ? 0xffffffffu : 0xffffu;
+  static_assert(T::HALF >= PA_ROWS * DH * 4, "the joining area is one slot");
+  extern __shared__ __align__(1024) uint8_t pa_raw[];
   Sm &sm = *reinterpret_cast<Sm *>(pa_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int group = a.n_heads / a.pages.n_kv_heads;
-  const int tiles_per_page = a.pages.block_size / PA_TILE;
+  const unsigned bs = a.pages.block_size;
+  const int bs_shift = (bs & (bs - 1)) ? -1 : __ffs(bs) - 1;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Cursor c;
+  Cursor<T::UNIT> c;
   long long total, per_block;
   const int n_units = locate(a, &c, &total, &per_block);
   if (threadIdx.x == 0) reinterpret_cast<int2 *>(a.workspace)[blockIdx.x] = make_int2(-1, -1);
   if (n_units == 0) return;
 
-  // chunk swizzles: K rows g and g + 1 of a tile are read together (chunks t + 4i), V rows 2t of one chunk pair
-  const auto k_chunk = [](int row, int ch) { return CH >= 8 ? ch ^ ((row & 1) << 2) : ch; };
-  const auto v_chunk = [](int row, int ch) { return CH >= 8 ? ch ^ (((row >> 1) & 3) << 1) : ch ^ (((row >> 1) & 1) << 1); };
+  // Chunk ch of row r of a half lies at chunk ch ^ swz(r): the eight rows of an 8 x 8 matrix fall in different banks.
+  const auto swz = [](int row) { return CH >= 8 ? row & 7 : (row >> 1) & 3; };
 
-  // ---- producer side: the warp's tile of unit `p`, K half first, then V
-  Cursor p = c;
+  // ---- producer side: the warp's tile of unit `p`, K half first, then V. A lane copies chunks lane + 32 i.
+  Cursor<T::UNIT> p = c;
   int p_index = 0;  // unit of the run that p stands at
-  int64_t p_page = -1;
-  auto fetch_page = [&]() {  // the page id of p's tile, requested one unit before it is used
-    const int tile = p.s.tile0 + p.unit * PA_WARPS + warp;
-    p_page = -1;
-    if (p_index < n_units && tile * PA_TILE < p.s.len) p_page = a.block_table[p.b * a.table_stride + tile / tiles_per_page];
-  };
   uint32_t p_live = 0;
-  auto issue = [&](int slot, bool is_v) {
-    if (!is_v) {
-      p_live = 0;
-      if (p_page >= 0 && p_page < a.pages.n_blocks) {
-        const int pos = (p.s.tile0 + p.unit * PA_WARPS + warp) * PA_TILE;
-        const int hi = min(PA_TILE, p.s.len - pos), lo = max(0, p.s.lo - pos);
-        p_live = ((1u << hi) - 1u) & ~((1u << lo) - 1u);
+  int p_page[SUBS];
+  const int row0 = lane / CH;  // row of the lane's first chunk; the next are 32 / CH rows on
+  const uint32_t dst_lane = (lane * 16) ^ (swz(row0) << 4);
+  const int64_t k_lane = (row0 * a.pages.k_stride[2]) * ES + (lane % CH) * 16, k_step = a.pages.k_stride[2] * ES * (32 / CH);
+  const int64_t v_lane = (row0 * a.pages.v_stride[2]) * ES + (lane % CH) * 16, v_step = a.pages.v_stride[2] * ES * (32 / CH);
+  const uint32_t ring0 = smem_u32(sm.ring[warp]);
+  auto first_pos = [&](const Cursor<T::UNIT> &x) { return x.s.from + (x.unit * PA_WARPS + warp) * T::POS; };
+  auto fetch_page = [&]() {  // the page ids of p's tile, requested one unit before they are used
+    const int pos = first_pos(p);
+#pragma unroll
+    for (int i = 0; i < SUBS; ++i) {
+      p_page[i] = -1;
+      if (p_index < n_units && pos + 16 * i < p.s.len) {
+        const unsigned at = pos + 16 * i;
+        p_page[i] = a.block_table[p.b * a.table_stride + (bs_shift >= 0 ? at >> bs_shift : at / bs)];
       }
-      if (lane == 0) sm.live[warp][p_index % (NS / 2)] = p_live;
+    }
+  };
+  auto issue = [&](int slot, bool is_v) {
+    const int pos = first_pos(p);
+    if (!is_v) {
+      const int hi = p.s.len - pos, lo = p.s.lo - pos;
+      p_live = hi >= T::POS ? FULL : hi > 0 ? (1u << hi) - 1u : 0u;
+      if (lo > 0) p_live &= lo >= 32 ? 0u : ~((1u << lo) - 1u);
+#pragma unroll
+      for (int i = 0; i < SUBS; ++i)
+        if ((unsigned)p_page[i] >= (unsigned)a.pages.n_blocks) p_live &= ~(0xffffu << (16 * i));
+      if (lane == 0) sm.live[warp][slot] = p_live;
     }
     if (p_live) {
-      const int r0 = (p.s.tile0 + p.unit * PA_WARPS + warp) % tiles_per_page * PA_TILE;
       const int64_t *st = is_v ? a.pages.v_stride : a.pages.k_stride;
-      const uint8_t *src = static_cast<const uint8_t *>(is_v ? a.pages.v : a.pages.k) +
-                           (p_page * st[0] + p.h * st[1] + r0 * st[2]) * ES;
-      uint8_t *dst = sm.ring[warp][slot];
+      const int64_t step = is_v ? v_step : k_step;
+      const uint32_t dst = ring0 + slot * T::HALF + dst_lane;
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        const int row = (lane + 32 * i) / CH, ch = (lane + 32 * i) % CH;
-        const int to = is_v ? v_chunk(row, ch) : k_chunk(row, ch);
-        cp_async16(dst + (row * CH + to) * 16, src + (int64_t)row * st[2] * ES + ch * 16, (p_live >> row) & 1u);
+      for (int s = 0; s < SUBS; ++s) {
+        const unsigned at = pos + 16 * s, off = bs_shift >= 0 ? at & (bs - 1) : at % bs;
+        const uint32_t live = (p_live >> (16 * s)) & 0xffffu;
+        const int64_t page = live ? p_page[s] : 0;  // an address inside the pages even where nothing is read
+        const uint8_t *src = static_cast<const uint8_t *>(is_v ? a.pages.v : a.pages.k) +
+                             (page * st[0] + p.h * st[1] + off * st[2]) * ES + (is_v ? v_lane : k_lane);
+        constexpr int N = LOADS / SUBS;
+        if (live == 0xffffu) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            cp_async16((dst ^ (swz((i + s * N) * (32 / CH)) << 4)) + (i + s * N) * 512, src);
+            src += step;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            cp_async16((dst ^ (swz((i + s * N) * (32 / CH)) << 4)) + (i + s * N) * 512, src,
+                       (p_live >> (row0 + (i + s * N) * (32 / CH))) & 1u);
+            src += step;
+          }
+        }
       }
-      if (KIND == PG_E4M3 && lane < PA_TILE) {
+      if (KIND == PG_E4M3) {  // a row's scale to each lane
         const int64_t *ss = is_v ? a.pages.v_scale_stride : a.pages.k_scale_stride;
-        cp_async4(&sm.scale[warp][slot][lane],
-                  (is_v ? a.pages.v_scale : a.pages.k_scale) + p_page * ss[0] + p.h * ss[1] + (r0 + lane) * ss[2],
-                  (p_live >> lane) & 1u);
+        const unsigned at = pos + lane, off = bs_shift >= 0 ? at & (bs - 1) : at % bs;
+        const bool live = (p_live >> lane) & 1u;
+        const int64_t page = live ? (lane < 16 ? p_page[0] : p_page[SUBS - 1]) : 0;
+        cp_async4(&sm.scale[warp][KIND == PG_E4M3 ? slot : 0][lane],
+                  (is_v ? a.pages.v_scale : a.pages.k_scale) + page * ss[0] + p.h * ss[1] + off * ss[2],
+                  live);
       }
     }
     if (is_v) {
-      if (++p_index < n_units) p.next(a);
+      if (++p_index < n_units) {
+        p.next(a);
+        if (p.unit == 0 && warp == 0) {  // a new item: its queries towards L2, a line to a lane
+          const int bytes = DH * paged_dtype_bytes(a.q_dtype), at = lane * 128;
+          const int r = at / bytes;
+          if (r < group)
+            prefetch_l2(static_cast<const uint8_t *>(a.q) +
+                        (p.b * a.q_stride[0] + (int64_t)(p.h * group + r) * a.q_stride[1]) * paged_dtype_bytes(a.q_dtype) +
+                        at % bytes);
+        }
+      }
       fetch_page();
     }
   };
 
   fetch_page();
+#pragma unroll
   for (int x = 0; x < NS - 1; ++x) {
     issue(x, x & 1);
     cp_commit();
   }
 
-  uint32_t qa[KSTEPS][SPLIT ? 4 : 2];
-  float row_scale = 0.f;
-  float o[NT][4], m = -INFINITY, l = 0.f, mw = -INFINITY;  // mw: the weights' reference (E4M3: of p * v_scale)
+  // ---- consumer side. Lane (g, t) holds, of the accumulators, heads 2t and 2t + 1; of the B operands, head g.
+  const uint32_t k_at = ((lane & 15) * ROW) + (((lane >> 4) ^ swz(lane & 7)) << 4);  // ldmatrix row of the lane
+  const uint32_t v_at = ((((lane >> 4) << 3) + (lane & 7)) * ROW) + ((((lane >> 3) & 1) ^ swz(lane & 7)) << 4);
+  uint32_t qb[KSTEPS][SPLIT ? 4 : 2];
+  float rs[2], m[2], bias[2], l[2], o[MT][4];  // rs: score scale in log2 units; bias: P_BIAS - m
   bool first = true;
-  int ring = 0;  // slot of the next half
   bool starts = c.unit == 0;  // this block holds the item's first unit
+  int ring = 0;               // slot of the next half
 
   for (int u = 0; u < n_units; ++u) {
-    if (first) {  // a new item: its query heads as A fragments, row g of the group
+    if (first) {  // a new item: its query heads as B fragments
       first = false;
-      const bool vec = ((uintptr_t)a.q | (uintptr_t)(a.q_stride[0] * paged_dtype_bytes(a.q_dtype)) |
-                        (uintptr_t)(a.q_stride[1] * paged_dtype_bytes(a.q_dtype))) % 16 == 0;
+      const int qs = paged_dtype_bytes(a.q_dtype);
+      const bool pair = ((uintptr_t)a.q | (uintptr_t)(a.q_stride[0] * qs) | (uintptr_t)(a.q_stride[1] * qs)) % (2 * qs) == 0;
       const int64_t at = c.b * a.q_stride[0] + (int64_t)(c.h * group + g) * a.q_stride[1];
-      float f[DH / 4];
+      float2 f[KSTEPS][2];
 #pragma unroll
-      for (int i = 0; i < DH / 32; ++i) {
-        // 8 consecutive dimensions a time, in the order of the K chunks that meet them
-        const int d = EC == 8 ? 8 * (t + 4 * i) : 16 * (t + 4 * (i >> 1)) + 8 * (i & 1);
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (g < group) {
-          if (vec)
-            load8<true>(a.q, at + d, a.q_dtype, v);
-          else
-            load8<false>(a.q, at + d, a.q_dtype, v);
+      for (int st = 0; st < KSTEPS; ++st)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // E4M3 rows come as four codes to a lane, so that the k order of a step is 4t .. 4t + 3
+          const int d = 16 * st + (KIND == PG_E4M3 ? 4 * t + 2 * e : 2 * t + 8 * e);
+          f[st][e] = g < group ? load_pair(a.q, at + d, a.q_dtype, pair) : make_float2(0.f, 0.f);
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[8 * i + e] = v[e];
-      }
-      row_scale = a.scale * LOG2E;
-      if (SPLIT) {  // bring the row's largest element to [2^13, 2^14) by a power of two
+      float down = 1.f;
+      if (SPLIT) {  // bring the head's largest element to [2^13, 2^14) by a power of two
         float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < DH / 4; ++i) top = fmaxf(top, fabsf(f[i]));
+        for (int st = 0; st < KSTEPS; ++st)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) top = fmaxf(top, fmaxf(fabsf(f[st][e].x), fabsf(f[st][e].y)));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        int e = 0;
-        if (top > 0.f && top <= FLT_MAX) e = max(-120, min(120, 13 - ilogbf(top)));
-        const float up = __int_as_float((127 + e) << 23);
-        row_scale *= __int_as_float((127 - e) << 23);
+        int e2 = 0;
+        if (top > 0.f && top <= FLT_MAX) e2 = max(-120, min(120, 140 - (int)(__float_as_uint(top) >> 23)));
+        const float up = __int_as_float((127 + e2) << 23);
+        down = __int_as_float((127 - e2) << 23);
 #pragma unroll
-        for (int i = 0; i < DH / 4; ++i) f[i] *= up;
+        for (int st = 0; st < KSTEPS; ++st)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) f[st][e].x *= up, f[st][e].y *= up;
       }
 #pragma unroll
-      for (int s = 0; s < KSTEPS; ++s) {
-        qa[s][0] = pack16<KIND>(f[4 * s], f[4 * s + 1]);
-        qa[s][1] = pack16<KIND>(f[4 * s + 2], f[4 * s + 3]);
-        if (SPLIT) {
-          qa[s][SPLIT ? 2 : 0] = rest16<KIND>(f[4 * s], f[4 * s + 1], qa[s][0]);
-          qa[s][SPLIT ? 3 : 0] = rest16<KIND>(f[4 * s + 2], f[4 * s + 3], qa[s][1]);
+      for (int st = 0; st < KSTEPS; ++st)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          qb[st][e] = pack16<KIND>(f[st][e].x, f[st][e].y);
+          if (SPLIT) qb[st][SPLIT ? 2 + e : e] = rest16<KIND>(f[st][e].x, f[st][e].y, qb[st][e]);
         }
-      }
-      m = mw = -INFINITY;
-      l = 0.f;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+      for (int h = 0; h < 2; ++h) {
+        rs[h] = a.scale * LOG2E;
+        if (SPLIT) rs[h] *= __shfl_sync(0xffffffffu, down, 8 * t + 4 * h);  // of head 2t + h
+        m[h] = -INFINITY;
+        bias[h] = P_BIAS;
+        l[h] = 0.f;
+      }
+#pragma unroll
+      for (int n = 0; n < MT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     }
 
-    // ---- K half: scores of the tile's 16 positions
+    // ---- K half: scores of the tile, s[.][2p + h] of position g + 8p and head 2t + h
     cp_wait<NS - 2>();
     __syncwarp();
-    issue((ring + NS - 1) % NS, true);
+    issue(ring == 0 ? NS - 1 : ring - 1, (NS - 1) & 1);
     cp_commit();
-    const uint32_t live = sm.live[warp][u % (NS / 2)];
-    uint32_t pa[4];
+    const uint32_t live = sm.live[warp][ring];
+    float s[SUBS][4];
     if (live) {
-      float s[2][4] = {};
-      const uint8_t *kt = sm.ring[warp][ring];
+      const uint32_t kt = ring0 + ring * T::HALF + k_at;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = 8 * j + g;
+      for (int i = 0; i < SUBS; ++i) {
+        float x[2][4] = {};
+        if (KIND != PG_E4M3) {
 #pragma unroll
-        for (int i = 0; i < CH / 4; ++i) {
-          const uint4 w = *reinterpret_cast<const uint4 *>(kt + (row * CH + k_chunk(row, t + 4 * i)) * 16);
-          const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+          for (int st = 0; st < KSTEPS; ++st) {
+            uint32_t A[4];
+            ldsm4(A, kt ^ (st << 5));
+            mma16<KIND>(x[SPLIT ? 0 : st & 1], A, qb[st][0], qb[st][1]);
+            if (SPLIT) mma16<KIND>(x[1], A, qb[st][SPLIT ? 2 : 0], qb[st][SPLIT ? 3 : 0]);
+          }
+        } else {
 #pragma unroll
-          for (int e = 0; e < EC / 4; ++e) {  // four dimensions of this lane to a step
-            const int st = i * (EC / 4) + e;
-            const uint32_t b0 = KIND == PG_E4M3 ? e4m3x2(r[e & 3] & 0xffffu) : r[(2 * e) & 3];
-            const uint32_t b1 = KIND == PG_E4M3 ? e4m3x2(r[e & 3] >> 16) : r[(2 * e + 1) & 3];
-            const uint32_t A[4] = {qa[st][0], SPLIT ? qa[st][SPLIT ? 2 : 0] : 0u, qa[st][1], SPLIT ? qa[st][SPLIT ? 3 : 0] : 0u};
-            mma16<KIND>(s[j], A, b0, b1);
+          for (int st = 0; st < KSTEPS; st += 2) {
+            uint32_t r[4];
+            ldsm4(r, (kt ^ (st << 4)) + i * 16 * ROW);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t A[4] = {e4m3x2(r[2 * k] & 0xffffu), e4m3x2(r[2 * k + 1] & 0xffffu), e4m3x2(r[2 * k] >> 16),
+                                     e4m3x2(r[2 * k + 1] >> 16)};
+              mma16<KIND>(x[0], A, qb[st + k][0], qb[st + k][1]);
+              mma16<KIND>(x[1], A, qb[st + k][SPLIT ? 2 : 0], qb[st + k][SPLIT ? 3 : 0]);
+            }
           }
         }
-      }
-      // scores in log2 units, row g, positions 8j + 2t, 8j + 2t + 1
-      float v[4], w[4];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float2 ks = make_float2(1.f, 1.f);
-        if (KIND == PG_E4M3) ks = *reinterpret_cast<const float2 *>(&sm.scale[warp][KIND == PG_E4M3 ? ring : 0][8 * j + 2 * t]);
-        v[2 * j] = (SPLIT ? s[j][0] + s[j][2] : s[j][0]) * row_scale * ks.x;
-        v[2 * j + 1] = (SPLIT ? s[j][1] + s[j][3] : s[j][1]) * row_scale * ks.y;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (!((live >> (8 * j + 2 * t + e)) & 1u)) v[2 * j + e] = -INFINITY;
-      }
-      float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
-      float sum = 0.f;
-      if (KIND != PG_E4M3) {
-        const float bias = KIND == PG_F16 ? P_BIAS : 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[e] = ex2(v[e] - ref + bias);
-          sum += w[e];
+        float ks[2] = {1.f, 1.f};
+        if (KIND == PG_E4M3) {
+          ks[0] = sm.scale[warp][KIND == PG_E4M3 ? ring : 0][16 * i + g];
+          ks[1] = sm.scale[warp][KIND == PG_E4M3 ? ring : 0][16 * i + g + 8];
         }
-        const float corr = m == mn ? 1.f : ex2(m - ref);
-        l = fmaf(l, corr, sum);
-        if (__any_sync(0xffffffffu, corr != 1.f)) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][e] *= corr;
-        }
-        m = mn;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum += ex2(v[e] - ref);
-        l = fmaf(l, m == mn ? 1.f : ex2(m - ref), sum);
-        m = mn;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = v[e];
-      }
-      if (KIND != PG_E4M3) {
-        pa[0] = pack16<KIND>(w[0], w[1]);
-        pa[2] = pack16<KIND>(w[2], w[3]);
-        pa[1] = rest16<KIND>(w[0], w[1], pa[0]);
-        pa[3] = rest16<KIND>(w[2], w[3], pa[2]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) pa[e] = __float_as_uint(w[e]);
+        for (int e = 0; e < 4; ++e) s[i][e] = (x[0][e] + x[1][e]) * ks[e >> 1];
       }
     }
     ring = ring + 1 == NS ? 0 : ring + 1;
 
-    // ---- V half: the outputs
+    // ---- V half: weights and outputs
     cp_wait<NS - 2>();
     __syncwarp();
-    issue((ring + NS - 1) % NS, false);
+    issue(ring == 0 ? NS - 1 : ring - 1, NS & 1);
     cp_commit();
     if (live) {
-      if (KIND == PG_E4M3) {
-        // The weight of a row's codes is p times its scale mant * 2^e: a second running maximum, of log2 p + e, keeps it
-        // in fp16's range whatever the size of the scales.
-        float v[4], w[4], mant[4];
+      float vs[SUBS][2], w[SUBS][4], part[2] = {0.f, 0.f};
+      bool far = m[0] == -INFINITY || m[1] == -INFINITY;
+      auto weights = [&]() {
+        part[0] = part[1] = 0.f;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float2 vs = *reinterpret_cast<const float2 *>(&sm.scale[warp][KIND == PG_E4M3 ? ring : 0][8 * j + 2 * t]);
+        for (int i = 0; i < SUBS; ++i)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float ex;
-            split_exponent(e ? vs.y : vs.x, &mant[2 * j + e], &ex);
-            v[2 * j + e] = __uint_as_float(pa[2 * j + e]) + ex;  // -inf where masked
+          for (int e = 0; e < 4; ++e) {
+            float x = fmaf(s[i][e], rs[e & 1], bias[e & 1]);
+            if (live != FULL && !((live >> (16 * i + g + 8 * (e >> 1))) & 1u)) x = -INFINITY;
+            const float y = ex2(x);
+            part[e & 1] += y;
+            w[i][e] = KIND == PG_E4M3 ? y * vs[i][e >> 1] : y;
           }
+      };
+#pragma unroll
+      for (int i = 0; i < SUBS; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          vs[i][k] = KIND == PG_E4M3 ? sm.scale[warp][KIND == PG_E4M3 ? ring : 0][16 * i + g + 8 * k] : 1.f;
+      weights();
+#pragma unroll
+      for (int i = 0; i < SUBS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) far = far || fabsf(w[i][e]) > P_LIMIT;
+      if (__any_sync(0xffffffffu, far)) {  // move the references to the maxima so far
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < SUBS; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if ((live >> (16 * i + g + 8 * (e >> 1))) & 1u)
+              top[e & 1] = fmaxf(top[e & 1], fmaf(s[i][e], rs[e & 1],
+                                                  KIND == PG_E4M3 ? fmaxf(lg2(fabsf(vs[i][e >> 1])), MIN_LOG2_SCALE) : 0.f));
+        float f[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], x));
+          const float mn = fmaxf(m[h], top[h]);
+          f[h] = m[h] == mn ? 1.f : ex2(m[h] - mn);
+          m[h] = mn;
+          bias[h] = P_BIAS - (mn == -INFINITY ? 0.f : mn);
+          l[h] *= f[h];
         }
-        float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float mn = fmaxf(mw, top), ref = mn == -INFINITY ? 0.f : mn;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = ex2(v[e] - ref + P_BIAS) * mant[e];
-        const float corr = mw == mn ? 1.f : ex2(mw - ref);
-        if (__any_sync(0xffffffffu, corr != 1.f)) {
+        for (int n = 0; n < MT; ++n)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][e] *= corr;
-        }
-        mw = mn;
-        pa[0] = pack16<KIND>(w[0], w[1]);
-        pa[2] = pack16<KIND>(w[2], w[3]);
-        pa[1] = rest16<KIND>(w[0], w[1], pa[0]);
-        pa[3] = rest16<KIND>(w[2], w[3], pa[2]);
+          for (int e = 0; e < 4; ++e) o[n][e] *= f[e & 1];
+        weights();
       }
-      const uint8_t *vt = sm.ring[warp][ring];
+      l[0] += part[0];
+      l[1] += part[1];
+      const uint32_t vt = ring0 + ring * T::HALF + v_at;
 #pragma unroll
-      for (int i = 0; i < DH / 64; ++i) {
-        uint32_t b[2][8];
+      for (int i = 0; i < SUBS; ++i) {
+        const uint32_t h0 = pack16<KIND>(w[i][0], w[i][1]), h1 = pack16<KIND>(w[i][2], w[i][3]);
+        const uint32_t r0 = rest16<KIND>(w[i][0], w[i][1], h0), r1 = rest16<KIND>(w[i][2], w[i][3], h1);
+        const uint32_t B[4] = {transpose8(h0), transpose8(h1), transpose8(r0), transpose8(r1)};
+        if (KIND != PG_E4M3) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {  // positions 2t + 8k and the next
-          const int row = 2 * t + 8 * k;
-          if (KIND == PG_E4M3) {
-            const int e = g + 8 * i;  // 8 dimensions: half a chunk
-            const uint2 x = *reinterpret_cast<const uint2 *>(vt + (row * CH + v_chunk(row, e >> 1)) * 16 + (e & 1) * 8);
-            const uint2 y = *reinterpret_cast<const uint2 *>(vt + ((row + 1) * CH + v_chunk(row + 1, e >> 1)) * 16 + (e & 1) * 8);
-            const uint32_t X[2] = {x.x, x.y}, Y[2] = {y.x, y.y};
+          for (int n = 0; n < MT; ++n) {
+            uint32_t A[4];
+            ldsm4_trans(A, vt ^ (n << 5));
+            mma16<KIND>(o[n], A, B[0], B[1]);
+            mma16<KIND>(o[n], A, B[2], B[3]);
+          }
+        } else {
+          // a transposed pair of codes: positions 2t, 2t + 1 of dimensions 2g and 2g + 1, rows g and g + 8 of the tile
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              const uint32_t lo = __byte_perm(X[q], Y[q], 0x5140), hi = __byte_perm(X[q], Y[q], 0x7362);
-              b[k][4 * q] = e4m3x2(lo & 0xffffu), b[k][4 * q + 1] = e4m3x2(lo >> 16);
-              b[k][4 * q + 2] = e4m3x2(hi & 0xffffu), b[k][4 * q + 3] = e4m3x2(hi >> 16);
-            }
-          } else {
-            const uint4 x = *reinterpret_cast<const uint4 *>(vt + (row * CH + v_chunk(row, g + 8 * i)) * 16);
-            const uint4 y = *reinterpret_cast<const uint4 *>(vt + ((row + 1) * CH + v_chunk(row + 1, g + 8 * i)) * 16);
-            const uint32_t X[4] = {x.x, x.y, x.z, x.w}, Y[4] = {y.x, y.y, y.z, y.w};
+          for (int n = 0; n < MT; n += 2) {
+            uint32_t r[4];
+            ldsm4_trans(r, (vt ^ (n << 4)) + i * 16 * ROW);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              b[k][2 * q] = __byte_perm(X[q], Y[q], 0x5410);
-              b[k][2 * q + 1] = __byte_perm(X[q], Y[q], 0x7632);
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t x = __byte_perm(r[k], 0u, 0x3120), y = __byte_perm(r[2 + k], 0u, 0x3120);
+              const uint32_t A[4] = {e4m3x2(x & 0xffffu), e4m3x2(x >> 16), e4m3x2(y & 0xffffu), e4m3x2(y >> 16)};
+              mma16<KIND>(o[n + k], A, B[0], B[1]);
+              mma16<KIND>(o[n + k], A, B[2], B[3]);
             }
           }
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) mma16<KIND>(o[8 * i + j], pa, b[0][j], b[1][j]);
       }
     }
-    ring = ring + 1 == NS ? 0 : ring + 1;
 
-    // ---- the item's end, or the run's: join the four warps
+    // ---- the item's end, or the run's: join the four warps through the slot just used
     const bool ends = c.unit + 1 == c.s.n;
     if (ends || u + 1 == n_units) {
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      float back = 1.f;  // brings o to the reference of l
-      if (KIND == PG_E4M3) back = mw == -INFINITY ? 0.f : ex2(mw - P_BIAS - (m == -INFINITY ? 0.f : m));
-      if (g < group) {
-        if (t == 0) {
-          sm.m[warp][g] = KIND == PG_F16 ? m - P_BIAS : m;
-          sm.l[warp][g] = l;
+      __syncwarp();  // every lane is done with the slot
+      float *join = reinterpret_cast<float *>(sm.ring[warp][ring]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
+        const int r = 2 * t + h;
+        if (g == 0) {
+          sm.m[warp][r] = m[h] - P_BIAS;
+          sm.l[warp][r] = l[h];
         }
-        // a lane holds 16 consecutive dimensions of row g to every 64
 #pragma unroll
-        for (int i = 0; i < DH / 64; ++i)
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              float4 x;
-              float *xs = &x.x;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int n = 8 * i + 4 * q + e;
-                xs[e] = (o[n][half] + o[n][half + 2]) * back;
-              }
-              *reinterpret_cast<float4 *>(&sm.o[warp][g][16 * (t + 4 * i) + 8 * half + 4 * q]) = x;
-            }
+        for (int n = 0; n < MT; ++n) {
+          if (KIND == PG_E4M3) {
+            *reinterpret_cast<float2 *>(&join[r * DH + join_col<KIND>(r, 16 * n + 2 * g)]) = make_float2(o[n][h], o[n][2 + h]);
+          } else {
+            join[r * DH + join_col<KIND>(r, 16 * n + g)] = o[n][h];
+            join[r * DH + join_col<KIND>(r, 16 * n + g + 8)] = o[n][2 + h];
+          }
+        }
       }
       __syncthreads();
       const bool whole = ends && starts;
@@ -530,13 +602,13 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS_PER_SM) paged_attn_kerne
 #pragma unroll
         for (int w = 0; w < PA_WARPS; ++w) {
           const float f = ex2(sm.m[w][r] - ref);
-          const float4 y = *reinterpret_cast<const float4 *>(&sm.o[w][r][d]);
+          const float4 y = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm.ring[w][ring]) + r * DH +
+                                                             join_col<KIND>(r, d));
           L = fmaf(sm.l[w][r], f, L);
           acc.x = fmaf(y.x, f, acc.x), acc.y = fmaf(y.y, f, acc.y), acc.z = fmaf(y.z, f, acc.z), acc.w = fmaf(y.w, f, acc.w);
         }
         if (whole) {
-          const int64_t head = (int64_t)c.h * group + r;
-          paged_finish4(a, c.b, head, d, acc, M, L);
+          paged_finish4(a, c.b, (int64_t)c.h * group + r, d, acc, M, L);
         } else {
           *reinterpret_cast<float4 *>(piece + r * DH + d) = acc;
           if (d == 0) {
@@ -550,10 +622,11 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS_PER_SM) paged_attn_kerne
         reinterpret_cast<int2 *>(a.workspace)[blockIdx.x] =
             make_int2(c.b * a.pages.n_kv_heads + c.h, (int)(last / per_block));
       }
-      __syncthreads();
+      __syncthreads();  // the next half may land in the slot, and the next item's sums in theirs
       first = true;
       starts = true;
     }
+    ring = ring + 1 == NS ? 0 : ring + 1;
     if (u + 1 < n_units) c.next(a);
   }
   cp_wait<0>();

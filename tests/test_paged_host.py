@@ -113,7 +113,7 @@ def attention_args(dtype=0):
 
 @pytest.mark.parametrize("change,word", [
     (dict(n_seqs=-1), "n_seqs"), (dict(window=-1), "window"), (dict(max_blocks=0), "max_blocks"),
-    (dict(max_blocks=1 << 27), "2^31"), (dict(n_heads=3), "multiple"), (dict(n_heads=18), "more than 8"),
+    (dict(max_blocks=1 << 27), "2^30"), (dict(n_heads=3), "multiple"), (dict(n_heads=18), "more than 8"),
     (dict(q_dtype=3), "KIE_F32"), (dict(q_dtype=1), "F16 pages"), (dict(scale=float("nan")), "finite"),
     (dict(scale=float("inf")), "finite"), (dict(q=None), "NULL"), (dict(lens=None), "NULL"),
     (dict(table_stride=3), "table_stride"), (dict(n_seqs=1 << 30), "2^31")])

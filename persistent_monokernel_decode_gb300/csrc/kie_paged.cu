@@ -2,6 +2,7 @@
 // points with their argument checks (kie_paged_attn.cu holds the attention).
 #include <limits.h>
 #include <stdio.h>
+#include <stdlib.h>
 
 #include <algorithm>
 
@@ -280,6 +281,7 @@ const char *check_pages(const kie_pages &p) {
   const int unit = 16 / paged_dtype_bytes(p.dtype);
   for (int i = 0; i < 3; ++i)
     if (p.k_stride[i] % unit || p.v_stride[i] % unit) return "the pages' strides must be multiples of 16 bytes";
+  if (llabs(p.k_stride[2]) >= 1 << 26 || llabs(p.v_stride[2]) >= 1 << 26) return "the strides of positions must be below 2^26";
   if (p.dtype == KIE_E4M3 && (!p.k_scale || !p.v_scale)) return "E4M3 pages need k_scale and v_scale";
   if (p.dtype == KIE_E4M3 && (!aligned(p.k_scale, 4) || !aligned(p.v_scale, 4))) return "scales must be 4-byte aligned";
   return nullptr;
@@ -410,5 +412,5 @@ int kie_paged_attention(const kie_paged_attention_args *p, void *stream) {
   const size_t need = kie_paged_attention_workspace_bytes(a.n_heads, a.pages.n_kv_heads, a.pages.head_dim, sms);
   if (!a.workspace || a.workspace_bytes < need || !aligned(a.workspace, 256))
     return refuse("the workspace is NULL, unaligned (256 bytes) or smaller than kie_paged_attention_workspace");
-  return finish(kie_launch_paged_attention(a, sms, (cudaStream_t)stream), "paged_attention");
+  return finish(kie_launch_paged_attention(a, dev, sms, (cudaStream_t)stream), "paged_attention");
 }

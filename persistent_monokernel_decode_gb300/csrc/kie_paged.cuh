@@ -86,21 +86,7 @@ __device__ __forceinline__ void store8(void *p, int64_t i, int dtype, const floa
       make_uint4(pack2(v[0], v[1], dtype), pack2(v[2], v[3], dtype), pack2(v[4], v[5], dtype), pack2(v[6], v[7], dtype));
 }
 
-// Four dimensions d .. d + 3 of a query head's output from its weighted sum, and its lse from the reference M (log2
-// units) and the sum of weights L: zeros and -inf where nothing was attended.
-__device__ __forceinline__ void paged_finish4(const kie_paged_attention_args &a, int b, int64_t head, int d, float4 acc,
-                                              float M, float L) {
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  const int64_t to = b * a.out_stride[0] + head * a.out_stride[1] + d;
-  paged_store(a.out, to, a.q_dtype, acc.x * inv);
-  paged_store(a.out, to + 1, a.q_dtype, acc.y * inv);
-  paged_store(a.out, to + 2, a.q_dtype, acc.z * inv);
-  paged_store(a.out, to + 3, a.q_dtype, acc.w * inv);
-  if (d == 0 && a.lse)
-    a.lse[(int64_t)b * a.n_heads + head] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-}
-
 }  // namespace kie
 
-cudaError_t kie_launch_paged_attention(const kie_paged_attention_args &a, int sms, cudaStream_t stream);
+cudaError_t kie_launch_paged_attention(const kie_paged_attention_args &a, int dev, int sms, cudaStream_t stream);
 size_t kie_paged_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim, int sms);

@@ -1,9 +1,11 @@
 // Attention of one new token per sequence over a paged K/V cache, split over the cache's length and joined.
 //
-// The work is a list of items (sequence, KV head), each a row of units of 64 positions. Every block of the grid takes
-// an equal run of consecutive units, whatever items they belong to, so a ragged batch and a single long sequence load
+// The work is a list of items (sequence, KV head), each a row of units of 64 (E4M3: 128) positions. Every block of the
+// grid takes an equal run of the list, whatever items it belongs to, so a ragged batch and a single long sequence load
 // the GPU alike; a block keeps the whole items of its run to itself and publishes the pieces of the (at most two)
-// items that it shares with its neighbours, which a second kernel joins.
+// items that it shares with its neighbours. The last block to publish a piece of an item joins them all (in two levels
+// where they are many), in the order of the pieces: no block waits for another, and the result does not depend on
+// which one is last.
 //
 // Inside a block each of four warps takes a quarter of a unit, one tile. Both products run as mma.sync m16n8k16 in the
 // transposed form, so that no row of an instruction is wasted on the at most 8 query heads of a KV head: S^T = K Q^T
@@ -16,6 +18,8 @@
 // fit in fp16, so it is only moved (with the shuffles and the rescaling that this costs) when a weight passes that.
 #include <float.h>
 
+#include <atomic>
+
 #include "kie_device.cuh"
 #include "kie_paged.cuh"
 
@@ -24,10 +28,10 @@ namespace {
 
 constexpr int PA_WARPS = 4;
 constexpr int PA_THREADS = PA_WARPS * 32;
-constexpr int PA_BLOCKS_PER_SM = 3;
+constexpr int PA_BLOCKS_PER_SM = 2;
+constexpr int PA_RING_BYTES = 24 * 1024;    // a warp's ring: 4 warps x 2 blocks x 24 KB = 192 KB of an SM
 constexpr int PA_ROWS = PAGED_MAX_GROUP;
-constexpr int PA_RING_BYTES = 16 * 1024;    // a warp's ring: 4 warps x 3 blocks x 16 KB = 192 KB of an SM
-constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // Weights are kept as 2^7 2^(v - ref): an fp16 pair holds them to 2^-25, which is 2^-32 of the largest.
 constexpr float P_BIAS = 7.f, P_LIMIT = 32768.f;
 // Scales of E4M3 value rows count into the reference down to this (log2), so that the plain weights stay finite.
@@ -52,7 +56,7 @@ struct PaSmem {
   using T = PaTile<KIND, DH>;
   uint8_t ring[PA_WARPS][T::NS][T::HALF];
   float scale[PA_WARPS][KIND == PG_E4M3 ? T::NS : 1][32];
-  float m[PA_WARPS][PA_ROWS], l[PA_WARPS][PA_ROWS];
+  float4 m[PA_ROWS], l[PA_ROWS];  // of a row: the four warps'
   uint32_t live[PA_WARPS][T::NS];
 };
 
@@ -71,11 +75,15 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float lg2(float x) {
@@ -153,37 +161,49 @@ __device__ __forceinline__ Span span_of(const kie_paged_attention_args &a, int b
   return s;
 }
 
-// A place in the list: unit `unit` of item (b, h).
+// Places in the list are numbered through, an item taking PA_ITEM_COST places before those of its units: starting an
+// item (its queries, the join of the warps, the output) takes a block about as long as that many units.
+constexpr int PA_ITEM_COST = 2, PA_MIN_RUN = 4;
+
+// Unit `unit` of item (b, h), at place v of this block's run.
 template <int UNIT>
 struct Cursor {
   Span s;
-  int b, h, unit;
+  int b, h, unit, v;
   __device__ __forceinline__ void next(const kie_paged_attention_args &a) {
+    ++v;
     if (++unit < s.n) return;
     unit = 0;
+    v += PA_ITEM_COST;
     if (++h < a.pages.n_kv_heads) return;
     h = 0;
     if (++b < a.n_seqs) s = span_of<UNIT>(a, b);
   }
 };
 
-// This block's run of units: the cursor at its first unit, and how many there are; total units of the list and units
-// per block. Every thread gets the same; two block barriers.
+// ceil(a / b), with a 32-bit division where it does (a 64-bit one takes a few hundred cycles at the kernel's start).
+__device__ __forceinline__ long long div_up(long long a, unsigned b) {
+  return a < (1ll << 31) ? (long long)(((unsigned)a + b - 1) / b) : (a + b - 1) / b;
+}
+
+// The number of places of this block's run (*end; 0 behind the list's end), the cursor at its first unit, and the
+// places of a full run (*per_block). Every thread gets the same; two block barriers. The cursor may stand at or past
+// *end: no units.
 template <int UNIT>
-__device__ __forceinline__ int locate(const kie_paged_attention_args &a, Cursor<UNIT> *c, long long *total, long long *per_block) {
+__device__ __forceinline__ void locate(const kie_paged_attention_args &a, Cursor<UNIT> *c, int *end, long long *per_block) {
   __shared__ long long s_warp[PA_WARPS];
-  __shared__ int s_b;
-  __shared__ long long s_off;
+  __shared__ int s_b, s_h;
+  __shared__ int s_off;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int per = (a.n_seqs + PA_THREADS - 1) / PA_THREADS;
   const int b0 = min(tid * per, a.n_seqs), b1 = min(b0 + per, a.n_seqs);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += span_of<UNIT>(a, b).n;
+  for (int b = b0; b < b1; ++b) mine += span_of<UNIT>(a, b).n + PA_ITEM_COST;
   long long up = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, up, o);
-    if (lane >= o) up += v;
+    const long long x = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += x;
   }
   if (lane == 31) s_warp[warp] = up;
   __syncthreads();
@@ -196,51 +216,249 @@ __device__ __forceinline__ int locate(const kie_paged_attention_args &a, Cursor<
   const int heads = a.pages.n_kv_heads;
   all *= heads;
   before *= heads;
-  *total = all;
-  *per_block = (all + gridDim.x - 1) / gridDim.x;
-  const long long u0 = blockIdx.x * *per_block;
-  if (u0 >= before && u0 < before + mine * heads) {
+  *per_block = max(div_up(all, gridDim.x), (long long)PA_MIN_RUN);
+  const long long v0 = blockIdx.x * *per_block;
+  *end = (int)max(0ll, min(*per_block, all - v0));
+  if (v0 >= before && v0 < before + mine * heads) {
     long long at = before;
     int b = b0;
     for (;; ++b) {
-      const long long n = (long long)span_of<UNIT>(a, b).n * heads;
-      if (u0 < at + n) break;
+      const long long n = (long long)(span_of<UNIT>(a, b).n + PA_ITEM_COST) * heads;
+      if (v0 < at + n) break;
       at += n;
     }
     s_b = b;
-    s_off = u0 - at;
+    long long off = v0 - at;  // into the sequence's items
+    const int n = span_of<UNIT>(a, b).n + PA_ITEM_COST;
+    int h = 0;
+    for (; off >= n; off -= n) ++h;
+    s_h = h;
+    s_off = (int)off;
   }
   __syncthreads();
-  if (u0 >= all) return 0;
+  c->v = 0;
+  if (v0 >= all) return;
   c->b = s_b;
   c->s = span_of<UNIT>(a, s_b);
-  c->h = (int)(s_off / c->s.n);
-  c->unit = (int)(s_off % c->s.n);
-  return (int)min(*per_block, all - u0);
+  c->h = s_h;
+  c->unit = max(0, s_off - PA_ITEM_COST);
+  c->v = max(0, PA_ITEM_COST - s_off);
 }
 
 // ---- workspace ----------------------------------------------------------------------------------------------
 
-// Per block: a header {first KV item it starts but does not end (or -1), the block that ends it}, and two pieces, [0]
-// of the item that an earlier block started and [1] of the one in the header: o [group][dh], then m and l [group].
-// (rounded to 16 bytes)
+// Per block: three arrival words, then four pieces: o [group][dh], then m and l [group] (rounded to 16 bytes). A block
+// continues at most one item that an earlier block started and starts at most one that it does not end:
+//   word / piece CONT, START: the arrivals of the group of blocks that begins with this one, as a continuation or as
+//   the item's start; this block's piece of either.
+//   word ITEM: arrivals of an item's groups, at the block that starts it; pieces JOINED + CONT / START: a joined group.
+enum { CONT = 0, START = 1, ITEM = 2, JOINED = 2 };
+constexpr int PA_WORDS = 3, PA_PIECES = 4;
+constexpr int PA_ONE_LEVEL = 24;  // up to this many pieces are joined at once, more in groups of about their root
+
 __host__ __device__ __forceinline__ size_t pa_piece_floats(int group, int dh) { return ((size_t)group * (dh + 2) + 3) / 4 * 4; }
-__host__ __device__ __forceinline__ size_t pa_header_bytes(int blocks) { return ((size_t)blocks * 8 + 255) / 256 * 256; }
-__device__ __forceinline__ float *pa_piece(const kie_paged_attention_args &a, int blocks, int block, int which) {
-  const int group = a.n_heads / a.pages.n_kv_heads;
-  return reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + pa_header_bytes(blocks)) +
-         ((size_t)block * 2 + which) * pa_piece_floats(group, a.pages.head_dim);
+__host__ __device__ __forceinline__ size_t pa_header_bytes(int blocks) {
+  return ((size_t)blocks * PA_WORDS * 8 + 255) / 256 * 256;
+}
+
+struct Workspace {
+  unsigned long long *words;
+  float *pieces;
+  size_t piece;  // floats
+  __device__ __forceinline__ Workspace(const kie_paged_attention_args &a, int dh)
+      : words(static_cast<unsigned long long *>(a.workspace)),
+        pieces(reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + pa_header_bytes(gridDim.x))),
+        piece(pa_piece_floats(a.n_heads / a.pages.n_kv_heads, dh)) {}
+  __device__ __forceinline__ unsigned long long *word(int block, int which) const { return words + block * PA_WORDS + which; }
+  __device__ __forceinline__ float *at(int block, int which) const { return pieces + ((size_t)block * PA_PIECES + which) * piece; }
+};
+
+// One more arrival at *word; true for the n-th, which leaves the word at 0. A word holds the call's number above 8 bits
+// of count: whatever it held before the call (an older call's number, other data) counts as no arrivals, so the
+// workspace needs no clearing; a replayed graph, whose number stays the same, finds the zeros of its last replay.
+__device__ __forceinline__ bool arrive(unsigned long long *word, unsigned long long call, int n) {
+  if (n == 1) return true;
+  unsigned long long seen = 0ull;  // what the last call left
+  while ((seen >> 8) != call) {    // a failed exchange finds other data once, or another block's first arrival
+    const unsigned long long was = atomicCAS(word, seen, (call << 8) | 1ull);
+    if (was == seen) return false;
+    seen = was;
+  }
+  if ((int)(atomicAdd(word, 1ull) & 255ull) + 1 < n) return false;
+  *word = 0ull;
+  return true;
+}
+
+// The block's earlier writes to the workspace are seen by the block that arrives last. Every thread must call.
+__device__ __forceinline__ bool block_arrive(unsigned long long *word, unsigned long long call, int n) {
+  __shared__ bool s_last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();  // cumulative: over the writes of the block's threads, ordered before it by the barrier
+    s_last = arrive(word, call, n);
+    __threadfence();
+  }
+  __syncthreads();
+  const bool last = s_last;
+  __syncthreads();
+  return last;
+}
+
+// A thread's share of a joined item: four dimensions d .. d + 3 of the rows r0, r0 + STEP, .. (ROWS of them at most).
+template <int DH>
+struct JoinShare {
+  static constexpr int LANES = DH / 4, STEP = PA_THREADS / LANES, ROWS = PA_ROWS / STEP;
+  int r0 = threadIdx.x / LANES, d = threadIdx.x % LANES * 4;
+};
+
+// The thread's share of pieces piece(0 .. n - 1), joined in order: put(r, d, sum, M, L) gets their sum at the largest
+// reference M. The loads of BATCH pieces are in flight at a time.
+template <int DH, class F, class P>
+__device__ __forceinline__ void join_pieces(const F &piece, int n, int group, const P &put) {
+  using S = JoinShare<DH>;
+  constexpr int BATCH = 8, R = S::ROWS;
+  const S me;
+  float top[R], sum[R];
+  float4 acc[R];
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    top[q] = -INFINITY;
+    sum[q] = 0.f;
+    acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  if (me.r0 >= group) return;
+  for (int i0 = 0; i0 < n; i0 += BATCH) {
+    float m[BATCH][R], l[BATCH][R];
+    float4 y[BATCH][R];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const float *p = piece(min(i0 + k, n - 1));
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        const int r = min(me.r0 + q * S::STEP, group - 1);
+        m[k][q] = __ldcg(p + group * DH + r);
+        l[k][q] = __ldcg(p + group * (DH + 1) + r);
+        y[k][q] = __ldcg(reinterpret_cast<const float4 *>(p + r * DH + me.d));
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      float mn = top[q];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k)
+        if (i0 + k < n) mn = fmaxf(mn, m[k][q]);
+      const float ref = mn == -INFINITY ? 0.f : mn, f0 = ex2(top[q] - ref);
+      sum[q] *= f0, acc[q].x *= f0, acc[q].y *= f0, acc[q].z *= f0, acc[q].w *= f0;
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k)
+        if (i0 + k < n) {
+          const float f = ex2(m[k][q] - ref);
+          sum[q] = fmaf(l[k][q], f, sum[q]);
+          acc[q].x = fmaf(y[k][q].x, f, acc[q].x), acc[q].y = fmaf(y[k][q].y, f, acc[q].y);
+          acc[q].z = fmaf(y[k][q].z, f, acc[q].z), acc[q].w = fmaf(y[k][q].w, f, acc[q].w);
+        }
+      top[q] = mn;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < R; ++q)
+    if (me.r0 + q * S::STEP < group) put(me.r0 + q * S::STEP, me.d, acc[q], top[q], sum[q]);
+}
+
+// Four dimensions of a query head's output from its weighted sum, and its lse from the reference M (log2 units) and the
+// sum of weights L: zeros and -inf where nothing was attended. vec: the output is aligned for one store of four.
+__device__ __forceinline__ void finish4(const kie_paged_attention_args &a, bool vec, int b, int64_t head, int d, float4 acc,
+                                        float M, float L) {
+  const float inv = L == 0.f ? 0.f : rcp(L);
+  const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+  const int64_t to = b * a.out_stride[0] + head * a.out_stride[1] + d;
+  if (!vec) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) paged_store(a.out, to + e, a.q_dtype, v[e]);
+  } else if (a.q_dtype == KIE_F32) {
+    *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + to) =
+        make_uint2(pack2(v[0], v[1], a.q_dtype), pack2(v[2], v[3], a.q_dtype));
+  }
+  if (d == 0 && a.lse) a.lse[(int64_t)b * a.n_heads + head] = L == 0.f ? -INFINITY : (M + lg2(L)) * LN2;
+}
+__device__ __forceinline__ bool out_vec(const kie_paged_attention_args &a) {
+  const int size = paged_dtype_bytes(a.q_dtype);
+  return ((uintptr_t)a.out | (uintptr_t)(a.out_stride[0] * size) | (uintptr_t)(a.out_stride[1] * size)) % (4 * size) == 0;
+}
+
+template <int DH>
+__device__ __forceinline__ void put_piece(float *p, int group, int r, int d, float4 acc, float M, float L) {
+  *reinterpret_cast<float4 *>(p + r * DH + d) = acc;
+  if (d == 0) {
+    p[group * DH + r] = M;
+    p[group * (DH + 1) + r] = L;
+  }
+}
+
+// After this block has written its piece of item (b, h), whose `units` units begin at place v of the list: whoever of
+// the blocks that share it comes last joins the pieces.
+template <int DH>
+__device__ __forceinline__ void publish(const kie_paged_attention_args &a, unsigned long long call, int b, int h, long long v,
+                                        int units, long long per_block) {
+  const Workspace ws(a, DH);
+  const int first = (int)(v / per_block), last = (int)((v + units - 1) / per_block);
+  const int group = a.n_heads / a.pages.n_kv_heads, n = last - first + 1;
+  int fan = n;
+  if (n > PA_ONE_LEVEL) {
+    fan = (int)ceilf(sqrtf((float)n));
+    const int g0 = ((int)blockIdx.x - first) / fan * fan, size = min(fan, n - g0), at = first + g0;
+    const int kind = g0 ? CONT : START;
+    if (!block_arrive(ws.word(at, kind), call, size)) return;
+    const auto piece = [&](int i) { return ws.at(at + i, g0 + i ? CONT : START); };
+    float *to = ws.at(at, JOINED + kind);
+    join_pieces<DH>(piece, size, group,
+                    [&](int r, int d, float4 acc, float M, float L) { put_piece<DH>(to, group, r, d, acc, M, L); });
+    if (!block_arrive(ws.word(first, ITEM), call, (n + fan - 1) / fan)) return;
+  } else if (!block_arrive(ws.word(first, START), call, n)) {
+    return;
+  }
+  const int parts = n > PA_ONE_LEVEL ? (n + fan - 1) / fan : n;
+  const auto piece = [&](int i) {
+    return n > PA_ONE_LEVEL ? ws.at(first + i * fan, JOINED + (i ? CONT : START)) : ws.at(first + i, i ? CONT : START);
+  };
+  const bool vec = out_vec(a);
+  join_pieces<DH>(piece, parts, group, [&](int r, int d, float4 acc, float M, float L) {
+    finish4(a, vec, b, (int64_t)h * group + r, d, acc, M, L);
+  });
 }
 
 // ---- the kernel ---------------------------------------------------------------------------------------------
 
-// Two consecutive elements at p + i as fp32; pair: p + i is aligned for one access.
-__device__ __forceinline__ float2 load_pair(const void *p, int64_t i, int dtype, bool pair) {
-  if (!pair) return make_float2(paged_load(p, i, dtype), paged_load(p, i + 1, dtype));
-  if (dtype == KIE_F32) return *reinterpret_cast<const float2 *>(static_cast<const float *>(p) + i);
-  const uint32_t w = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p) + i);
-  if (dtype == KIE_F16) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+// The pairs of elements at + off(0 .. N - 1) of a query head, as they are: two words each of fp32, else one. Nothing
+// waits for the loads here, so that they can be issued long before their use.
+template <int N, int WORDS, class F>
+__device__ __forceinline__ void request_pairs(const kie_paged_attention_args &a, int64_t at, const F &off, uint32_t (&w)[N * WORDS]) {
+  const int size = paged_dtype_bytes(a.q_dtype);
+  const bool pair = ((uintptr_t)a.q | (uintptr_t)(a.q_stride[0] * size) | (uintptr_t)(a.q_stride[1] * size)) % (2 * size) == 0;
+  if (WORDS == 2 && a.q_dtype == KIE_F32) {
+    const uint32_t *q = static_cast<const uint32_t *>(a.q) + at;
+    if (pair) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(q + off(i));
+        w[i * WORDS] = x.x, w[i * WORDS + WORDS - 1] = x.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i * WORDS] = q[off(i)], w[i * WORDS + WORDS - 1] = q[off(i) + 1];
+    }
+  } else {
+    const uint16_t *q = static_cast<const uint16_t *>(a.q) + at;
+    if (pair) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i * WORDS] = *reinterpret_cast<const uint32_t *>(q + off(i));
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i * WORDS] = q[off(i)] | (uint32_t)q[off(i) + 1] << 16;
+    }
+  }
 }
 
 // Where column d of a warp's output row r lies in the joining area: the accumulators' four column pairs of a lane
@@ -251,7 +469,8 @@ __device__ __forceinline__ int join_col(int r, int d) {
 }
 
 template <int KIND, int DH, bool SPLIT>
-__global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS_PER_SM) paged_attn_kernel(const kie_paged_attention_args a) {
+__global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS_PER_SM)
+paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
   using T = PaTile<KIND, DH>;
   using Sm = PaSmem<KIND, DH>;
   constexpr int NS = T::NS, CH = T::CH, ROW = T::ROW, ES = T::ES, SUBS = T::SUBS, LOADS = T::LOADS;
@@ -260,41 +479,38 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS_PER_SM) paged_attn_kerne
   static_assert(T::HALF >= PA_ROWS * DH * 4, "the joining area is one slot");
   extern __shared__ __align__(1024) uint8_t pa_raw[];
   Sm &sm = *reinterpret_cast<Sm *>(pa_raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int group = a.n_heads / a.pages.n_kv_heads;
   const unsigned bs = a.pages.block_size;
   const int bs_shift = (bs & (bs - 1)) ? -1 : __ffs(bs) - 1;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Cursor<T::UNIT> c;
-  long long total, per_block;
-  const int n_units = locate(a, &c, &total, &per_block);
-  if (threadIdx.x == 0) reinterpret_cast<int2 *>(a.workspace)[blockIdx.x] = make_int2(-1, -1);
-  if (n_units == 0) return;
+  int end;
+  long long per_block;
+  locate(a, &c, &end, &per_block);
+  if (c.v >= end) return;
 
   // Chunk ch of row r of a half lies at chunk ch ^ swz(r): the eight rows of an 8 x 8 matrix fall in different banks.
   const auto swz = [](int row) { return CH >= 8 ? row & 7 : (row >> 1) & 3; };
 
   // ---- producer side: the warp's tile of unit `p`, K half first, then V. A lane copies chunks lane + 32 i.
   Cursor<T::UNIT> p = c;
-  int p_index = 0;  // unit of the run that p stands at
   uint32_t p_live = 0;
-  int p_page[SUBS];
+  int p_base = 0, p_page[SUBS], p_id[SUBS];  // lane j: the pages of the warp's tile of unit p_base + j; of p's tile
   const int row0 = lane / CH;  // row of the lane's first chunk; the next are 32 / CH rows on
   const uint32_t dst_lane = (lane * 16) ^ (swz(row0) << 4);
-  const int64_t k_lane = (row0 * a.pages.k_stride[2]) * ES + (lane % CH) * 16, k_step = a.pages.k_stride[2] * ES * (32 / CH);
-  const int64_t v_lane = (row0 * a.pages.v_stride[2]) * ES + (lane % CH) * 16, v_step = a.pages.v_stride[2] * ES * (32 / CH);
+  const int k_lane = row0 * (int)a.pages.k_stride[2] * ES + (lane % CH) * 16;  // 16 rows span less than 2^31 bytes
+  const int v_lane = row0 * (int)a.pages.v_stride[2] * ES + (lane % CH) * 16;
   const uint32_t ring0 = smem_u32(sm.ring[warp]);
   auto first_pos = [&](const Cursor<T::UNIT> &x) { return x.s.from + (x.unit * PA_WARPS + warp) * T::POS; };
-  auto fetch_page = [&]() {  // the page ids of p's tile, requested one unit before they are used
-    const int pos = first_pos(p);
+  auto fetch_pages = [&]() {  // requested before the issue that uses them
+    p_base = p.unit;
 #pragma unroll
     for (int i = 0; i < SUBS; ++i) {
+      const int pos = first_pos(p) + lane * T::UNIT + 16 * i;
       p_page[i] = -1;
-      if (p_index < n_units && pos + 16 * i < p.s.len) {
-        const unsigned at = pos + 16 * i;
-        p_page[i] = a.block_table[p.b * a.table_stride + (bs_shift >= 0 ? at >> bs_shift : at / bs)];
-      }
+      if (p.v < end && pos < p.s.len)
+        p_page[i] = a.block_table[p.b * a.table_stride + (bs_shift >= 0 ? (unsigned)pos >> bs_shift : (unsigned)pos / bs)];
     }
   };
   auto issue = [&](int slot, bool is_v) {
@@ -304,19 +520,22 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS_PER_SM) paged_attn_kerne
       p_live = hi >= T::POS ? FULL : hi > 0 ? (1u << hi) - 1u : 0u;
       if (lo > 0) p_live &= lo >= 32 ? 0u : ~((1u << lo) - 1u);
 #pragma unroll
-      for (int i = 0; i < SUBS; ++i)
-        if ((unsigned)p_page[i] >= (unsigned)a.pages.n_blocks) p_live &= ~(0xffffu << (16 * i));
+      for (int i = 0; i < SUBS; ++i) {
+        p_id[i] = __shfl_sync(0xffffffffu, p_page[i], p.unit - p_base);
+        if ((unsigned)p_id[i] >= (unsigned)a.pages.n_blocks) p_live &= ~(0xffffu << (16 * i));
+      }
+      if (p.v >= end) p_live = 0u;  // behind the run
       if (lane == 0) sm.live[warp][slot] = p_live;
     }
     if (p_live) {
       const int64_t *st = is_v ? a.pages.v_stride : a.pages.k_stride;
-      const int64_t step = is_v ? v_step : k_step;
+      const int step = (int)st[2] * ES * (32 / CH);
       const uint32_t dst = ring0 + slot * T::HALF + dst_lane;
 #pragma unroll
       for (int s = 0; s < SUBS; ++s) {
         const unsigned at = pos + 16 * s, off = bs_shift >= 0 ? at & (bs - 1) : at % bs;
         const uint32_t live = (p_live >> (16 * s)) & 0xffffu;
-        const int64_t page = live ? p_page[s] : 0;  // an address inside the pages even where nothing is read
+        const int64_t page = live ? p_id[s] : 0;  // an address inside the pages even where nothing is read
         const uint8_t *src = static_cast<const uint8_t *>(is_v ? a.pages.v : a.pages.k) +
                              (page * st[0] + p.h * st[1] + off * st[2]) * ES + (is_v ? v_lane : k_lane);
         constexpr int N = LOADS / SUBS;
@@ -339,29 +558,29 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS_PER_SM) paged_attn_kerne
         const int64_t *ss = is_v ? a.pages.v_scale_stride : a.pages.k_scale_stride;
         const unsigned at = pos + lane, off = bs_shift >= 0 ? at & (bs - 1) : at % bs;
         const bool live = (p_live >> lane) & 1u;
-        const int64_t page = live ? (lane < 16 ? p_page[0] : p_page[SUBS - 1]) : 0;
+        const int64_t page = live ? (lane < 16 ? p_id[0] : p_id[SUBS - 1]) : 0;
         cp_async4(&sm.scale[warp][KIND == PG_E4M3 ? slot : 0][lane],
                   (is_v ? a.pages.v_scale : a.pages.k_scale) + page * ss[0] + p.h * ss[1] + off * ss[2],
                   live);
       }
     }
     if (is_v) {
-      if (++p_index < n_units) {
-        p.next(a);
-        if (p.unit == 0 && warp == 0) {  // a new item: its queries towards L2, a line to a lane
-          const int bytes = DH * paged_dtype_bytes(a.q_dtype), at = lane * 128;
-          const int r = at / bytes;
-          if (r < group)
-            prefetch_l2(static_cast<const uint8_t *>(a.q) +
-                        (p.b * a.q_stride[0] + (int64_t)(p.h * group + r) * a.q_stride[1]) * paged_dtype_bytes(a.q_dtype) +
-                        at % bytes);
-        }
-      }
-      fetch_page();
+      if (p.v < end) p.next(a);
+      if (p.unit == 0 || p.unit == p_base + 32) fetch_pages();
     }
   };
 
-  fetch_page();
+  // the first item's queries, and its pages, on their way together
+  const int g = lane >> 2, t = lane & 3;
+  uint32_t raw[2 * KSTEPS * (SPLIT ? 2 : 1)];
+  auto request_q = [&](int b, int h) {
+    // E4M3 rows come as four codes to a lane, so that the k order of a step is 4t .. 4t + 3
+    request_pairs<2 * KSTEPS, SPLIT ? 2 : 1>(
+        a, b * a.q_stride[0] + (int64_t)(h * group + min(g, group - 1)) * a.q_stride[1],
+        [&](int i) { return 16 * (i >> 1) + (KIND == PG_E4M3 ? 4 * t + 2 * (i & 1) : 2 * t + 8 * (i & 1)); }, raw);
+  };
+  request_q(c.b, c.h);
+  fetch_pages();
 #pragma unroll
   for (int x = 0; x < NS - 1; ++x) {
     issue(x, x & 1);
@@ -373,32 +592,27 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS_PER_SM) paged_attn_kerne
   const uint32_t v_at = ((((lane >> 4) << 3) + (lane & 7)) * ROW) + ((((lane >> 3) & 1) ^ swz(lane & 7)) << 4);
   uint32_t qb[KSTEPS][SPLIT ? 4 : 2];
   float rs[2], m[2], bias[2], l[2], o[MT][4];  // rs: score scale in log2 units; bias: P_BIAS - m
-  bool first = true;
-  bool starts = c.unit == 0;  // this block holds the item's first unit
-  int ring = 0;               // slot of the next half
+  int ring = 0;  // slot of the next half
 
-  for (int u = 0; u < n_units; ++u) {
-    if (first) {  // a new item: its query heads as B fragments
-      first = false;
-      const int qs = paged_dtype_bytes(a.q_dtype);
-      const bool pair = ((uintptr_t)a.q | (uintptr_t)(a.q_stride[0] * qs) | (uintptr_t)(a.q_stride[1] * qs)) % (2 * qs) == 0;
-      const int64_t at = c.b * a.q_stride[0] + (int64_t)(c.h * group + g) * a.q_stride[1];
-      float2 f[KSTEPS][2];
-#pragma unroll
-      for (int st = 0; st < KSTEPS; ++st)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // E4M3 rows come as four codes to a lane, so that the k order of a step is 4t .. 4t + 3
-          const int d = 16 * st + (KIND == PG_E4M3 ? 4 * t + 2 * e : 2 * t + 8 * e);
-          f[st][e] = g < group ? load_pair(a.q, at + d, a.q_dtype, pair) : make_float2(0.f, 0.f);
-        }
+  for (;;) {  // an item, or this block's part of it
+    const int units = min(c.s.n - c.unit, end - c.v);
+    {  // its query heads as B fragments
       float down = 1.f;
-      if (SPLIT) {  // bring the head's largest element to [2^13, 2^14) by a power of two
+      if (!SPLIT) {
+#pragma unroll
+        for (int i = 0; i < 2 * KSTEPS; ++i) qb[i >> 1][i & 1] = g < group ? raw[SPLIT ? 0 : i] : 0u;
+      } else {  // bring the head's largest element to [2^13, 2^14) by a power of two
+        float2 f[2 * KSTEPS];
         float top = 0.f;
 #pragma unroll
-        for (int st = 0; st < KSTEPS; ++st)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) top = fmaxf(top, fmaxf(fabsf(f[st][e].x), fabsf(f[st][e].y)));
+        for (int i = 0; i < 2 * KSTEPS; ++i) {
+          const uint32_t w = raw[SPLIT ? 2 * i : i];
+          f[i] = a.q_dtype == KIE_F32   ? make_float2(__uint_as_float(w), __uint_as_float(raw[SPLIT ? 2 * i + 1 : i]))
+                 : a.q_dtype == KIE_F16 ? __half22float2(*reinterpret_cast<const __half2 *>(&w))
+                                        : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+          if (g >= group) f[i] = make_float2(0.f, 0.f);
+          top = fmaxf(top, fmaxf(fabsf(f[i].x), fabsf(f[i].y)));
+        }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         int e2 = 0;
@@ -406,17 +620,13 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS_PER_SM) paged_attn_kerne
         const float up = __int_as_float((127 + e2) << 23);
         down = __int_as_float((127 - e2) << 23);
 #pragma unroll
-        for (int st = 0; st < KSTEPS; ++st)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) f[st][e].x *= up, f[st][e].y *= up;
-      }
-#pragma unroll
-      for (int st = 0; st < KSTEPS; ++st)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          qb[st][e] = pack16<KIND>(f[st][e].x, f[st][e].y);
-          if (SPLIT) qb[st][SPLIT ? 2 + e : e] = rest16<KIND>(f[st][e].x, f[st][e].y, qb[st][e]);
+        for (int i = 0; i < 2 * KSTEPS; ++i) {
+          const float x = f[i].x * up, y = f[i].y * up;
+          const uint32_t w = pack16<KIND>(x, y);
+          qb[i >> 1][i & 1] = w;
+          qb[i >> 1][SPLIT ? 2 + (i & 1) : 0] = rest16<KIND>(x, y, w);
         }
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         rs[h] = a.scale * LOG2E;
@@ -429,6 +639,7 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS_PER_SM) paged_attn_kerne
       for (int n = 0; n < MT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     }
 
+    for (int u = 0; u < units; ++u) {
     // ---- K half: scores of the tile, s[.][2p + h] of position g + 8p and head 2t + h
     cp_wait<NS - 2>();
     __syncwarp();
@@ -565,157 +776,111 @@ __global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS_PER_SM) paged_attn_kerne
       }
     }
 
+    ring = ring + 1 == NS ? 0 : ring + 1;
+    }
+
     // ---- the item's end, or the run's: join the four warps through the slot just used
-    const bool ends = c.unit + 1 == c.s.n;
-    if (ends || u + 1 == n_units) {
+    const bool starts = c.unit == 0, ends = c.unit + units == c.s.n;
+    const int used = ring == 0 ? NS - 1 : ring - 1, b = c.b, h = c.h, n = c.s.n;
+    const long long v = blockIdx.x * per_block + c.v - c.unit;  // place of the item's first unit
+    c.unit += units - 1;
+    c.v += units - 1;
+    c.next(a);
+    const bool done = c.v >= end;
+    if (!done) request_q(c.b, c.h);  // the next item's queries arrive while this one is finished
+    {
       __syncwarp();  // every lane is done with the slot
-      float *join = reinterpret_cast<float *>(sm.ring[warp][ring]);
+      float *join = reinterpret_cast<float *>(sm.ring[warp][used]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int k = 0; k < 2; ++k) {
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], x);
-        const int r = 2 * t + h;
+        for (int x = 4; x < 32; x <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], x);
+        const int r = 2 * t + k;
         if (g == 0) {
-          sm.m[warp][r] = m[h] - P_BIAS;
-          sm.l[warp][r] = l[h];
+          reinterpret_cast<float *>(&sm.m[r])[warp] = m[k] - P_BIAS;
+          reinterpret_cast<float *>(&sm.l[r])[warp] = l[k];
         }
 #pragma unroll
         for (int n = 0; n < MT; ++n) {
           if (KIND == PG_E4M3) {
-            *reinterpret_cast<float2 *>(&join[r * DH + join_col<KIND>(r, 16 * n + 2 * g)]) = make_float2(o[n][h], o[n][2 + h]);
+            *reinterpret_cast<float2 *>(&join[r * DH + join_col<KIND>(r, 16 * n + 2 * g)]) = make_float2(o[n][k], o[n][2 + k]);
           } else {
-            join[r * DH + join_col<KIND>(r, 16 * n + g)] = o[n][h];
-            join[r * DH + join_col<KIND>(r, 16 * n + g + 8)] = o[n][2 + h];
+            join[r * DH + join_col<KIND>(r, 16 * n + g)] = o[n][k];
+            join[r * DH + join_col<KIND>(r, 16 * n + g + 8)] = o[n][2 + k];
           }
         }
       }
       __syncthreads();
       const bool whole = ends && starts;
-      float *piece = pa_piece(a, gridDim.x, blockIdx.x, starts ? 1 : 0);
-      for (int x = threadIdx.x; x < group * (DH / 4); x += PA_THREADS) {
-        const int r = x / (DH / 4), d = x % (DH / 4) * 4;
-        float M = -INFINITY, L = 0.f;
+      float *piece = Workspace(a, DH).at(blockIdx.x, starts ? START : CONT);
+      const bool vec = out_vec(a);
+      const JoinShare<DH> me;
 #pragma unroll
-        for (int w = 0; w < PA_WARPS; ++w) M = fmaxf(M, sm.m[w][r]);
-        const float ref = M == -INFINITY ? 0.f : M;
+      for (int q = 0; q < JoinShare<DH>::ROWS; ++q) {
+        const int r = me.r0 + q * JoinShare<DH>::STEP;
+        if (r >= group) break;
+        const float4 wm = sm.m[r], wl = sm.l[r];
+        const float M = fmaxf(fmaxf(wm.x, wm.y), fmaxf(wm.z, wm.w)), ref = M == -INFINITY ? 0.f : M;
+        const float f[PA_WARPS] = {ex2(wm.x - ref), ex2(wm.y - ref), ex2(wm.z - ref), ex2(wm.w - ref)};
+        const float L = fmaf(wl.w, f[3], fmaf(wl.z, f[2], fmaf(wl.y, f[1], wl.x * f[0])));
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < PA_WARPS; ++w) {
-          const float f = ex2(sm.m[w][r] - ref);
-          const float4 y = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm.ring[w][ring]) + r * DH +
-                                                             join_col<KIND>(r, d));
-          L = fmaf(sm.l[w][r], f, L);
-          acc.x = fmaf(y.x, f, acc.x), acc.y = fmaf(y.y, f, acc.y), acc.z = fmaf(y.z, f, acc.z), acc.w = fmaf(y.w, f, acc.w);
+          const float4 y = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(sm.ring[w][used]) + r * DH +
+                                                             join_col<KIND>(r, me.d));
+          acc.x = fmaf(y.x, f[w], acc.x), acc.y = fmaf(y.y, f[w], acc.y);
+          acc.z = fmaf(y.z, f[w], acc.z), acc.w = fmaf(y.w, f[w], acc.w);
         }
-        if (whole) {
-          paged_finish4(a, c.b, (int64_t)c.h * group + r, d, acc, M, L);
-        } else {
-          *reinterpret_cast<float4 *>(piece + r * DH + d) = acc;
-          if (d == 0) {
-            piece[group * DH + r] = M;
-            piece[group * (DH + 1) + r] = L;
-          }
-        }
+        if (whole)
+          finish4(a, vec, b, (int64_t)h * group + r, me.d, acc, M, L);
+        else
+          put_piece<DH>(piece, group, r, me.d, acc, M, L);
       }
-      if (starts && !ends && threadIdx.x == 0) {
-        const long long last = blockIdx.x * per_block + u + (c.s.n - 1 - c.unit);  // the item's last unit
-        reinterpret_cast<int2 *>(a.workspace)[blockIdx.x] =
-            make_int2(c.b * a.pages.n_kv_heads + c.h, (int)(last / per_block));
-      }
+      if (!whole)
+        publish<DH>(a, call, b, h, v, n, per_block);
       __syncthreads();  // the next half may land in the slot, and the next item's sums in theirs
-      first = true;
-      starts = true;
+      if (done) break;
     }
-    ring = ring + 1 == NS ? 0 : ring + 1;
-    if (u + 1 < n_units) c.next(a);
   }
   cp_wait<0>();
 }
 
-// Joins the pieces of the item that block blockIdx.x of the attention started and did not end, for one query head:
-// out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i over pieces in block order.
-constexpr int PJ_THREADS = 128;
-template <int DH>
-__global__ void __launch_bounds__(PJ_THREADS) paged_join_kernel(const kie_paged_attention_args a) {
-  constexpr int LANES = DH / 4, SETS = PJ_THREADS / LANES;  // a thread holds four dimensions of every SETS-th piece
-  __shared__ float4 s_acc[SETS][LANES];
-  __shared__ float s_m[SETS], s_l[SETS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int blocks = gridDim.x, r = blockIdx.y, group = a.n_heads / a.pages.n_kv_heads;
-  const int2 head = reinterpret_cast<const int2 *>(a.workspace)[blockIdx.x];
-  if (head.x < 0) return;
-  const int set = threadIdx.x / LANES, d = threadIdx.x % LANES * 4;
-  const int n = head.y - (int)blockIdx.x + 1;
-  float M = -INFINITY, L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = set; i < n; i += SETS) {
-    const float *p = pa_piece(a, blocks, blockIdx.x + i, i == 0 ? 1 : 0);
-    const float4 y = *reinterpret_cast<const float4 *>(p + r * DH + d);
-    const float m = p[group * DH + r], l = p[group * (DH + 1) + r];
-    const float mn = fmaxf(M, m), ref = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2(m - ref), k = ex2(M - ref);
-    L = fmaf(L, k, l * f);
-    acc.x = fmaf(acc.x, k, y.x * f), acc.y = fmaf(acc.y, k, y.y * f);
-    acc.z = fmaf(acc.z, k, y.z * f), acc.w = fmaf(acc.w, k, y.w * f);
-    M = mn;
-  }
-  s_acc[set][d / 4] = acc;
-  if (d == 0) {
-    s_m[set] = M;
-    s_l[set] = L;
-  }
-  __syncthreads();
-  if (set != 0) return;
-  for (int s = 1; s < SETS; ++s) {
-    const float m = s_m[s], mn = fmaxf(M, m), ref = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2(m - ref), k = ex2(M - ref);
-    const float4 y = s_acc[s][d / 4];
-    L = fmaf(L, k, s_l[s] * f);
-    acc.x = fmaf(acc.x, k, y.x * f), acc.y = fmaf(acc.y, k, y.y * f);
-    acc.z = fmaf(acc.z, k, y.z * f), acc.w = fmaf(acc.w, k, y.w * f);
-    M = mn;
-  }
-  paged_finish4(a, head.x / a.pages.n_kv_heads, (int64_t)(head.x % a.pages.n_kv_heads) * group + r, d, acc, M, L);
+// 56 bits, never 0, that no other call of the process has (steps through the odd numbers) and other data hardly holds.
+unsigned long long call_number() {
+  static std::atomic<uint64_t> calls{0x9e3779b97f4a7dull};
+  return calls.fetch_add(0x3c6ef372fe94faull, std::memory_order_relaxed) & ((1ull << 56) - 1);
 }
 
 template <int KIND, int DH, bool SPLIT>
-cudaError_t launch(const kie_paged_attention_args &a, int blocks, cudaStream_t stream) {
+cudaError_t launch(const kie_paged_attention_args &a, int dev, int sms, cudaStream_t stream) {
+  static std::atomic<uint64_t> ready{0};  // devices whose limit of dynamic shared memory is raised
   const int smem = sizeof(PaSmem<KIND, DH>);
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<KIND, DH, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  paged_attn_kernel<KIND, DH, SPLIT><<<blocks, PA_THREADS, smem, stream>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // the joining kernel is launched while the attention runs and waits for its end on the device
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, a.n_heads / a.pages.n_kv_heads);
-  cfg.blockDim = dim3(PJ_THREADS);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<DH>, a);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!bit || !(ready.load(std::memory_order_relaxed) & bit)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(paged_attn_kernel<KIND, DH, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  paged_attn_kernel<KIND, DH, SPLIT><<<sms * PA_BLOCKS_PER_SM, PA_THREADS, smem, stream>>>(a, call_number());
+  return cudaGetLastError();
 }
 
 template <int DH>
-cudaError_t launch_dh(const kie_paged_attention_args &a, int blocks, cudaStream_t stream) {
-  if (a.pages.dtype == KIE_BF16) return launch<PG_BF16, DH, false>(a, blocks, stream);
-  if (a.pages.dtype == KIE_E4M3) return launch<PG_E4M3, DH, true>(a, blocks, stream);
-  return a.q_dtype == KIE_F32 ? launch<PG_F16, DH, true>(a, blocks, stream) : launch<PG_F16, DH, false>(a, blocks, stream);
+cudaError_t launch_dh(const kie_paged_attention_args &a, int dev, int sms, cudaStream_t stream) {
+  if (a.pages.dtype == KIE_BF16) return launch<PG_BF16, DH, false>(a, dev, sms, stream);
+  if (a.pages.dtype == KIE_E4M3) return launch<PG_E4M3, DH, true>(a, dev, sms, stream);
+  return a.q_dtype == KIE_F32 ? launch<PG_F16, DH, true>(a, dev, sms, stream) : launch<PG_F16, DH, false>(a, dev, sms, stream);
 }
 
 }  // namespace
 }  // namespace kie
 
 size_t kie_paged_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim, int sms) {
-  const int blocks = sms * kie::PA_BLOCKS_PER_SM;
-  return kie::pa_header_bytes(blocks) + (size_t)blocks * 2 * kie::pa_piece_floats(n_heads / n_kv_heads, head_dim) * 4;
+  const size_t blocks = (size_t)sms * kie::PA_BLOCKS_PER_SM;
+  return kie::pa_header_bytes(blocks) + blocks * kie::PA_PIECES * kie::pa_piece_floats(n_heads / n_kv_heads, head_dim) * 4;
 }
 
-cudaError_t kie_launch_paged_attention(const kie_paged_attention_args &a, int sms, cudaStream_t stream) {
-  const int blocks = sms * kie::PA_BLOCKS_PER_SM;
-  return a.pages.head_dim == 64 ? kie::launch_dh<64>(a, blocks, stream) : kie::launch_dh<128>(a, blocks, stream);
+cudaError_t kie_launch_paged_attention(const kie_paged_attention_args &a, int dev, int sms, cudaStream_t stream) {
+  return a.pages.head_dim == 64 ? kie::launch_dh<64>(a, dev, sms, stream) : kie::launch_dh<128>(a, dev, sms, stream);
 }

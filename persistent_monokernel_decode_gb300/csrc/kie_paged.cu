@@ -16,81 +16,101 @@ namespace {
 
 constexpr int PX_THREADS = 512;
 
-__device__ __forceinline__ long long warp_scan(long long v) {  // inclusive, over the lanes
+// Inclusive sums of v and w over the block's threads; all[0], all[1] get the sums of all. Every thread must call it.
+__device__ __forceinline__ void block_scan(long long &v, long long &w, long long (&all)[2]) {
+  constexpr int WARPS = PX_THREADS / 32;
+  __shared__ long long part[2][WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, v, o);
-    if ((threadIdx.x & 31) >= o) v += u;
+    const long long a = __shfl_up_sync(0xffffffffu, v, o), b = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) v += a, w += b;
   }
-  return v;
-}
-
-// Inclusive sum over the block's threads; *total gets the sum of all. Every thread must call it.
-__device__ __forceinline__ long long block_scan(long long v, long long *total) {
-  __shared__ long long part[PX_THREADS / 32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  v = warp_scan(v);
   __syncthreads();  // the last call's readers are done
-  if (lane == 31) part[warp] = v;
+  if (lane == 31) part[0][warp] = v, part[1][warp] = w;
   __syncthreads();
-  long long before = 0, all = 0;
-  for (int w = 0; w < PX_THREADS / 32; ++w) {
-    if (w < warp) before += part[w];
-    all += part[w];
+  long long a = lane < WARPS ? part[0][lane] : 0, b = lane < WARPS ? part[1][lane] : 0;  // every warp scans the warps' sums
+#pragma unroll
+  for (int o = 1; o < WARPS; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+    if (lane >= o) a += x, b += y;
   }
-  *total = all;
-  return v + before;
+  all[0] = __shfl_sync(0xffffffffu, a, WARPS - 1);
+  all[1] = __shfl_sync(0xffffffffu, b, WARPS - 1);
+  const long long before_v = __shfl_sync(0xffffffffu, a, (warp + 31) & 31), before_w = __shfl_sync(0xffffffffu, b, (warp + 31) & 31);
+  if (warp > 0) v += before_v, w += before_w;
 }
 
 __device__ __forceinline__ int clamp_int(long long v) { return (int)(v > INT_MAX ? INT_MAX : v); }
 
-// Every block scans all requests (two running sums: rows, and pages needed) and then writes its share: the requests
-// r = blockIdx.x (mod grid) and the rows [blockIdx.x * per, + per). No block waits for another.
+// Every block scans all requests (two running sums in one pass: rows, and pages needed) and then writes its share: the
+// requests r = blockIdx.x (mod grid) and the rows [blockIdx.x * per, + per). No block waits for another. One scan does
+// for both sums although a request whose rows do not fit needs no pages: such requests are all behind those that fit.
+// Bound by latency (a load, the scan, a search and a load): 1,025 requests and 84,208 rows move 1.05 MB.
+// PER requests to a thread: 1 up to 512 requests (each request's pages are then taken by a thread of its own), else 4.
+template <int PER>
 __global__ void __launch_bounds__(PX_THREADS) paged_extend_kernel(const kie_paged_extend_args a, int per) {
-  __shared__ long long s_end[PX_THREADS], s_first[PX_THREADS];
-  __shared__ int s_start[PX_THREADS], s_len[PX_THREADS], s_have[PX_THREADS];  // s_have < 0: not admitted
+  constexpr int CHUNK = PX_THREADS * PER;  // requests of a pass over the block
+  __shared__ int s_end[CHUNK], s_first[CHUNK], s_start[CHUNK], s_len[CHUNK], s_have[CHUNK];  // s_have < 0: not admitted
+  __shared__ int s_taken;  // pages given
   const int tid = threadIdx.x, bs = a.block_size;
   const int n_free = min(max(*a.n_free, 0), a.free_capacity);
   const long long cap = (long long)a.max_blocks * bs;
   const long long t0 = (long long)blockIdx.x * per, t1 = min(t0 + per, (long long)a.n_rows);
   long long rows = 0, pages = 0;  // of the chunks before
-  long long taken = 0;            // pages really given
-  for (int r0 = 0; r0 < a.n_seqs; r0 += PX_THREADS) {
-    const int r = r0 + tid;
-    const bool in = r < a.n_seqs;
-    const int len = in ? a.lens[r] : 0, nw = in ? a.new_lens[r] : 0;
-    const bool sane = in && len >= 0 && nw >= 0;
-    long long all;
-    const long long end = rows + block_scan(sane ? nw : 0, &all), start = end - (sane ? nw : 0);
-    const long long rows_next = rows + all;
-    const long long sum = (long long)len + nw;
-    const bool fits = sane && sum <= cap && end <= a.n_rows;
-    const int have = sane ? (int)((len + (long long)bs - 1) / bs) : 0;
-    const int need = fits ? (int)((sum + bs - 1) / bs) - have : 0;
-    const long long after = pages + block_scan(need, &all);
-    const bool ok = fits && (need == 0 || after <= n_free);
-    pages += all;
-    const long long first = after - need;
-    block_scan(ok ? need : 0, &all);
-    taken += all;
-    s_end[tid] = in ? end : LLONG_MAX;
-    s_start[tid] = clamp_int(start);
-    s_first[tid] = first;
-    s_len[tid] = len;
-    s_have[tid] = ok ? have : -1;
-    if (in && r % gridDim.x == blockIdx.x) {
-      a.lens_out[r] = ok ? (int)sum : len;
-      a.admitted[r] = ok;
-      a.row_start[r] = clamp_int(start);
-      if (ok)
-        for (int j = 0; j < need; ++j)
-          a.block_table[r * a.table_stride + have + j] = a.free_blocks[n_free - 1 - (first + j)];
+  if (tid == 0) s_taken = 0;
+  for (int r0 = 0; r0 < a.n_seqs; r0 += CHUNK) {
+    int len[PER], nw[PER], have[PER], need[PER];
+    long long v = 0, w = 0, all[2];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int r = r0 + tid * PER + i;
+      len[i] = r < a.n_seqs ? a.lens[r] : -1;
+      nw[i] = r < a.n_seqs ? a.new_lens[r] : -1;
     }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const bool sane = len[i] >= 0 && nw[i] >= 0;
+      const long long sum = (long long)len[i] + nw[i];
+      have[i] = sane && sum <= cap ? (int)((unsigned)(len[i] + bs - 1) / (unsigned)bs) : -1;  // -1: no room in the table
+      need[i] = have[i] >= 0 ? (int)((unsigned)(sum + bs - 1) / (unsigned)bs) - have[i] : 0;
+      v += sane ? nw[i] : 0;
+      w += need[i];
+    }
+    const long long mine_v = v, mine_w = w;
+    block_scan(v, w, all);
+    long long end = rows + v - mine_v, after = pages + w - mine_w;
+    int taken = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int x = tid * PER + i, r = r0 + x;
+      const long long start = end, first = after;
+      if (len[i] >= 0 && nw[i] >= 0) end += nw[i];
+      after += need[i];
+      const bool ok = have[i] >= 0 && end <= a.n_rows && (need[i] == 0 || after <= n_free);
+      if (ok && need[i]) taken = (int)after;
+      s_end[x] = r < a.n_seqs ? clamp_int(end) : INT_MAX;
+      s_start[x] = clamp_int(start);
+      s_first[x] = clamp_int(first);
+      s_len[x] = len[i];
+      s_have[x] = ok ? have[i] : -1;
+      if (r < a.n_seqs && r % gridDim.x == blockIdx.x) {
+        a.lens_out[r] = ok ? len[i] + nw[i] : len[i];
+        a.admitted[r] = ok;
+        a.row_start[r] = clamp_int(start);
+        if (ok)
+          for (int j = 0; j < need[i]; ++j)
+            a.block_table[r * a.table_stride + have[i] + j] = a.free_blocks[n_free - 1 - (first + j)];
+      }
+    }
+    if (taken) atomicMax(&s_taken, taken);  // the pages up to the last request admitted
+    const long long rows_next = rows + all[0];
+    pages += all[1];
     __syncthreads();
     // rows of this chunk's requests that are this block's
     const long long lo = max(t0, rows), hi = min(t1, rows_next);
     for (long long t = lo + tid; t < hi; t += PX_THREADS) {
-      int x = 0, n = min(PX_THREADS, a.n_seqs - r0);  // the first request whose rows end past t
+      int x = 0, n = min(CHUNK, a.n_seqs - r0);  // the first request whose rows end past t
       while (n > 0) {
         const int half = n >> 1;
         if (s_end[x + half] <= t) {
@@ -104,10 +124,10 @@ __global__ void __launch_bounds__(PX_THREADS) paged_extend_kernel(const kie_page
       const int pos = s_len[x] + (int)(t - s_start[x]);
       int slot = -1;
       if (ok) {
-        const int j = pos / bs;
+        const int j = (int)((unsigned)pos / (unsigned)bs);
         const int page = j < s_have[x] ? a.block_table[(r0 + x) * a.table_stride + j]
-                                       : a.free_blocks[n_free - 1 - (s_first[x] + j - s_have[x])];
-        slot = page * bs + pos % bs;
+                                       : a.free_blocks[n_free - 1 - ((long long)s_first[x] + j - s_have[x])];
+        slot = page * bs + pos - j * bs;
       }
       a.slots[t] = slot;
       a.positions[t] = ok ? pos : -1;
@@ -121,37 +141,67 @@ __global__ void __launch_bounds__(PX_THREADS) paged_extend_kernel(const kie_page
     a.positions[t] = -1;
     a.seqs[t] = -1;
   }
+  __syncthreads();
   if (blockIdx.x == 0 && tid == 0) {
     a.row_start[a.n_seqs] = clamp_int(rows);
-    *a.n_free_out = (int)(n_free - taken);
+    *a.n_free_out = n_free - s_taken;
   }
 }
 
+// Every block scans the page counts of all finished requests and copies the pages of its share, the requests
+// r = blockIdx.x (mod grid), PX_TEAM threads to each. Bound by latency like the above.
+constexpr int PX_TEAM = 128;
+template <int PER>
 __global__ void __launch_bounds__(PX_THREADS) paged_release_kernel(const kie_paged_release_args a) {
-  __shared__ long long s_first[PX_THREADS];
-  __shared__ int s_pages[PX_THREADS];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, bs = a.block_size;
+  constexpr int CHUNK = PX_THREADS * PER;  // requests of a pass over the block
+  __shared__ long long s_first[CHUNK];
+  __shared__ int s_pages[CHUNK];
+  const int tid = threadIdx.x, bs = a.block_size;
   const int n_free = min(max(*a.n_free, 0), a.free_capacity);
   long long pages = 0;
-  for (int r0 = 0; r0 < a.n_seqs; r0 += PX_THREADS) {
-    const int r = r0 + tid;
-    const bool in = r < a.n_seqs, done = in && a.done[r];
-    const int len = in ? a.lens[r] : 0;
-    const int mine = done && len > 0 ? (int)min((len + (long long)bs - 1) / bs, (long long)a.max_blocks) : 0;
-    long long all;
-    s_first[tid] = pages + block_scan(mine, &all) - mine;
-    s_pages[tid] = mine;
-    pages += all;
-    if (in && r % gridDim.x == blockIdx.x) a.lens_out[r] = done ? 0 : len;
+  for (int r0 = 0; r0 < a.n_seqs; r0 += CHUNK) {
+    int len[PER], mine[PER];
+    bool done[PER];
+    long long v = 0, unused = 0, all[2];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int r = r0 + tid * PER + i;
+      done[i] = r < a.n_seqs && a.done[r];
+      len[i] = r < a.n_seqs ? a.lens[r] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      mine[i] = done[i] && len[i] > 0 ? min((int)(((unsigned)len[i] + bs - 1) / (unsigned)bs), a.max_blocks) : 0;
+      v += mine[i];
+    }
+    const long long sum = v;
+    block_scan(v, unused, all);
+    v += pages - sum;
+    pages += all[0];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int x = tid * PER + i, r = r0 + x;
+      s_first[x] = v;
+      s_pages[x] = mine[i];
+      v += mine[i];
+      if (r < a.n_seqs && r % gridDim.x == blockIdx.x) a.lens_out[r] = done[i] ? 0 : len[i];
+    }
     __syncthreads();
-    // a warp to each of this block's requests
-    const int n = min(PX_THREADS, a.n_seqs - r0);
+    const int n = min(CHUNK, a.n_seqs - r0);
     const int skew = (int)((blockIdx.x + gridDim.x - r0 % gridDim.x) % gridDim.x);
-    for (int x = skew + warp * gridDim.x; x < n; x += gridDim.x * (PX_THREADS / 32))
-      for (int j = lane; j < s_pages[x]; j += 32) {
-        const long long to = n_free + s_first[x] + j;
-        if (to < a.free_capacity) a.free_blocks[to] = a.block_table[(r0 + x) * a.table_stride + j];
+    for (int x = skew + (tid / PX_TEAM) * gridDim.x; x < n; x += gridDim.x * (PX_THREADS / PX_TEAM)) {
+      const int *from = a.block_table + (r0 + x) * a.table_stride;
+      const long long to = n_free + s_first[x];
+      const int count = (int)min((long long)s_pages[x], a.free_capacity - to);
+      for (int j0 = tid % PX_TEAM; j0 < count; j0 += 4 * PX_TEAM) {  // four loads in flight
+        int id[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) id[i] = j0 + i * PX_TEAM < count ? from[j0 + i * PX_TEAM] : 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (j0 + i * PX_TEAM < count) a.free_blocks[to + j0 + i * PX_TEAM] = id[i];
       }
+    }
     __syncthreads();
   }
   if (blockIdx.x == 0 && tid == 0) *a.n_free_out = (int)min(n_free + pages, (long long)a.free_capacity);
@@ -166,91 +216,182 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float scale) {
-  uint32_t w[2] = {0u, 0u};
+constexpr int PP_THREADS = 128;
+constexpr int PP_HEADS = 2;  // heads of a row that a thread takes: their loads are in flight together, and share the angles
+
+__device__ __forceinline__ bool codes_fast(float scale) { return scale >= 0x1p-90f && scale <= 0x1p90f; }
+
+// E4M3 codes of v / scale, the quotient correctly rounded. With r = RN(1 / scale), q = RN(v r) and the exact remainder
+// v - q scale, RN(q + r remainder) is the correctly rounded quotient (Markstein, IBM J. Res. Dev. 34, 1990); the row's
+// elements are at most 448 scale, so nothing overflows, and a remainder that underflows belongs to a quotient below
+// 2^-50, whose code is 0 either way. Scales near the ends of the range take the division.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float scale, float r, bool fast) {
+  uint32_t w[2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    w[e >> 2] |= (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(v[e], scale), __NV_SATFINITE, __NV_E4M3) << (8 * (e & 3));
+  for (int h = 0; h < 2; ++h) {
+    float q[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = v[4 * h + e];
+      if (fast) {
+        const float q0 = __fmul_rn(x, r);
+        q[e] = __fmaf_rn(__fmaf_rn(-q0, scale, x), r, q0);
+      } else {
+        q[e] = __fdiv_rn(x, scale);
+      }
+    }
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3);
+    w[h] = lo | hi << 16;
+  }
   return make_uint2(w[0], w[1]);
 }
 
-constexpr int PP_THREADS = 256;
+// Eight consecutive elements of type X, as loaded.
+template <int X>
+struct Eight {
+  static constexpr int WORDS = X == KIE_F32 ? 8 : 4;
+  uint32_t w[WORDS];
+  template <bool VEC>
+  __device__ __forceinline__ void load(const void *p, int64_t i) {
+    if (VEC) {
+      const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p) + i * (WORDS / 2));
+#pragma unroll
+      for (int k = 0; k < WORDS / 4; ++k) {
+        const uint4 x = s[k];
+        w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < WORDS; ++k)
+        w[k] = X == KIE_F32 ? static_cast<const uint32_t *>(p)[i + k]
+                            : static_cast<const uint16_t *>(p)[i + 2 * k] |
+                                  (uint32_t) static_cast<const uint16_t *>(p)[i + 2 * k + 1] << 16;
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int k = 0; k < WORDS; ++k) {
+      if (X == KIE_F32) {
+        v[k] = __uint_as_float(w[k]);
+      } else if (X == KIE_F16) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+        v[(2 * k) & 7] = f.x, v[(2 * k + 1) & 7] = f.y;
+      } else {
+        v[(2 * k) & 7] = __uint_as_float(w[k] << 16), v[(2 * k + 1) & 7] = __uint_as_float(w[k] & 0xffff0000u);
+      }
+    }
+  }
+};
 
-// DH / 16 threads to each head of each row: thread t holds elements 8t .. 8t + 7 and their partners of the other
-// half. The rotation's products and sums are rounded one by one (no fused multiply-add), so that a plain fp32
-// evaluation gives the same bits, and with them the same E4M3 codes.
-template <int DH, bool VEC>
+// DH / 16 threads to PP_HEADS heads of a row, a warp's teams on the same heads of neighbouring rows (so that a warp does
+// not diverge between queries, keys and values): thread t holds elements 8t .. 8t + 7 of each and their partners of the
+// other half. The rotation's products and sums are rounded one by one (no fused multiply-add), so that a plain fp32
+// evaluation gives the same bits, and with them the same E4M3 codes. Bound by HBM where there are many rows (each
+// element is read and written once), by a chain of two loads where there are few.
+template <int DH, int X, bool VEC>
 __global__ void __launch_bounds__(PP_THREADS) paged_append_kernel(const kie_paged_append_args a) {
   constexpr int TPH = DH / 16, HALF = DH / 2;
   const kie_pages &pg = a.pages;
-  const unsigned nq = a.q ? a.n_heads : 0u, heads = nq + 2u * pg.n_kv_heads;
-  const unsigned u = (blockIdx.x * PP_THREADS + threadIdx.x) / TPH;
-  const int i0 = (threadIdx.x % TPH) * 8;
-  if (u >= (unsigned)a.n_rows * heads) return;  // whole groups of TPH threads leave together
-  const int row = u / heads;
-  unsigned h = u % heads;
+  const unsigned nq = a.q ? a.n_heads : 0u, heads = nq + 2u * pg.n_kv_heads, groups = (heads + PP_HEADS - 1) / PP_HEADS;
+  const unsigned warp = (blockIdx.x * PP_THREADS + threadIdx.x) / 32, lane = threadIdx.x & 31;
+  const int i0 = (lane % TPH) * 8;
+  const int row = warp / groups * (32 / TPH) + lane / TPH;
+  const unsigned head0 = warp % groups * PP_HEADS;
+  if (row >= a.n_rows) return;  // whole teams of TPH threads leave together
   const int slot = a.slots[row];
   const int pos = a.rope ? a.positions[row] : 0;
-  if (slot < 0 || slot >= pg.n_blocks * pg.block_size || (a.rope && (pos < 0 || pos >= a.n_pos))) return;
-  const int what = h < nq ? 0 : h < nq + pg.n_kv_heads ? 1 : 2;  // q, k, v
-  h -= what == 0 ? 0u : what == 1 ? nq : nq + pg.n_kv_heads;
-  float lo[8], hi[8];
-  const void *src = what == 0 ? a.q : what == 1 ? a.k : a.v;
-  const int64_t *ss = what == 0 ? a.q_stride : what == 1 ? a.k_stride : a.v_stride;
-  const int64_t at = row * ss[0] + h * ss[1];
-  if (what == 1 && a.k_pairs) {
-    float x[8], y[8];
-    load8<VEC>(src, at + 2 * i0, a.x_dtype, x);
-    load8<VEC>(src, at + 2 * i0 + 8, a.x_dtype, y);
+  Eight<X> raw[PP_HEADS][2];  // as they are: converted when it is their turn
 #pragma unroll
-    for (int e = 0; e < 4; ++e) lo[e] = x[2 * e], hi[e] = x[2 * e + 1], lo[4 + e] = y[2 * e], hi[4 + e] = y[2 * e + 1];
-  } else {
-    load8<VEC>(src, at + i0, a.x_dtype, lo);
-    load8<VEC>(src, at + i0 + HALF, a.x_dtype, hi);
+  for (int j = 0; j < PP_HEADS; ++j) {
+    const unsigned head = head0 + j;
+    if (head >= heads) break;
+    const bool is_q = head < nq, is_k = !is_q && head < nq + pg.n_kv_heads;
+    const unsigned h = head - (is_q ? 0u : is_k ? nq : nq + pg.n_kv_heads);
+    const void *src = is_q ? a.q : is_k ? a.k : a.v;
+    const int64_t *ss = is_q ? a.q_stride : is_k ? a.k_stride : a.v_stride;
+    const int64_t at = row * ss[0] + h * ss[1];
+    // k_pairs: element pairs (i, i + HALF) are adjacent; they are told apart below
+    const bool pairs = is_k && a.k_pairs;
+    raw[j][0].template load<VEC>(src, at + (pairs ? 2 * i0 : i0));
+    raw[j][1].template load<VEC>(src, at + (pairs ? 2 * i0 + 8 : i0 + HALF));
   }
-  if (what < 2 && a.rope) {
+  if (slot < 0 || slot >= pg.n_blocks * pg.block_size || (a.rope && (pos < 0 || pos >= a.n_pos))) return;
+  float c[8], s[8];
+  if (a.rope && head0 < nq + pg.n_kv_heads) {
     const float4 *cs = reinterpret_cast<const float4 *>(a.rope + ((int64_t)pos * HALF + i0) * 2);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float4 w = cs[e];  // cos, sin of two pairs
-      const float c[2] = {w.x, w.z}, s[2] = {w.y, w.w};
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const float x = lo[2 * e + f], y = hi[2 * e + f];
-        lo[2 * e + f] = __fsub_rn(__fmul_rn(x, c[f]), __fmul_rn(y, s[f]));
-        hi[2 * e + f] = __fadd_rn(__fmul_rn(y, c[f]), __fmul_rn(x, s[f]));
-      }
+      c[2 * e] = w.x, s[2 * e] = w.y, c[2 * e + 1] = w.z, s[2 * e + 1] = w.w;
     }
   }
-  if (what == 0) {
-    const int64_t to = row * a.q_out_stride[0] + h * a.q_out_stride[1] + i0;
-    store8<VEC>(a.q_out, to, a.x_dtype, lo);
-    store8<VEC>(a.q_out, to + HALF, a.x_dtype, hi);
-    return;
-  }
-  const int64_t page = slot / pg.block_size, off = slot % pg.block_size;
-  const int64_t *cst = what == 1 ? pg.k_stride : pg.v_stride;
-  const int64_t to = page * cst[0] + h * cst[1] + off * cst[2] + i0;
-  void *dst = what == 1 ? pg.k : pg.v;
-  if (pg.dtype != KIE_E4M3) {
-    store8<true>(dst, to, pg.dtype, lo);
-    store8<true>(dst, to + HALF, pg.dtype, hi);
-    return;
-  }
-  float top = 0.f;
+  const int64_t page = (unsigned)slot / (unsigned)pg.block_size, off = (unsigned)slot % (unsigned)pg.block_size;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) top = max_nan(top, max_nan(fabsf(lo[e]), fabsf(hi[e])));
-  const unsigned group = ((1u << TPH) - 1u) << ((threadIdx.x & 31) / TPH * TPH);
+  for (int j = 0; j < PP_HEADS; ++j) {
+    const unsigned head = head0 + j;
+    if (head >= heads) break;
+    const bool is_q = head < nq, is_k = !is_q && head < nq + pg.n_kv_heads;
+    const unsigned h = head - (is_q ? 0u : is_k ? nq : nq + pg.n_kv_heads);
+    float lo[8], hi[8];
+    raw[j][0].get(lo);
+    raw[j][1].get(hi);
+    if (is_k && a.k_pairs) {
+      float x[8], y[8];
 #pragma unroll
-  for (int o = 1; o < TPH; o <<= 1) top = max_nan(top, __shfl_xor_sync(group, top, o));
-  const float scale = top == 0.f ? 0x1p-126f : __fdiv_rn(top, 448.f);
-  uint8_t *q8 = static_cast<uint8_t *>(dst);
-  *reinterpret_cast<uint2 *>(q8 + to) = codes8(lo, scale);
-  *reinterpret_cast<uint2 *>(q8 + to + HALF) = codes8(hi, scale);
-  if (i0 == 0) {
-    const int64_t *sst = what == 1 ? pg.k_scale_stride : pg.v_scale_stride;
-    (what == 1 ? pg.k_scale : pg.v_scale)[page * sst[0] + h * sst[1] + off * sst[2]] = scale;
+      for (int e = 0; e < 4; ++e) {
+        x[e] = lo[2 * e], y[e] = lo[2 * e + 1];
+        x[4 + e] = hi[2 * e], y[4 + e] = hi[2 * e + 1];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) lo[e] = x[e], hi[e] = y[e];
+    }
+    if (a.rope && (is_q || is_k)) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = lo[e], y = hi[e];
+        lo[e] = __fsub_rn(__fmul_rn(x, c[e]), __fmul_rn(y, s[e]));
+        hi[e] = __fadd_rn(__fmul_rn(y, c[e]), __fmul_rn(x, s[e]));
+      }
+    }
+    if (is_q) {
+      const int64_t to = row * a.q_out_stride[0] + h * a.q_out_stride[1] + i0;
+      store8<VEC>(a.q_out, to, X, lo);
+      store8<VEC>(a.q_out, to + HALF, X, hi);
+      continue;
+    }
+    const int64_t *cst = is_k ? pg.k_stride : pg.v_stride;
+    const int64_t to = page * cst[0] + h * cst[1] + off * cst[2] + i0;
+    void *dst = is_k ? pg.k : pg.v;
+    if (pg.dtype != KIE_E4M3) {
+      store8<true>(dst, to, pg.dtype, lo);
+      store8<true>(dst, to + HALF, pg.dtype, hi);
+      continue;
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max_nan(top, max_nan(fabsf(lo[e]), fabsf(hi[e])));
+    const unsigned lanes = ((1u << TPH) - 1u) << ((threadIdx.x & 31) / TPH * TPH);
+#pragma unroll
+    for (int o = 1; o < TPH; o <<= 1) top = max_nan(top, __shfl_xor_sync(lanes, top, o));
+    const float scale = top == 0.f ? 0x1p-126f : __fdiv_rn(top, 448.f), r = __frcp_rn(scale);
+    const bool fast = codes_fast(scale);
+    uint8_t *q8 = static_cast<uint8_t *>(dst);
+    *reinterpret_cast<uint2 *>(q8 + to) = codes8(lo, scale, r, fast);
+    *reinterpret_cast<uint2 *>(q8 + to + HALF) = codes8(hi, scale, r, fast);
+    if (i0 == 0) {
+      const int64_t *sst = is_k ? pg.k_scale_stride : pg.v_scale_stride;
+      (is_k ? pg.k_scale : pg.v_scale)[page * sst[0] + h * sst[1] + off * sst[2]] = scale;
+    }
   }
+}
+
+template <int DH, int X>
+void launch_append(const kie_paged_append_args &a, unsigned grid, bool vec, cudaStream_t s) {
+  if (vec)
+    paged_append_kernel<DH, X, true><<<grid, PP_THREADS, 0, s>>>(a);
+  else
+    paged_append_kernel<DH, X, false><<<grid, PP_THREADS, 0, s>>>(a);
 }
 
 // ---- checks of arguments ------------------------------------------------------------------------------------
@@ -325,7 +466,10 @@ int kie_paged_extend(const kie_paged_extend_args *p, void *stream) {
   if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
   const int grid = (int)std::min<int64_t>(sms, std::max<int64_t>(1, ((int64_t)a.n_rows + PX_THREADS - 1) / PX_THREADS));
   const int per = (int)(((int64_t)a.n_rows + grid - 1) / grid);
-  paged_extend_kernel<<<grid, PX_THREADS, 0, (cudaStream_t)stream>>>(a, per);
+  if (a.n_seqs <= PX_THREADS)
+    paged_extend_kernel<1><<<grid, PX_THREADS, 0, (cudaStream_t)stream>>>(a, per);
+  else
+    paged_extend_kernel<4><<<grid, PX_THREADS, 0, (cudaStream_t)stream>>>(a, per);
   return finish(cudaGetLastError(), "paged_extend");
 }
 
@@ -344,8 +488,11 @@ int kie_paged_release(const kie_paged_release_args *p, void *stream) {
     return refuse("lens_out and n_free_out must not be the inputs");
   int dev, sms;
   if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
-  const int grid = std::min(sms, std::max(1, (a.n_seqs + PX_THREADS / 32 - 1) / (PX_THREADS / 32)));
-  paged_release_kernel<<<grid, PX_THREADS, 0, (cudaStream_t)stream>>>(a);
+  const int teams = PX_THREADS / PX_TEAM, grid = std::min(sms, std::max(1, (a.n_seqs + teams - 1) / teams));
+  if (a.n_seqs <= PX_THREADS)
+    paged_release_kernel<1><<<grid, PX_THREADS, 0, (cudaStream_t)stream>>>(a);
+  else
+    paged_release_kernel<4><<<grid, PX_THREADS, 0, (cudaStream_t)stream>>>(a);
   return finish(cudaGetLastError(), "paged_release");
 }
 
@@ -362,24 +509,21 @@ int kie_paged_append(const kie_paged_append_args *p, void *stream) {
   if (a.rope && !aligned(a.rope, 16)) return refuse("the rope table must be 16-byte aligned");
   if (a.q && a.q_out == a.q && (a.q_stride[0] != a.q_out_stride[0] || a.q_stride[1] != a.q_out_stride[1]))
     return refuse("q_out in place of q needs q's strides");
-  const int64_t units = (int64_t)a.n_rows * ((a.q ? a.n_heads : 0) + 2ll * a.pages.n_kv_heads);
-  if (units > INT_MAX / 8) return refuse("too many rows x heads (2^28 at most)");
+  const int64_t heads = (a.q ? a.n_heads : 0) + 2ll * a.pages.n_kv_heads, groups = (heads + PP_HEADS - 1) / PP_HEADS;
+  if (a.n_rows * groups * PP_HEADS > 1ll << 28) return refuse("too many rows x heads (2^28 at most)");
   const int tph = a.pages.head_dim / 16;
-  const unsigned grid = (unsigned)((units * tph + PP_THREADS - 1) / PP_THREADS);
+  const int64_t warps = (a.n_rows + 32 / tph - 1) / (32 / tph) * groups;
+  const unsigned grid = (unsigned)((warps * 32 + PP_THREADS - 1) / PP_THREADS);
   const bool vec = aligned_rows(a.k, a.k_stride, a.x_dtype) && aligned_rows(a.v, a.v_stride, a.x_dtype) &&
                    (!a.q || (aligned_rows(a.q, a.q_stride, a.x_dtype) && aligned_rows(a.q_out, a.q_out_stride, a.x_dtype)));
   cudaStream_t s = (cudaStream_t)stream;
-  if (a.pages.head_dim == 64) {
-    if (vec)
-      paged_append_kernel<64, true><<<grid, PP_THREADS, 0, s>>>(a);
-    else
-      paged_append_kernel<64, false><<<grid, PP_THREADS, 0, s>>>(a);
-  } else {
-    if (vec)
-      paged_append_kernel<128, true><<<grid, PP_THREADS, 0, s>>>(a);
-    else
-      paged_append_kernel<128, false><<<grid, PP_THREADS, 0, s>>>(a);
-  }
+  const bool wide = a.pages.head_dim == 128;
+  if (a.x_dtype == KIE_F16)
+    wide ? launch_append<128, KIE_F16>(a, grid, vec, s) : launch_append<64, KIE_F16>(a, grid, vec, s);
+  else if (a.x_dtype == KIE_BF16)
+    wide ? launch_append<128, KIE_BF16>(a, grid, vec, s) : launch_append<64, KIE_BF16>(a, grid, vec, s);
+  else
+    wide ? launch_append<128, KIE_F32>(a, grid, vec, s) : launch_append<64, KIE_F32>(a, grid, vec, s);
   return finish(cudaGetLastError(), "paged_append");
 }
 

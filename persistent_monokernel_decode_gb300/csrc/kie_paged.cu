@@ -290,7 +290,7 @@ struct Eight {
 // evaluation gives the same bits, and with them the same E4M3 codes. Bound by HBM where there are many rows (each
 // element is read and written once), by a chain of two loads where there are few.
 template <int DH, int X, bool VEC>
-__global__ void __launch_bounds__(PP_THREADS) paged_append_kernel(const kie_paged_append_args a) {
+__global__ void __launch_bounds__(PP_THREADS, X == KIE_F32 ? 6 : 8) paged_append_kernel(const kie_paged_append_args a) {
   constexpr int TPH = DH / 16, HALF = DH / 2;
   const kie_pages &pg = a.pages;
   const unsigned nq = a.q ? a.n_heads : 0u, heads = nq + 2u * pg.n_kv_heads, groups = (heads + PP_HEADS - 1) / PP_HEADS;

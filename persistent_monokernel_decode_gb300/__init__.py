@@ -20,6 +20,7 @@ _CSRC = os.path.join(_HERE, "csrc")
 _INCLUDE = os.path.join(_ROOT, "include")
 _BUILD = os.path.join(_ROOT, "_build")
 LIB_PATH = os.path.join(_HERE, "libkie.so")
+BINDING_PATH, BINDING_SOURCE = os.path.join(_HERE, "_paged.so"), "kie_paged_py.cpp"
 SOURCES = ("kie_api.cu", "kie_decode.cu", "kie_gemv.cu", "kie_prefill.cu", "kie_paged.cu", "kie_paged_attn.cu")
 HEADERS = ("kie_layout.h", "kie_device.cuh", "kie_decode.cuh", "kie_prefill.cuh", "kie_tcgemm.cuh", "kie_tcattn.cuh",
            "kie_paged.cuh")
@@ -48,11 +49,25 @@ def link_cmd() -> list[str]:
     return [_nvcc(), *ARCH, "-shared", "-o", LIB_PATH, *[os.path.join(_BUILD, s + ".o") for s in SOURCES]]
 
 
+def binding_cmd() -> list[str]:
+    """The marshalling module of the paged-cache operators (host C++ against PyTorch's headers)."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc())) if os.path.isabs(_nvcc()) else "/usr/local/cuda"
+    include = (os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include"), _INCLUDE)
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f"-I{i}" for i in include], os.path.join(_CSRC, BINDING_SOURCE), "-o", BINDING_PATH,
+            f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
-    deps = [os.path.join(_CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(_INCLUDE, "kie.h")]
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
+    deps = [os.path.join(_CSRC, f) for f in SOURCES + HEADERS + (BINDING_SOURCE,)] + [os.path.join(_INCLUDE, "kie.h")]
     return any(os.path.getmtime(f) > t for f in deps)
 
 
@@ -74,15 +89,15 @@ def source_digest(files=DECODE_SOURCES) -> str:
 
 
 def build(force: bool = False) -> str:
-    """Compile libkie.so in-tree for sm_103a (the translation units in parallel, then link)."""
+    """Compile libkie.so in-tree for sm_103a (the translation units in parallel, then link), and the binding module."""
     if not force and not _stale():
         return LIB_PATH
     os.makedirs(_BUILD, exist_ok=True)
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
-        results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), compile_cmds()))
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), [binding_cmd()] + compile_cmds()))
     for r in results:
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
+            raise RuntimeError(f"{os.path.basename(r.args[0])} failed:\n" + r.stdout + r.stderr)
     r = subprocess.run(link_cmd(), capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("nvcc link failed:\n" + r.stdout + r.stderr)

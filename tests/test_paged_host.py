@@ -141,23 +141,6 @@ def test_workspace_of_bad_heads_is_zero(heads):
     assert kie.lib().kie_paged_attention_workspace(*heads) == 0
 
 
-@pytest.mark.parametrize("packed,fields", [("_EXTEND", kie.KiePagedExtendArgs), ("_RELEASE", kie.KiePagedReleaseArgs),
-                                           ("_APPEND", kie.KiePagedAppendArgs), ("_ATTENTION", kie.KiePagedAttentionArgs)])
-def test_packed_arguments_have_the_layout_of_the_structs(packed, fields):
-    """Numbering the packed fields 1, 2, ... and reading them back through the ctypes struct gives 1, 2, ... in order."""
-    from persistent_monokernel_decode_gb300 import paged
-    s = getattr(paged, packed)
-    assert s.size == ctypes.sizeof(fields)
-
-    def flat(x):
-        if isinstance(x, ctypes.Structure):
-            return [v for name, *_ in x._fields_ for v in flat(getattr(x, name))]
-        return [v for e in x for v in flat(e)] if isinstance(x, ctypes.Array) else [x]
-
-    n = len(flat(fields()))
-    assert flat(fields.from_buffer_copy(s.pack(*range(1, n + 1)))) == list(range(1, n + 1))
-
-
 def test_the_oracle_extends_by_hand():
     # bs 16; request 0: 15 + 1 (no page), 1: 16 + 1 (one), 2: 0 + 33 (three), 3: 5 + 0 (none)
     table = [[3, -1, -1], [4, -1, -1], [-1, -1, -1], [5, -1, -1]]

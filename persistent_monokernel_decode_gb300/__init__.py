@@ -60,7 +60,7 @@ def binding_cmd() -> list[str]:
                sysconfig.get_paths()["include"], os.path.join(cuda, "include"), _INCLUDE)
     return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *[f"-I{i}" for i in include], os.path.join(_CSRC, BINDING_SOURCE), "-o", BINDING_PATH,
-            f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+            f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
 
 
 def _stale() -> bool:

@@ -9,7 +9,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/DeviceGuard.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 
 #include <stdexcept>
@@ -136,7 +136,15 @@ kie_pages pages(const at::Tensor &k, const at::Tensor &v, PyObject *k_scale, PyO
 void *stream_of(const at::Device &dev) { return c10::cuda::getCurrentCUDAStream(dev.index()).stream(); }
 
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Device &dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  return at::Tensor(at::detail::empty_cuda(shape, at::TensorOptions().dtype(type).device(dev)));
+}
+
+// Elements [at, at + n) of a new buffer as a tensor of its own on the same storage.
+at::Tensor part(const at::Tensor &buffer, int64_t at, int64_t n) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buffer.storage()), buffer.key_set(), buffer.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return t;
 }
 
 PyObject *wrap(at::Tensor t) {
@@ -185,18 +193,19 @@ PyObject *extend(PyObject *const *x) {
   a.block_size = (int)integer(x[5], "block_size");
   a.free_capacity = size_of(free.numel(), "the length of free_blocks");
   const c10::DeviceGuard guard(dev);
-  at::Tensor lens_out = empty({R}, at::kInt, dev), n_free_out = empty({1}, at::kInt, dev), admitted = empty({R}, at::kBool, dev),
-             row_start = empty({R + 1}, at::kInt, dev), slots = empty({a.n_rows}, at::kInt, dev),
-             positions = empty({a.n_rows}, at::kInt, dev), seqs = empty({a.n_rows}, at::kInt, dev);
-  a.lens_out = static_cast<int32_t *>(lens_out.data_ptr());
-  a.n_free_out = static_cast<int32_t *>(n_free_out.data_ptr());
+  const at::Tensor admitted = empty({R}, at::kBool, dev), buffer = empty({2 * R + 2 + 3ll * a.n_rows}, at::kInt, dev);
+  const int64_t at[] = {0, R, R + 1, 2 * R + 2, 2 * R + 2 + a.n_rows, 2 * R + 2 + 2ll * a.n_rows};
+  int32_t *p = static_cast<int32_t *>(buffer.data_ptr());
   a.admitted = static_cast<uint8_t *>(admitted.data_ptr());
-  a.row_start = static_cast<int32_t *>(row_start.data_ptr());
-  a.slots = static_cast<int32_t *>(slots.data_ptr());
-  a.positions = static_cast<int32_t *>(positions.data_ptr());
-  a.seqs = static_cast<int32_t *>(seqs.data_ptr());
+  a.lens_out = p + at[0];
+  a.n_free_out = p + at[1];
+  a.row_start = p + at[2];
+  a.slots = p + at[3];
+  a.positions = p + at[4];
+  a.seqs = p + at[5];
   check(g_extend(&a, stream_of(dev)));
-  return wrap_all(lens_out, n_free_out, admitted, row_start, slots, positions, seqs);
+  return wrap_all(part(buffer, at[0], R), part(buffer, at[1], 1), admitted, part(buffer, at[2], R + 1),
+                  part(buffer, at[3], a.n_rows), part(buffer, at[4], a.n_rows), part(buffer, at[5], a.n_rows));
 }
 
 // release(done, lens, block_table, free_blocks, n_free, block_size)
@@ -220,11 +229,11 @@ PyObject *release(PyObject *const *x) {
   a.block_size = (int)integer(x[5], "block_size");
   a.free_capacity = size_of(free.numel(), "the length of free_blocks");
   const c10::DeviceGuard guard(dev);
-  at::Tensor lens_out = empty({R}, at::kInt, dev), n_free_out = empty({1}, at::kInt, dev);
-  a.lens_out = static_cast<int32_t *>(lens_out.data_ptr());
-  a.n_free_out = static_cast<int32_t *>(n_free_out.data_ptr());
+  const at::Tensor buffer = empty({R + 1}, at::kInt, dev);
+  a.lens_out = static_cast<int32_t *>(buffer.data_ptr());
+  a.n_free_out = a.lens_out + R;
   check(g_release(&a, stream_of(dev)));
-  return wrap_all(lens_out, n_free_out);
+  return wrap_all(part(buffer, 0, R), part(buffer, R, 1));
 }
 
 // append(k, v, k_cache, v_cache, slots, positions, rope, q, q_out, k_scale, v_scale, k_pairs)

@@ -28,8 +28,8 @@ namespace {
 
 constexpr int PA_WARPS = 4;
 constexpr int PA_THREADS = PA_WARPS * 32;
-constexpr int PA_BLOCKS_PER_SM = 2;
-constexpr int PA_RING_BYTES = 24 * 1024;    // a warp's ring: 4 warps x 2 blocks x 24 KB = 192 KB of an SM
+constexpr int PA_MAX_BLOCKS_PER_SM = 3;
+constexpr int PA_RING_BYTES = 192 * 1024;   // the rings of an SM's blocks
 constexpr int PA_ROWS = PAGED_MAX_GROUP;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // Weights are kept as 2^7 2^(v - ref): an fp16 pair holds them to 2^-25, which is 2^-32 of the largest.
@@ -45,7 +45,10 @@ struct PaTile {
   static constexpr int ES = KIND == PG_E4M3 ? 1 : 2, SUBS = KIND == PG_E4M3 ? 2 : 1;  // 16-position parts
   static constexpr int POS = 16 * SUBS, UNIT = POS * PA_WARPS;
   static constexpr int ROW = DH * ES, CH = ROW / 16, HALF = POS * ROW;  // bytes; 16-byte chunks of a row
-  static constexpr int NS = PA_RING_BYTES / HALF;                       // ring slots, a half each
+  // Blocks of an SM: a third helps where its 168 registers a thread are enough (256 x 4,096 positions, 16 heads over 4:
+  // 311 us against 316 with two); E4M3 needs more (191 against 186), and rows of 64 gain nothing (171 against 167).
+  static constexpr int BLOCKS = KIND != PG_E4M3 && DH == 128 ? 3 : 2;
+  static constexpr int NS = PA_RING_BYTES / BLOCKS / PA_WARPS / HALF;   // ring slots, a half each
   static constexpr int LOADS = HALF / 512;                              // chunks each lane copies
 };
 
@@ -181,9 +184,9 @@ struct Cursor {
   }
 };
 
-// ceil(a / b), with a 32-bit division where it does (a 64-bit one takes a few hundred cycles at the kernel's start).
-__device__ __forceinline__ long long div_up(long long a, unsigned b) {
-  return a < (1ll << 31) ? (long long)(((unsigned)a + b - 1) / b) : (a + b - 1) / b;
+// a / b, with a 32-bit division where it does (a 64-bit one takes a few hundred cycles).
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
 // The number of places of this block's run (*end; 0 behind the list's end), the cursor at its first unit, and the
@@ -216,7 +219,7 @@ __device__ __forceinline__ void locate(const kie_paged_attention_args &a, Cursor
   const int heads = a.pages.n_kv_heads;
   all *= heads;
   before *= heads;
-  *per_block = max(div_up(all, gridDim.x), (long long)PA_MIN_RUN);
+  *per_block = max(divide(all + gridDim.x - 1, gridDim.x), (long long)PA_MIN_RUN);
   const long long v0 = blockIdx.x * *per_block;
   *end = (int)max(0ll, min(*per_block, all - v0));
   if (v0 >= before && v0 < before + mine * heads) {
@@ -247,7 +250,7 @@ __device__ __forceinline__ void locate(const kie_paged_attention_args &a, Cursor
 
 // ---- workspace ----------------------------------------------------------------------------------------------
 
-// Per block: three arrival words, then four pieces: o [group][dh], then m and l [group] (rounded to 16 bytes). A block
+// Per block: three arrival words, then four pieces: o [group][dh], then (m, l) [group] (rounded to 16 bytes). A block
 // continues at most one item that an earlier block started and starts at most one that it does not end:
 //   word / piece CONT, START: the arrivals of the group of blocks that begins with this one, as a continuation or as
 //   the item's start; this block's piece of either.
@@ -280,11 +283,16 @@ __device__ __forceinline__ bool arrive(unsigned long long *word, unsigned long l
   if (n == 1) return true;
   unsigned long long seen = 0ull;  // what the last call left
   while ((seen >> 8) != call) {    // a failed exchange finds other data once, or another block's first arrival
-    const unsigned long long was = atomicCAS(word, seen, (call << 8) | 1ull);
+    unsigned long long was;
+    asm volatile("atom.acquire.gpu.global.cas.b64 %0, [%1], %2, %3;"
+                 : "=l"(was)
+                 : "l"(word), "l"(seen), "l"((call << 8) | 1ull)
+                 : "memory");
     if (was == seen) return false;
     seen = was;
   }
-  if ((int)(atomicAdd(word, 1ull) & 255ull) + 1 < n) return false;
+  asm volatile("atom.acquire.gpu.global.add.u64 %0, [%1], %2;" : "=l"(seen) : "l"(word), "l"(1ull) : "memory");
+  if ((int)(seen & 255ull) + 1 < n) return false;
   *word = 0ull;
   return true;
 }
@@ -294,9 +302,8 @@ __device__ __forceinline__ bool block_arrive(unsigned long long *word, unsigned 
   __shared__ bool s_last;
   __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();  // cumulative: over the writes of the block's threads, ordered before it by the barrier
+    __threadfence();  // release: cumulative over the writes of the block's threads, ordered before it by the barrier
     s_last = arrive(word, call, n);
-    __threadfence();
   }
   __syncthreads();
   const bool last = s_last;
@@ -316,7 +323,7 @@ struct JoinShare {
 template <int DH, class F, class P>
 __device__ __forceinline__ void join_pieces(const F &piece, int n, int group, const P &put) {
   using S = JoinShare<DH>;
-  constexpr int BATCH = 8, R = S::ROWS;
+  constexpr int R = S::ROWS, BATCH = 8 / R;
   const S me;
   float top[R], sum[R];
   float4 acc[R];
@@ -328,7 +335,7 @@ __device__ __forceinline__ void join_pieces(const F &piece, int n, int group, co
   }
   if (me.r0 >= group) return;
   for (int i0 = 0; i0 < n; i0 += BATCH) {
-    float m[BATCH][R], l[BATCH][R];
+    float2 ml[BATCH][R];
     float4 y[BATCH][R];
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
@@ -336,8 +343,7 @@ __device__ __forceinline__ void join_pieces(const F &piece, int n, int group, co
 #pragma unroll
       for (int q = 0; q < R; ++q) {
         const int r = min(me.r0 + q * S::STEP, group - 1);
-        m[k][q] = __ldcg(p + group * DH + r);
-        l[k][q] = __ldcg(p + group * (DH + 1) + r);
+        ml[k][q] = __ldcg(reinterpret_cast<const float2 *>(p + group * DH + 2 * r));
         y[k][q] = __ldcg(reinterpret_cast<const float4 *>(p + r * DH + me.d));
       }
     }
@@ -346,14 +352,14 @@ __device__ __forceinline__ void join_pieces(const F &piece, int n, int group, co
       float mn = top[q];
 #pragma unroll
       for (int k = 0; k < BATCH; ++k)
-        if (i0 + k < n) mn = fmaxf(mn, m[k][q]);
+        if (i0 + k < n) mn = fmaxf(mn, ml[k][q].x);
       const float ref = mn == -INFINITY ? 0.f : mn, f0 = ex2(top[q] - ref);
       sum[q] *= f0, acc[q].x *= f0, acc[q].y *= f0, acc[q].z *= f0, acc[q].w *= f0;
 #pragma unroll
       for (int k = 0; k < BATCH; ++k)
         if (i0 + k < n) {
-          const float f = ex2(m[k][q] - ref);
-          sum[q] = fmaf(l[k][q], f, sum[q]);
+          const float f = ex2(ml[k][q].x - ref);
+          sum[q] = fmaf(ml[k][q].y, f, sum[q]);
           acc[q].x = fmaf(y[k][q].x, f, acc[q].x), acc[q].y = fmaf(y[k][q].y, f, acc[q].y);
           acc[q].z = fmaf(y[k][q].z, f, acc[q].z), acc[q].w = fmaf(y[k][q].w, f, acc[q].w);
         }
@@ -391,10 +397,7 @@ __device__ __forceinline__ bool out_vec(const kie_paged_attention_args &a) {
 template <int DH>
 __device__ __forceinline__ void put_piece(float *p, int group, int r, int d, float4 acc, float M, float L) {
   *reinterpret_cast<float4 *>(p + r * DH + d) = acc;
-  if (d == 0) {
-    p[group * DH + r] = M;
-    p[group * (DH + 1) + r] = L;
-  }
+  if (d == 0) *reinterpret_cast<float2 *>(p + group * DH + 2 * r) = make_float2(M, L);
 }
 
 // After this block has written its piece of item (b, h), whose `units` units begin at place v of the list: whoever of
@@ -403,7 +406,7 @@ template <int DH>
 __device__ __forceinline__ void publish(const kie_paged_attention_args &a, unsigned long long call, int b, int h, long long v,
                                         int units, long long per_block) {
   const Workspace ws(a, DH);
-  const int first = (int)(v / per_block), last = (int)((v + units - 1) / per_block);
+  const int first = (int)divide(v, per_block), last = (int)divide(v + units - 1, per_block);
   const int group = a.n_heads / a.pages.n_kv_heads, n = last - first + 1;
   int fan = n;
   if (n > PA_ONE_LEVEL) {
@@ -469,7 +472,7 @@ __device__ __forceinline__ int join_col(int r, int d) {
 }
 
 template <int KIND, int DH, bool SPLIT>
-__global__ void __launch_bounds__(PA_THREADS, PA_BLOCKS_PER_SM)
+__global__ void __launch_bounds__(PA_THREADS, PaTile<KIND, DH>::BLOCKS)
 paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
   using T = PaTile<KIND, DH>;
   using Sm = PaSmem<KIND, DH>;
@@ -862,7 +865,7 @@ cudaError_t launch(const kie_paged_attention_args &a, int dev, int sms, cudaStre
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  paged_attn_kernel<KIND, DH, SPLIT><<<sms * PA_BLOCKS_PER_SM, PA_THREADS, smem, stream>>>(a, call_number());
+  paged_attn_kernel<KIND, DH, SPLIT><<<sms * PaTile<KIND, DH>::BLOCKS, PA_THREADS, smem, stream>>>(a, call_number());
   return cudaGetLastError();
 }
 
@@ -877,7 +880,7 @@ cudaError_t launch_dh(const kie_paged_attention_args &a, int dev, int sms, cudaS
 }  // namespace kie
 
 size_t kie_paged_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim, int sms) {
-  const size_t blocks = (size_t)sms * kie::PA_BLOCKS_PER_SM;
+  const size_t blocks = (size_t)sms * kie::PA_MAX_BLOCKS_PER_SM;
   return kie::pa_header_bytes(blocks) + blocks * kie::PA_PIECES * kie::pa_piece_floats(n_heads / n_kv_heads, head_dim) * 4;
 }
 

@@ -50,6 +50,7 @@ __device__ __forceinline__ int clamp_int(long long v) { return (int)(v > INT_MAX
 // PER requests to a thread: 1 up to 512 requests (each request's pages are then taken by a thread of its own), else 4.
 template <int PER>
 __global__ void __launch_bounds__(PX_THREADS) paged_extend_kernel(const kie_paged_extend_args a, int per) {
+  begin_after_previous();
   constexpr int CHUNK = PX_THREADS * PER;  // requests of a pass over the block
   __shared__ int s_end[CHUNK], s_first[CHUNK], s_start[CHUNK], s_len[CHUNK], s_have[CHUNK];  // s_have < 0: not admitted
   __shared__ int s_taken;  // pages given
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(PX_THREADS) paged_extend_kernel(const kie_page
 constexpr int PX_TEAM = 128;
 template <int PER>
 __global__ void __launch_bounds__(PX_THREADS) paged_release_kernel(const kie_paged_release_args a) {
+  begin_after_previous();
   constexpr int CHUNK = PX_THREADS * PER;  // requests of a pass over the block
   __shared__ long long s_first[CHUNK];
   __shared__ int s_pages[CHUNK];
@@ -291,6 +293,7 @@ struct Eight {
 // element is read and written once), by a chain of two loads where there are few.
 template <int DH, int X, bool VEC>
 __global__ void __launch_bounds__(PP_THREADS, X == KIE_F32 ? 6 : 8) paged_append_kernel(const kie_paged_append_args a) {
+  begin_after_previous();
   constexpr int TPH = DH / 16, HALF = DH / 2;
   const kie_pages &pg = a.pages;
   const unsigned nq = a.q ? a.n_heads : 0u, heads = nq + 2u * pg.n_kv_heads, groups = (heads + PP_HEADS - 1) / PP_HEADS;
@@ -387,11 +390,9 @@ __global__ void __launch_bounds__(PP_THREADS, X == KIE_F32 ? 6 : 8) paged_append
 }
 
 template <int DH, int X>
-void launch_append(const kie_paged_append_args &a, unsigned grid, bool vec, cudaStream_t s) {
-  if (vec)
-    paged_append_kernel<DH, X, true><<<grid, PP_THREADS, 0, s>>>(a);
-  else
-    paged_append_kernel<DH, X, false><<<grid, PP_THREADS, 0, s>>>(a);
+cudaError_t launch_append(const kie_paged_append_args &a, unsigned grid, bool vec, cudaStream_t s) {
+  auto *kernel = vec ? paged_append_kernel<DH, X, true> : paged_append_kernel<DH, X, false>;
+  return launch_after_previous(kernel, grid, PP_THREADS, 0, s, a);
 }
 
 // ---- checks of arguments ------------------------------------------------------------------------------------
@@ -466,11 +467,8 @@ int kie_paged_extend(const kie_paged_extend_args *p, void *stream) {
   if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
   const int grid = (int)std::min<int64_t>(sms, std::max<int64_t>(1, ((int64_t)a.n_rows + PX_THREADS - 1) / PX_THREADS));
   const int per = (int)(((int64_t)a.n_rows + grid - 1) / grid);
-  if (a.n_seqs <= PX_THREADS)
-    paged_extend_kernel<1><<<grid, PX_THREADS, 0, (cudaStream_t)stream>>>(a, per);
-  else
-    paged_extend_kernel<4><<<grid, PX_THREADS, 0, (cudaStream_t)stream>>>(a, per);
-  return finish(cudaGetLastError(), "paged_extend");
+  auto *kernel = a.n_seqs <= PX_THREADS ? paged_extend_kernel<1> : paged_extend_kernel<4>;
+  return finish(launch_after_previous(kernel, grid, PX_THREADS, 0, (cudaStream_t)stream, a, per), "paged_extend");
 }
 
 int kie_paged_release(const kie_paged_release_args *p, void *stream) {
@@ -489,11 +487,8 @@ int kie_paged_release(const kie_paged_release_args *p, void *stream) {
   int dev, sms;
   if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
   const int teams = PX_THREADS / PX_TEAM, grid = std::min(sms, std::max(1, (a.n_seqs + teams - 1) / teams));
-  if (a.n_seqs <= PX_THREADS)
-    paged_release_kernel<1><<<grid, PX_THREADS, 0, (cudaStream_t)stream>>>(a);
-  else
-    paged_release_kernel<4><<<grid, PX_THREADS, 0, (cudaStream_t)stream>>>(a);
-  return finish(cudaGetLastError(), "paged_release");
+  auto *kernel = a.n_seqs <= PX_THREADS ? paged_release_kernel<1> : paged_release_kernel<4>;
+  return finish(launch_after_previous(kernel, grid, PX_THREADS, 0, (cudaStream_t)stream, a), "paged_release");
 }
 
 int kie_paged_append(const kie_paged_append_args *p, void *stream) {
@@ -518,13 +513,14 @@ int kie_paged_append(const kie_paged_append_args *p, void *stream) {
                    (!a.q || (aligned_rows(a.q, a.q_stride, a.x_dtype) && aligned_rows(a.q_out, a.q_out_stride, a.x_dtype)));
   cudaStream_t s = (cudaStream_t)stream;
   const bool wide = a.pages.head_dim == 128;
+  cudaError_t e;
   if (a.x_dtype == KIE_F16)
-    wide ? launch_append<128, KIE_F16>(a, grid, vec, s) : launch_append<64, KIE_F16>(a, grid, vec, s);
+    e = wide ? launch_append<128, KIE_F16>(a, grid, vec, s) : launch_append<64, KIE_F16>(a, grid, vec, s);
   else if (a.x_dtype == KIE_BF16)
-    wide ? launch_append<128, KIE_BF16>(a, grid, vec, s) : launch_append<64, KIE_BF16>(a, grid, vec, s);
+    e = wide ? launch_append<128, KIE_BF16>(a, grid, vec, s) : launch_append<64, KIE_BF16>(a, grid, vec, s);
   else
-    wide ? launch_append<128, KIE_F32>(a, grid, vec, s) : launch_append<64, KIE_F32>(a, grid, vec, s);
-  return finish(cudaGetLastError(), "paged_append");
+    e = wide ? launch_append<128, KIE_F32>(a, grid, vec, s) : launch_append<64, KIE_F32>(a, grid, vec, s);
+  return finish(e, "paged_append");
 }
 
 size_t kie_paged_attention_workspace(int n_heads, int n_kv_heads, int head_dim) {

@@ -86,6 +86,32 @@ __device__ __forceinline__ void store8(void *p, int64_t i, int dtype, const floa
       make_uint4(pack2(v[0], v[1], dtype), pack2(v[2], v[3], dtype), pack2(v[4], v[5], dtype), pack2(v[6], v[7], dtype));
 }
 
+// The short paged-cache kernels are launched so that their blocks may take their places while the kernel before them on
+// the stream (one of them, as a rule: each of a step's operators needs the one before) still ends. The first thing a
+// block does is to wait, on the device, until everything before it is complete and visible; then it lets the next one
+// in. It saves about 0.4 us of each (extend of 256 requests 3.8 -> 3.4 us, append of 32 rows 2.4 -> 2.0 us). The
+// attention is launched plainly: its blocks would crowd on the SMs that were free first (64 sequences of 64 positions:
+// 8.0 us instead of 7.2).
+__device__ __forceinline__ void begin_after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <class K, class... A>
+cudaError_t launch_after_previous(K kernel, unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace kie
 
 cudaError_t kie_launch_paged_attention(const kie_paged_attention_args &a, int dev, int sms, cudaStream_t stream);

@@ -364,7 +364,8 @@ int kie_paged_append(const kie_paged_append_args *a, void *stream);
  * left out. Rows behind a sequence's end are never read. q, out: q_dtype, strides {sequence, head} in elements,
  * head_dim contiguous; lse [n_seqs][n_heads]. q_dtype is KIE_F32 (F16 and E4M3 pages), or the pages' own 16-bit
  * type, or either 16-bit type for E4M3 pages. Sums and the softmax are fp32; fp32 queries and the weights p go
- * through the tensor cores as two 16-bit parts.
+ * through the tensor cores as two 16-bit parts (E4M3 value rows whose scale is below 2^-60 with fewer bits).
+ * n_seqs * max_blocks * block_size * n_kv_heads must not pass 2^45. out may be q, with the same strides.
  * workspace: kie_paged_attention_workspace bytes, 256-byte aligned, contents arbitrary before and after; calls that
  * may overlap need one each. */
 typedef struct {

@@ -5,6 +5,7 @@
 #include <stdlib.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "kie_device.cuh"
 #include "kie_paged.cuh"
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(PX_THREADS) paged_extend_kernel(const kie_page
     for (int i = 0; i < PER; ++i) {
       const bool sane = len[i] >= 0 && nw[i] >= 0;
       const long long sum = (long long)len[i] + nw[i];
-      have[i] = sane && sum <= cap ? (int)((unsigned)(len[i] + bs - 1) / (unsigned)bs) : -1;  // -1: no room in the table
+      have[i] = sane && sum <= cap ? (int)(((unsigned)len[i] + bs - 1) / (unsigned)bs) : -1;  // -1: no room in the table
       need[i] = have[i] >= 0 ? (int)((unsigned)(sum + bs - 1) / (unsigned)bs) - have[i] : 0;
       v += sane ? nw[i] : 0;
       w += need[i];
@@ -122,16 +123,17 @@ __global__ void __launch_bounds__(PX_THREADS) paged_extend_kernel(const kie_page
         }
       }
       const bool ok = s_have[x] >= 0;
-      const int pos = s_len[x] + (int)(t - s_start[x]);
-      int slot = -1;
+      const int pos = ok ? s_len[x] + (int)(t - s_start[x]) : -1;
+      long long slot = -1;
       if (ok) {
         const int j = (int)((unsigned)pos / (unsigned)bs);
         const int page = j < s_have[x] ? a.block_table[(r0 + x) * a.table_stride + j]
                                        : a.free_blocks[n_free - 1 - ((long long)s_first[x] + j - s_have[x])];
-        slot = page * bs + pos - j * bs;
+        slot = (long long)page * bs + pos - j * bs;
+        if (slot > INT_MAX) slot = -1;  // no page of a cache: the append would have to find its slot out of range
       }
-      a.slots[t] = slot;
-      a.positions[t] = ok ? pos : -1;
+      a.slots[t] = (int)max(slot, -1ll);
+      a.positions[t] = pos;
       a.seqs[t] = ok ? r0 + x : -1;
     }
     __syncthreads();
@@ -429,6 +431,12 @@ const char *check_pages(const kie_pages &p) {
   return nullptr;
 }
 
+bool ints_aligned(std::initializer_list<const void *> arrays) {
+  for (const void *p : arrays)
+    if (!aligned(p, 4)) return false;
+  return true;
+}
+
 bool activation(int dtype) { return dtype == KIE_F16 || dtype == KIE_BF16 || dtype == KIE_F32; }
 
 bool aligned_rows(const void *p, const int64_t (&stride)[2], int dtype) {
@@ -461,6 +469,9 @@ int kie_paged_extend(const kie_paged_extend_args *p, void *stream) {
   if (a.n_rows > 0 && (!a.slots || !a.positions || !a.seqs)) return refuse("an array of the rows is NULL");
   if (a.free_capacity > 0 && !a.free_blocks) return refuse("free_blocks is NULL");
   if (a.n_seqs > 1 && a.table_stride < a.max_blocks) return refuse("table_stride is below max_blocks");
+  if (!ints_aligned({a.lens, a.new_lens, a.free_blocks, a.n_free, a.block_table, a.lens_out, a.n_free_out, a.row_start, a.slots,
+                     a.positions, a.seqs}))
+    return refuse("an int32 array is not 4-byte aligned");
   if (a.n_free_out == a.n_free || (a.n_seqs > 0 && (a.lens_out == a.lens || a.lens_out == a.new_lens)))
     return refuse("lens_out and n_free_out must not be the inputs");
   int dev, sms;
@@ -482,6 +493,8 @@ int kie_paged_release(const kie_paged_release_args *p, void *stream) {
   if (a.n_seqs > 0 && (!a.lens || !a.done || !a.block_table || !a.lens_out)) return refuse("an array of the requests is NULL");
   if (a.free_capacity > 0 && !a.free_blocks) return refuse("free_blocks is NULL");
   if (a.n_seqs > 1 && a.table_stride < a.max_blocks) return refuse("table_stride is below max_blocks");
+  if (!ints_aligned({a.lens, a.n_free, a.block_table, a.free_blocks, a.lens_out, a.n_free_out}))
+    return refuse("an int32 array is not 4-byte aligned");
   if (a.n_free_out == a.n_free || (a.n_seqs > 0 && a.lens_out == a.lens))
     return refuse("lens_out and n_free_out must not be the inputs");
   int dev, sms;
@@ -502,6 +515,9 @@ int kie_paged_append(const kie_paged_append_args *p, void *stream) {
   if (!a.k || !a.v || !a.slots) return refuse("k, v or slots is NULL");
   if (a.rope && (!a.positions || a.n_pos < 1)) return refuse("a rope table needs positions and n_pos >= 1");
   if (a.rope && !aligned(a.rope, 16)) return refuse("the rope table must be 16-byte aligned");
+  if (!ints_aligned({a.slots, a.positions})) return refuse("an int32 array is not 4-byte aligned");
+  for (const void *x : {a.k, a.v, a.q, (const void *)a.q_out})
+    if (!aligned(x, paged_dtype_bytes(a.x_dtype))) return refuse("k, v, q or q_out is not aligned to its elements");
   if (a.q && a.q_out == a.q && (a.q_stride[0] != a.q_out_stride[0] || a.q_stride[1] != a.q_out_stride[1]))
     return refuse("q_out in place of q needs q's strides");
   const int64_t heads = (a.q ? a.n_heads : 0) + 2ll * a.pages.n_kv_heads, groups = (heads + PP_HEADS - 1) / PP_HEADS;
@@ -547,6 +563,11 @@ int kie_paged_attention(const kie_paged_attention_args *p, void *stream) {
   if (a.n_seqs == 0) return KIE_OK;
   if (!a.q || !a.out || !a.block_table || !a.lens) return refuse("q, out, block_table or lens is NULL");
   if (a.n_seqs > 1 && a.table_stride < a.max_blocks) return refuse("table_stride is below max_blocks");
+  if (!ints_aligned({a.block_table, a.lens, a.lse})) return refuse("block_table, lens or lse is not 4-byte aligned");
+  if (!aligned(a.q, paged_dtype_bytes(a.q_dtype)) || !aligned(a.out, paged_dtype_bytes(a.q_dtype)))
+    return refuse("q or out is not aligned to its elements");
+  if ((double)a.n_seqs * a.max_blocks * a.pages.block_size * a.pages.n_kv_heads > 0x1p45)
+    return refuse("n_seqs * max_blocks * block_size * n_kv_heads must not pass 2^45");
   int dev, sms;
   if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
   const size_t need = kie_paged_attention_workspace_bytes(a.n_heads, a.pages.n_kv_heads, a.pages.head_dim, sms);

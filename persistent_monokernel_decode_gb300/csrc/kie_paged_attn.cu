@@ -166,7 +166,7 @@ __device__ __forceinline__ Span span_of(const kie_paged_attention_args &a, int b
 
 // Places in the list are numbered through, an item taking PA_ITEM_COST places before those of its units: starting an
 // item (its queries, the join of the warps, the output) takes a block about as long as that many units.
-constexpr int PA_ITEM_COST = 2, PA_MIN_RUN = 4;
+constexpr int PA_ITEM_COST = 2, PA_MIN_RUN = 3;  // and a block takes at least one unit of an item that it starts
 
 // Unit `unit` of item (b, h), at place v of this block's run.
 template <int UNIT>

@@ -33,7 +33,11 @@ def _native():
     if _ready is None:
         _torch()
         L = lib()
-        from . import _paged
+        try:
+            from . import _paged
+        except ImportError as e:
+            raise RuntimeError("the paged operators' binding is missing: run __graft_entry__.build() (or "
+                               "persistent_monokernel_decode_gb300.build()) first") from e
         _paged.bind(*[ctypes.cast(getattr(L, "kie_paged_" + n), ctypes.c_void_p).value
                       for n in ("extend", "release", "append", "attention", "attention_workspace", "last_error")], KieError)
         _ready = _paged
@@ -130,8 +134,8 @@ class PagedCache:
 
     def load(self, decoder, step: PagedStep, first_row: int = 0) -> None:
         """Copy the prompt that `decoder` (a Decoder of this model) has prefilled, positions 0 .. position - 1 of
-        every layer, to the slots of rows first_row .. of a step that extended a sequence by that many tokens. Waits
-        for the decoder's stream."""
+        every layer, to the slots of rows first_row .. of a step that extended a sequence by that many tokens.
+        Synchronous, like the prefill."""
         torch = _torch()
         n, m, d = decoder.position, self.model, decoder
         decoder.sync()
@@ -142,3 +146,4 @@ class PagedCache:
             raise ValueError("the step has too few rows for the decoder's prompt")
         for l in range(m.n_layers):
             paged_append(kv[l, 0], kv[l, 1], slots=slots, k_pairs=True, **self._layer(l))
+        torch.cuda.current_stream(self.device).synchronize()  # the decoder may go on, on whatever stream it has

@@ -60,7 +60,8 @@ def attention(q, k, v, table, lens, scale, window=0, k_scale=None, v_scale=None)
     count = []
     for b in range(B):
         L = min(max(int(lens[b]), 0), table.shape[1] * bs)
-        at = [p for p in range(max(0, L - window) if window else 0, L) if 0 <= int(table[b, p // bs]) < nb]
+        row = table[b].tolist()
+        at = [p for p in range(max(0, L - window) if window else 0, L) if 0 <= row[p // bs] < nb]
         count.append(len(at))
         if not at:
             continue

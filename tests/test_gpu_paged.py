@@ -417,6 +417,81 @@ def test_a_captured_step_follows_its_inputs():
     assert n_free.tolist() == [40 - 5 * 2]
 
 
+def raw_attention(q, k, v, table, lens, workspace):
+    """The C entry point itself, with a workspace of the caller's."""
+    import ctypes
+    out = torch.empty_like(q)
+    a = kie.KiePagedAttentionArgs(q=q.data_ptr(), out=out.data_ptr(), block_table=table.data_ptr(), lens=lens.data_ptr(),
+                                  table_stride=table.stride(0), workspace=workspace.data_ptr(),
+                                  workspace_bytes=workspace.numel(), scale=q.shape[-1] ** -0.5, n_seqs=q.shape[0],
+                                  n_heads=q.shape[1], max_blocks=table.shape[1], q_dtype={F16: 0, BF16: 1, F32: 2}[q.dtype])
+    a.q_stride[:], a.out_stride[:] = q.stride()[:2], out.stride()[:2]
+    p = a.pages
+    p.k, p.v, p.dtype = k.data_ptr(), v.data_ptr(), {F16: 0, BF16: 1}[k.dtype]
+    p.k_stride[:], p.v_stride[:] = k.stride()[:3], v.stride()[:3]
+    p.n_blocks, p.n_kv_heads, p.block_size, p.head_dim = k.shape
+    rc = kie.lib().kie_paged_attention(ctypes.byref(a), torch.cuda.current_stream().cuda_stream)
+    assert rc == 0, kie.lib().kie_paged_last_error()
+    return out
+
+
+@pytest.mark.parametrize("qt", [F16, F32])
+def test_the_workspace_may_hold_anything(qt):
+    """Zeros, ones, noise, and what another batch's call left: the results are the same bits."""
+    a, b = (batch(l, 20, 4, 128, 16, F16, qt, seed=i) for i, l in enumerate(([9000, 3, 700], [2000, 2500, 64, 1, 3000])))
+    want = [kie.paged_attention(*x[:5]) for x in (a, b)]
+    size = kie.lib().kie_paged_attention_workspace(20, 4, 128)
+    noise = torch.randint(0, 256, (size,), device="cuda", dtype=torch.uint8, generator=gen(5))
+    counts = torch.randint(0, 30, (size // 8,), device="cuda", generator=gen(6)).view(torch.uint8)  # small whole numbers
+    for fill in (torch.zeros_like(noise), torch.full_like(noise, 255), noise, counts):
+        ws = fill.clone() if fill.numel() == size else torch.cat([fill, fill[:size - fill.numel()]])
+        for _ in range(3):
+            assert torch.equal(raw_attention(*a[:5], ws), want[0])
+            assert torch.equal(raw_attention(*b[:5], ws), want[1])
+
+
+@pytest.mark.parametrize("cache,qt", [(F16, F32), (F16, F16), (E4M3, F16)])
+def test_attention_of_one_long_sequence(cache, qt):
+    """Pieces of one item on more blocks than are joined at once."""
+    check_attention(*batch([40007], 8, 1, 128, 64, cache, qt, seed=2))
+
+
+@pytest.mark.parametrize("n", [700, 5000])
+def test_attention_of_many_short_sequences(n):
+    lens = np.random.RandomState(n).randint(0, 4, n).tolist()
+    check_attention(*batch(lens, 4, 2, 64, 16, F16, F16, seed=n))
+
+
+def test_attention_of_random_batches():
+    rng = np.random.RandomState(1)
+    for i in range(12):
+        lens = np.exp(rng.uniform(0, np.log(4000), rng.randint(1, 12))).astype(int).tolist()
+        cache, qt = TYPES[i % len(TYPES)]
+        hq, hkv, dh = HEADS[rng.randint(len(HEADS))]
+        check_attention(*batch(lens, hq, hkv, dh, int(rng.choice([16, 32, 80, 256])), cache, qt, seed=i))
+
+
+def test_attention_in_place_of_the_query():
+    q, k, v, table, lens, ks, vs = batch([3000, 20, 700, 0], 20, 4, 128, 16, F16, F16)
+    want = kie.paged_attention(q, k, v, table, lens)
+    assert kie.paged_attention(q, k, v, table, lens, out=q) is q
+    assert torch.equal(q, want)
+
+
+def test_a_replayed_graph_follows_the_lengths():
+    """One captured call replayed with other lengths each time, so that other blocks share other items."""
+    q, k, v, table, lens, ks, vs = batch([4000, 4000, 4000], 20, 4, 128, 16, F16, F32)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = kie.paged_attention(q, k, v, table, lens)
+    rng = np.random.RandomState(3)
+    for _ in range(15):
+        lens.copy_(ints(rng.randint(0, 4001, 3).tolist()))
+        want = kie.paged_attention(q, k, v, table, lens)
+        g.replay()
+        assert torch.equal(out, want)
+
+
 # ---- refusals of the binding ---------------------------------------------------------------------------------
 
 def test_the_binding_refuses():
@@ -515,3 +590,30 @@ def test_a_batched_decode_matches_the_decoder():
     run(5)
     for d in decs:
         d.close()
+
+
+def test_load_from_a_decoder_on_another_stream():
+    """The pages hold the prompt although the decoder, on its own stream, takes another one right after."""
+    import synth
+    from synth.configs import TINY as M
+    dec = kie.Decoder(M, synth.model_weights(M), max_seq=64, stream=torch.cuda.Stream())
+    cache = kie.PagedCache(M, n_blocks=8, block_size=16, max_seqs=2, max_blocks=4)
+    got = []
+    for s in (21, 22):
+        dec.reset()
+        dec.prefill(synth.tokens(s, 50, M.vocab))
+        kv = dec._kvbuf.view(F16)[:2 * M.n_layers * M.n_kv_heads * 64 * M.head_dim].view(M.n_layers, 2, M.n_kv_heads, 64, -1)
+        got.append(kv[:, :, :, :50].clone())
+        step = cache.extend(ints([50, 0] if s == 21 else [0, 50]), 50)
+        cache.load(dec, step)
+    for b in range(2):
+        at = torch.arange(50, device="cuda")
+        page = cache.block_table[b].long()[at // 16]
+        half = M.head_dim // 2
+        for l in range(M.n_layers):
+            k, v = (x[l][page, :, at % 16].transpose(0, 1) for x in (cache.k, cache.v))
+            assert torch.equal(v, got[b][l, 1])
+            assert torch.equal(k[..., :half], got[b][l, 0][..., 0::2]) and torch.equal(k[..., half:], got[b][l, 0][..., 1::2])
+    with pytest.raises(ValueError):
+        cache.load(dec, step, first_row=1)
+    dec.close()

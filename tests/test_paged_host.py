@@ -43,14 +43,14 @@ def extend_args(**change):
     (dict(block_size=0), "block_size"), (dict(block_size=24), "block_size"), (dict(max_blocks=1 << 27), "2^31"),
     (dict(n_free=None), "n_free"), (dict(lens=None), "requests"), (dict(slots=None), "rows"),
     (dict(free_blocks=None), "free_blocks"), (dict(table_stride=3), "table_stride"), (dict(lens_out=SOME), "must not"),
-    (dict(n_free_out=SOME), "must not"), (dict(free_capacity=-1), "free_capacity")])
+    (dict(n_free_out=SOME), "must not"), (dict(free_capacity=-1), "free_capacity"), (dict(slots=SOME + 2), "aligned")])
 def test_extend_refuses(change, word):
     refused("kie_paged_extend", extend_args(**change), word)
 
 
 @pytest.mark.parametrize("change,word", [
     (dict(n_seqs=-1), "n_seqs"), (dict(block_size=8), "block_size"), (dict(done=None), "requests"),
-    (dict(n_free_out=SOME), "must not"), (dict(lens_out=SOME), "must not"), (dict(table_stride=1), "table_stride")])
+    (dict(n_free_out=SOME), "must not"), (dict(lens_out=SOME), "must not"), (dict(table_stride=1), "table_stride"), (dict(block_table=SOME + 1), "aligned")])
 def test_release_refuses(change, word):
     a = kie.KiePagedReleaseArgs(SOME, SOME, SOME, SOME, 4, SOME, SOME + 64, SOME + 128, 3, 4, 16, 8)
     for k, v in change.items():
@@ -92,7 +92,8 @@ def test_page_strides_and_scales_are_checked(fn):
 @pytest.mark.parametrize("change,word", [
     (dict(n_rows=-1), "n_rows"), (dict(x_dtype=3), "KIE_F32"), (dict(q_out=None), "q_out"), (dict(n_heads=0), "n_heads"),
     (dict(slots=None), "slots"), (dict(positions=None), "positions"), (dict(n_pos=0), "n_pos"),
-    (dict(rope=SOME + 4), "aligned"), (dict(n_rows=1 << 27), "2^28")])
+    (dict(rope=SOME + 4), "aligned"), (dict(n_rows=1 << 27), "2^28"), (dict(slots=SOME + 2), "aligned"),
+    (dict(k=SOME + 1), "aligned")])
 def test_append_refuses(change, word):
     a = append_args()
     for k, v in change.items():
@@ -116,7 +117,8 @@ def attention_args(dtype=0):
     (dict(max_blocks=1 << 27), "2^30"), (dict(n_heads=3), "multiple"), (dict(n_heads=18), "more than 8"),
     (dict(q_dtype=3), "KIE_F32"), (dict(q_dtype=1), "F16 pages"), (dict(scale=float("nan")), "finite"),
     (dict(scale=float("inf")), "finite"), (dict(q=None), "NULL"), (dict(lens=None), "NULL"),
-    (dict(table_stride=3), "table_stride"), (dict(n_seqs=1 << 30), "2^31")])
+    (dict(table_stride=3), "table_stride"), (dict(n_seqs=1 << 30), "2^31"), (dict(lens=SOME + 2), "aligned"),
+    (dict(out=SOME + 1), "aligned"), (dict(n_seqs=1 << 20, max_blocks=1 << 26, table_stride=1 << 26), "2^45")])
 def test_attention_refuses(change, word):
     a = attention_args()
     for k, v in change.items():

@@ -290,7 +290,7 @@ enum { KIE_F16 = 0, KIE_BF16 = 1, KIE_F32 = 2, KIE_E4M3 = 3 };
 
 /* The pages of one layer. k and v: element (page, kv head, position in the page, i) at page * stride[0] +
  * head * stride[1] + position * stride[2] + i, strides in elements, each a multiple of 16 bytes, as are the
- * addresses, and stride[2] below 2^26. dtype KIE_F16, KIE_BF16 or KIE_E4M3. E4M3 codes (OCP "fn") have one fp32 scale per row, at
+ * addresses; they are not negative and below 2^31, stride[2] below 2^26. dtype KIE_F16, KIE_BF16 or KIE_E4M3. E4M3 codes (OCP "fn") have one fp32 scale per row, at
  * k_scale / v_scale [page * scale_stride[0] + head * scale_stride[1] + position * scale_stride[2]], the value being
  * code * scale, as in the FP8 experts' rows above; else the scales are not read (may be NULL). head_dim 64 or 128;
  * block_size a multiple of 16; n_blocks * block_size < 2^31. */

@@ -2,7 +2,6 @@
 // points with their argument checks (kie_paged_attn.cu holds the attention).
 #include <limits.h>
 #include <stdio.h>
-#include <stdlib.h>
 
 #include <algorithm>
 #include <initializer_list>
@@ -152,12 +151,13 @@ __global__ void __launch_bounds__(PX_THREADS) paged_extend_kernel(const kie_page
 }
 
 // Every block scans the page counts of all finished requests and copies the pages of its share, the requests
-// r = blockIdx.x (mod grid), PX_TEAM threads to each. Bound by latency like the above.
-constexpr int PX_TEAM = 128;
+// r = blockIdx.x (mod grid), a team of threads to each: 128 up to 512 requests (few, whose pages may be many), else a
+// warp. Bound by latency like the above.
+__host__ __device__ constexpr int px_team(int per) { return per == 1 ? 128 : 32; }
 template <int PER>
 __global__ void __launch_bounds__(PX_THREADS) paged_release_kernel(const kie_paged_release_args a) {
   begin_after_previous();
-  constexpr int CHUNK = PX_THREADS * PER;  // requests of a pass over the block
+  constexpr int CHUNK = PX_THREADS * PER, PX_TEAM = px_team(PER);  // requests of a pass over the block
   __shared__ long long s_first[CHUNK];
   __shared__ int s_pages[CHUNK];
   const int tid = threadIdx.x, bs = a.block_size;
@@ -414,6 +414,10 @@ int finish(cudaError_t e, const char *what) {
 
 bool aligned(const void *p, size_t n) { return (uintptr_t)p % n == 0; }
 
+bool strides_fit(const int64_t (&st)[3], int64_t most_of_positions) {
+  return st[0] >= 0 && st[0] < 1ll << 31 && st[1] >= 0 && st[1] < 1ll << 31 && st[2] >= 0 && st[2] < most_of_positions;
+}
+
 const char *check_pages(const kie_pages &p) {
   if (p.n_blocks < 1 || p.n_kv_heads < 1) return "the pages need n_blocks >= 1 and n_kv_heads >= 1";
   if (p.head_dim != 64 && p.head_dim != 128) return "head_dim must be 64 or 128";
@@ -425,8 +429,11 @@ const char *check_pages(const kie_pages &p) {
   const int unit = 16 / paged_dtype_bytes(p.dtype);
   for (int i = 0; i < 3; ++i)
     if (p.k_stride[i] % unit || p.v_stride[i] % unit) return "the pages' strides must be multiples of 16 bytes";
-  if (llabs(p.k_stride[2]) >= 1 << 26 || llabs(p.v_stride[2]) >= 1 << 26) return "the strides of positions must be below 2^26";
+  for (const auto *st : {&p.k_stride, &p.v_stride})
+    if (!strides_fit(*st, 1ll << 26)) return "strides must be from 0 to below 2^31, those of positions below 2^26";
   if (p.dtype == KIE_E4M3 && (!p.k_scale || !p.v_scale)) return "E4M3 pages need k_scale and v_scale";
+  if (p.dtype == KIE_E4M3 && (!strides_fit(p.k_scale_stride, 1ll << 31) || !strides_fit(p.v_scale_stride, 1ll << 31)))
+    return "the scales' strides must be from 0 to below 2^31";
   if (p.dtype == KIE_E4M3 && (!aligned(p.k_scale, 4) || !aligned(p.v_scale, 4))) return "scales must be 4-byte aligned";
   return nullptr;
 }
@@ -499,7 +506,7 @@ int kie_paged_release(const kie_paged_release_args *p, void *stream) {
     return refuse("lens_out and n_free_out must not be the inputs");
   int dev, sms;
   if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
-  const int teams = PX_THREADS / PX_TEAM, grid = std::min(sms, std::max(1, (a.n_seqs + teams - 1) / teams));
+  const int teams = PX_THREADS / px_team(a.n_seqs <= PX_THREADS ? 1 : 4), grid = std::min(sms, std::max(1, (a.n_seqs + teams - 1) / teams));
   auto *kernel = a.n_seqs <= PX_THREADS ? paged_release_kernel<1> : paged_release_kernel<4>;
   return finish(launch_after_previous(kernel, grid, PX_THREADS, 0, (cudaStream_t)stream, a), "paged_release");
 }

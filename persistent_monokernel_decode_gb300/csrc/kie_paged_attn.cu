@@ -166,7 +166,10 @@ __device__ __forceinline__ Span span_of(const kie_paged_attention_args &a, int b
 
 // Places in the list are numbered through, an item taking PA_ITEM_COST places before those of its units: starting an
 // item (its queries, the join of the warps, the output) takes a block about as long as that many units.
-constexpr int PA_ITEM_COST = 2, PA_MIN_RUN = 3;  // and a block takes at least one unit of an item that it starts
+// A run is at least PA_MIN_RUN places, or a whole item where items are short (PA_WHOLE places on average at most): to
+// share an item costs about 2 us in the end, which is worth four units. (One sequence of 128 positions: 7.3 us whole,
+// 8.3 us shared by two blocks. One of 1,152: 11.1 us in runs of 3 places, 11.6 in runs of 4, 12.0 in runs of 5.)
+constexpr int PA_ITEM_COST = 2, PA_MIN_RUN = 3, PA_WHOLE = PA_ITEM_COST + 4;
 
 // Unit `unit` of item (b, h), at place v of this block's run.
 template <int UNIT>
@@ -219,7 +222,8 @@ __device__ __forceinline__ void locate(const kie_paged_attention_args &a, Cursor
   const int heads = a.pages.n_kv_heads;
   all *= heads;
   before *= heads;
-  *per_block = max(divide(all + gridDim.x - 1, gridDim.x), (long long)PA_MIN_RUN);
+  const long long items = (long long)a.n_seqs * heads, mean = divide(all + items - 1, items);
+  *per_block = max(divide(all + gridDim.x - 1, gridDim.x), mean <= PA_WHOLE ? mean : PA_MIN_RUN);
   const long long v0 = blockIdx.x * *per_block;
   *end = (int)max(0ll, min(*per_block, all - v0));
   if (v0 >= before && v0 < before + mine * heads) {
@@ -502,8 +506,15 @@ paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
   int p_base = 0, p_page[SUBS], p_id[SUBS];  // lane j: the pages of the warp's tile of unit p_base + j; of p's tile
   const int row0 = lane / CH;  // row of the lane's first chunk; the next are 32 / CH rows on
   const uint32_t dst_lane = (lane * 16) ^ (swz(row0) << 4);
-  const int k_lane = row0 * (int)a.pages.k_stride[2] * ES + (lane % CH) * 16;  // 16 rows span less than 2^31 bytes
-  const int v_lane = row0 * (int)a.pages.v_stride[2] * ES + (lane % CH) * 16;
+  // strides in bytes: below 2^32, of positions below 2^27, so that an address is the base and two 32 x 32-bit products
+  const uint32_t k_page = (uint32_t)a.pages.k_stride[0] * ES, k_row = (uint32_t)a.pages.k_stride[2] * ES;
+  const uint32_t v_page = (uint32_t)a.pages.v_stride[0] * ES, v_row = (uint32_t)a.pages.v_stride[2] * ES;
+  const uint8_t *k_base, *v_base;  // the lane's first chunk in page 0 of p's head
+  auto set_head = [&]() {
+    const int at = (lane % CH) * 16;
+    k_base = static_cast<const uint8_t *>(a.pages.k) + (uint64_t)p.h * (uint32_t)a.pages.k_stride[1] * ES + (uint64_t)row0 * k_row + at;
+    v_base = static_cast<const uint8_t *>(a.pages.v) + (uint64_t)p.h * (uint32_t)a.pages.v_stride[1] * ES + (uint64_t)row0 * v_row + at;
+  };
   const uint32_t ring0 = smem_u32(sm.ring[warp]);
   auto first_pos = [&](const Cursor<T::UNIT> &x) { return x.s.from + (x.unit * PA_WARPS + warp) * T::POS; };
   auto fetch_pages = [&]() {  // requested before the issue that uses them
@@ -531,29 +542,25 @@ paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
       if (lane == 0) sm.live[warp][slot] = p_live;
     }
     if (p_live) {
-      const int64_t *st = is_v ? a.pages.v_stride : a.pages.k_stride;
-      const int step = (int)st[2] * ES * (32 / CH);
+      const uint32_t row = is_v ? v_row : k_row, step = row * (32 / CH);
       const uint32_t dst = ring0 + slot * T::HALF + dst_lane;
 #pragma unroll
       for (int s = 0; s < SUBS; ++s) {
         const unsigned at = pos + 16 * s, off = bs_shift >= 0 ? at & (bs - 1) : at % bs;
         const uint32_t live = (p_live >> (16 * s)) & 0xffffu;
-        const int64_t page = live ? p_id[s] : 0;  // an address inside the pages even where nothing is read
-        const uint8_t *src = static_cast<const uint8_t *>(is_v ? a.pages.v : a.pages.k) +
-                             (page * st[0] + p.h * st[1] + off * st[2]) * ES + (is_v ? v_lane : k_lane);
+        const uint32_t page = live ? p_id[s] : 0;  // an address inside the pages even where nothing is read
+        const uint8_t *src = (is_v ? v_base : k_base) + (uint64_t)page * (is_v ? v_page : k_page) + (uint64_t)off * row;
         constexpr int N = LOADS / SUBS;
         if (live == 0xffffu) {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            cp_async16((dst ^ (swz((i + s * N) * (32 / CH)) << 4)) + (i + s * N) * 512, src);
-            src += step;
+            cp_async16((dst ^ (swz((i + s * N) * (32 / CH)) << 4)) + (i + s * N) * 512, src + (uint64_t)step * i);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            cp_async16((dst ^ (swz((i + s * N) * (32 / CH)) << 4)) + (i + s * N) * 512, src,
+            cp_async16((dst ^ (swz((i + s * N) * (32 / CH)) << 4)) + (i + s * N) * 512, src + (uint64_t)step * i,
                        (p_live >> (row0 + (i + s * N) * (32 / CH))) & 1u);
-            src += step;
           }
         }
       }
@@ -569,6 +576,7 @@ paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
     }
     if (is_v) {
       if (p.v < end) p.next(a);
+      if (p.unit == 0) set_head();
       if (p.unit == 0 || p.unit == p_base + 32) fetch_pages();
     }
   };
@@ -583,6 +591,7 @@ paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
         [&](int i) { return 16 * (i >> 1) + (KIND == PG_E4M3 ? 4 * t + 2 * (i & 1) : 2 * t + 8 * (i & 1)); }, raw);
   };
   request_q(c.b, c.h);
+  set_head();
   fetch_pages();
 #pragma unroll
   for (int x = 0; x < NS - 1; ++x) {

@@ -79,19 +79,21 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Flushing results and arguments below 2^-126 to 0 (a weight that small counts for nothing) saves the rescaling around
+// each of these.
 __device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float rcp(float x) {
   float y;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float lg2(float x) {
   float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
@@ -322,10 +324,17 @@ struct JoinShare {
   int r0 = threadIdx.x / LANES, d = threadIdx.x % LANES * 4;
 };
 
-// The thread's share of pieces piece(0 .. n - 1), joined in order: put(r, d, sum, M, L) gets their sum at the largest
+// Pieces in their order: the first, and the others `step` floats apart.
+struct Pieces {
+  const float *first, *rest;
+  size_t step;
+  __device__ __forceinline__ const float *operator[](int i) const { return i == 0 ? first : rest + (size_t)(i - 1) * step; }
+};
+
+// The thread's share of n pieces, joined in order: put(r, d, sum, M, L) gets their sum at the largest
 // reference M. The loads of BATCH pieces are in flight at a time.
-template <int DH, class F, class P>
-__device__ __forceinline__ void join_pieces(const F &piece, int n, int group, const P &put) {
+template <int DH, class P>
+__device__ __forceinline__ void join_pieces(const Pieces &piece, int n, int group, const P &put) {
   using S = JoinShare<DH>;
   constexpr int R = S::ROWS, BATCH = 8 / R;
   const S me;
@@ -343,7 +352,7 @@ __device__ __forceinline__ void join_pieces(const F &piece, int n, int group, co
     float4 y[BATCH][R];
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) {
-      const float *p = piece(min(i0 + k, n - 1));
+      const float *p = piece[min(i0 + k, n - 1)];
 #pragma unroll
       for (int q = 0; q < R; ++q) {
         const int r = min(me.r0 + q * S::STEP, group - 1);
@@ -412,28 +421,25 @@ __device__ __forceinline__ void publish(const kie_paged_attention_args &a, unsig
   const Workspace ws(a, DH);
   const int first = (int)divide(v, per_block), last = (int)divide(v + units - 1, per_block);
   const int group = a.n_heads / a.pages.n_kv_heads, n = last - first + 1;
-  int fan = n;
-  if (n > PA_ONE_LEVEL) {
-    fan = (int)ceilf(sqrtf((float)n));
-    const int g0 = ((int)blockIdx.x - first) / fan * fan, size = min(fan, n - g0), at = first + g0;
-    const int kind = g0 ? CONT : START;
-    if (!block_arrive(ws.word(at, kind), call, size)) return;
-    const auto piece = [&](int i) { return ws.at(at + i, g0 + i ? CONT : START); };
-    float *to = ws.at(at, JOINED + kind);
-    join_pieces<DH>(piece, size, group,
-                    [&](int r, int d, float4 acc, float M, float L) { put_piece<DH>(to, group, r, d, acc, M, L); });
-    if (!block_arrive(ws.word(first, ITEM), call, (n + fan - 1) / fan)) return;
-  } else if (!block_arrive(ws.word(first, START), call, n)) {
+  const bool vec = out_vec(a);
+  const auto finish = [&](int r, int d, float4 acc, float M, float L) {
+    finish4(a, vec, b, (int64_t)h * group + r, d, acc, M, L);
+  };
+  const size_t step = PA_PIECES * ws.piece;
+  if (n <= PA_ONE_LEVEL) {
+    if (block_arrive(ws.word(first, START), call, n))
+      join_pieces<DH>(Pieces{ws.at(first, START), ws.at(first + 1, CONT), step}, n, group, finish);
     return;
   }
-  const int parts = n > PA_ONE_LEVEL ? (n + fan - 1) / fan : n;
-  const auto piece = [&](int i) {
-    return n > PA_ONE_LEVEL ? ws.at(first + i * fan, JOINED + (i ? CONT : START)) : ws.at(first + i, i ? CONT : START);
-  };
-  const bool vec = out_vec(a);
-  join_pieces<DH>(piece, parts, group, [&](int r, int d, float4 acc, float M, float L) {
-    finish4(a, vec, b, (int64_t)h * group + r, d, acc, M, L);
-  });
+  const int fan = (int)ceilf(sqrtf((float)n));
+  const int g0 = ((int)blockIdx.x - first) / fan * fan, size = min(fan, n - g0), at = first + g0, kind = g0 ? CONT : START;
+  if (!block_arrive(ws.word(at, kind), call, size)) return;
+  float *to = ws.at(at, JOINED + kind);
+  join_pieces<DH>(Pieces{ws.at(at, kind), ws.at(at + 1, CONT), step}, size, group,
+                  [&](int r, int d, float4 acc, float M, float L) { put_piece<DH>(to, group, r, d, acc, M, L); });
+  const int groups = (n + fan - 1) / fan;
+  if (block_arrive(ws.word(first, ITEM), call, groups))
+    join_pieces<DH>(Pieces{ws.at(first, JOINED + START), ws.at(first + fan, JOINED + CONT), fan * step}, groups, group, finish);
 }
 
 // ---- the kernel ---------------------------------------------------------------------------------------------
@@ -491,6 +497,7 @@ paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
   const unsigned bs = a.pages.block_size;
   const int bs_shift = (bs & (bs - 1)) ? -1 : __ffs(bs) - 1;
 
+  wait_for_previous();
   Cursor<T::UNIT> c;
   int end;
   long long per_block;
@@ -854,6 +861,7 @@ paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
       if (done) break;
     }
   }
+  let_next_begin();
   cp_wait<0>();
 }
 
@@ -874,8 +882,7 @@ cudaError_t launch(const kie_paged_attention_args &a, int dev, int sms, cudaStre
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  paged_attn_kernel<KIND, DH, SPLIT><<<sms * PaTile<KIND, DH>::BLOCKS, PA_THREADS, smem, stream>>>(a, call_number());
-  return cudaGetLastError();
+  return launch_after_previous(paged_attn_kernel<KIND, DH, SPLIT>, sms * PaTile<KIND, DH>::BLOCKS, PA_THREADS, smem, stream, a, call_number());
 }
 
 template <int DH>

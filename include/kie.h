@@ -361,7 +361,7 @@ int kie_paged_append(const kie_paged_append_args *a, void *stream);
  * to 8 query heads each), out = sum_j p_j V_j with p = softmax(scale * q . K_j) over the positions j in
  * [max(0, lens[b] - window), lens[b]) (window 0: all), and lse (if not NULL) = ln sum exp(scale * q . K_j). The new
  * token's own row is already in the pages (it is position lens[b] - 1). A sequence of length <= 0 gets zeros and an
- * lse of -inf; lengths past max_blocks * block_size (at most 2^30) are cut there. Positions on a page outside
+ * lse of -inf, as does a head whose every score is -inf; lengths past max_blocks * block_size (at most 2^30) are cut there. Positions on a page outside
  * [0, n_blocks) are left out. Rows behind a sequence's end are never read. q, out: q_dtype, strides {sequence, head} in elements,
  * head_dim contiguous; lse [n_seqs][n_heads]. q_dtype is KIE_F32 (F16 and E4M3 pages), or the pages' own 16-bit
  * type, or either 16-bit type for E4M3 pages. Sums and the softmax are fp32; fp32 queries and the weights p go

@@ -413,6 +413,7 @@ int refuse(const char *msg) {
 
 int finish(cudaError_t e, const char *what) {
   if (e == cudaSuccess) return KIE_OK;
+  cudaGetLastError();  // reported here: the next caller's check shall not find it again
   snprintf(g_paged_error, sizeof(g_paged_error), "%s: %s", what, cudaGetErrorString(e));
   return KIE_ERR_CUDA;
 }

@@ -89,7 +89,7 @@ def rope_table(theta: float, head_dim: int, n_pos: int, device=None):
 
 class PagedCache:
     """K/V pages of every layer of a model for up to max_seqs sequences, with their block table, lengths and free
-    list, all on the GPU. A step: ``extend`` (pages and slots for the new tokens), then per layer ``append`` and
+    list, all on the GPU at fixed addresses. A step: ``extend`` (pages and slots for the new tokens), then per layer ``append`` and
     ``attention``; ``release`` takes finished sequences' pages back; ``load`` copies a prompt that a Decoder has
     prefilled."""
 
@@ -114,15 +114,18 @@ class PagedCache:
         return {"k_cache": self.k[l], "v_cache": self.v[l], **scales}
 
     def extend(self, new_lens, n_rows: int) -> PagedStep:
-        """Pages and slots for new_lens (int32 [max_seqs]) more tokens per sequence; updates lens and the free list."""
+        """Pages and slots for new_lens (int32 [max_seqs]) more tokens per sequence. lens, the table and the free list
+        are updated in place, so that a captured step goes on from where its last replay ended."""
         step = paged_extend(new_lens, self.lens, self.block_table, self.free_blocks, self.n_free, self.block_size, n_rows)
-        self.lens, self.n_free = step.lens, step.n_free
+        self._update(step.lens, step.n_free)
         return step
+
+    def _update(self, lens, n_free) -> None:
+        _torch()._foreach_copy_([self.lens, self.n_free], [lens, n_free])
 
     def release(self, done) -> None:
         """Take back the pages of the sequences with done (bool [max_seqs])."""
-        self.lens, self.n_free = paged_release(done, self.lens, self.block_table, self.free_blocks, self.n_free,
-                                               self.block_size)
+        self._update(*paged_release(done, self.lens, self.block_table, self.free_blocks, self.n_free, self.block_size))
 
     def append(self, l: int, k, v, step: PagedStep, q=None, q_out=None):
         """Rotate and store layer l's K/V rows of a step; returns the rotated q."""

@@ -400,21 +400,50 @@ def test_a_captured_step_follows_its_inputs():
     cache = kie.PagedCache(M, n_blocks=40, block_size=bs, max_seqs=n, max_blocks=4)
     one = ints([1, 1, 0, 1, 1, 1])
     q, k, v = (torch.randn(n, h, M.head_dim, device="cuda") for h in (M.n_heads, M.n_kv_heads, M.n_kv_heads))
-    lens, n_free = cache.lens, cache.n_free
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         step = cache.extend(one, n)
         rq = cache.append(0, k, v, step, q=q)
         out = cache.attention(0, rq)
-        lens.copy_(step.lens), n_free.copy_(step.n_free)
     want_lens = np.zeros(n, dtype=int)
     for t in range(20):
         g.replay()
         want_lens += np.array(one.tolist())
-        assert lens.tolist() == want_lens.tolist()
-    ref = oracle.attention(rq, cache.k[0], cache.v[0], cache.block_table, lens, M.head_dim ** -0.5)
+        assert cache.lens.tolist() == want_lens.tolist()
+    ref = oracle.attention(rq, cache.k[0], cache.v[0], cache.block_table, cache.lens, M.head_dim ** -0.5)
     assert torch.all((out.double() - ref[0]).abs() <= oracle.attention_bounds(rq, F16, *ref)[0])
-    assert n_free.tolist() == [40 - 5 * 2]
+    assert cache.n_free.tolist() == [40 - 5 * 2]
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    """No kernel has run, or been loaded, when the operators are captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch, persistent_monokernel_decode_gb300 as kie
+from synth.configs import MOE_TINY as M
+n = 3
+for dtype in (torch.float16, torch.float8_e4m3fn):
+    cache = kie.PagedCache(M, 9, 16, n, 4, dtype=dtype)
+    one = torch.ones(n, dtype=torch.int32, device="cuda")
+    q, k, v = (torch.ones(n, h, M.head_dim, device="cuda") for h in (M.n_heads, M.n_kv_heads, M.n_kv_heads))
+    done = torch.ones(n, dtype=torch.bool, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step = cache.extend(one, n)
+        out = cache.attention(0, cache.append(0, k, v, step, q=q))
+        cache.release(done)
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert cache.n_free.tolist() == [9] and cache.lens.tolist() == [0] * n
+        assert torch.allclose(out, torch.ones_like(out), atol=1e-6), out
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
 
 
 def raw_attention(q, k, v, table, lens, workspace):

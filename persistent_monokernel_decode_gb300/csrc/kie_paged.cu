@@ -294,9 +294,10 @@ struct Eight {
 // not diverge between queries, keys and values): thread t holds elements 8t .. 8t + 7 of each and their partners of the
 // other half. The rotation's products and sums are rounded one by one (no fused multiply-add), so that a plain fp32
 // evaluation gives the same bits, and with them the same E4M3 codes. Bound by HBM where there are many rows (each
-// element is read and written once): 8,192 fp32 rows of 16 + 8 heads, 189 MB, take 31 us, 6.1 TB/s; 16-bit rows have half
-// the bytes in flight per thread and reach 5.0 TB/s (bf16 pages), 4.0-4.5 (E4M3, whose maxima and quotients add a third
-// to the instructions). Two heads to a thread: one reached 3.8 TB/s on the bf16 rows, four 5.1 but 74 % of two's rate on
+// element is read and written once): 8,192 fp32 rows of 16 + 8 heads, 189 MB, take 31 us, 6.1 TB/s; 16-bit rows take as
+// many instructions for half the bytes and reach 5.0 TB/s (bf16 pages), 4.0-4.5 (E4M3, whose maxima and quotients add a
+// third). Resident blocks that loop with the next row's loads in flight were no faster there (E4M3 14.5 us instead of 14.4
+// for 4,097 rows). Two heads to a thread: one reached 3.8 TB/s on the bf16 rows, four 5.1 but 74 % of two's rate on
 // fp32 ones. Few rows are a chain of two loads (32 rows 2.0 us, an empty launch included).
 template <int DH, int X, bool VEC>
 __global__ void __launch_bounds__(PP_THREADS, X == KIE_F32 ? 6 : 8) paged_append_kernel(const kie_paged_append_args a) {

@@ -340,7 +340,7 @@ int kie_paged_release(const kie_paged_release_args *a, void *stream);
  * q_out may be q with the same strides). All inputs are x_dtype (KIE_F16, KIE_BF16, KIE_F32). With a table
  * rope [n_pos][head_dim / 2] of (cos, sin) fp32 pairs, k and q are rotated first at positions[t] (pairs
  * (i, i + head_dim / 2), in fp32: x_i c - x_j s, x_j c + x_i s); v never. Rows are rounded to the cache's type once;
- * an E4M3 row gets the scale max|x| / 448 (2^-126 for a zero row) and the codes of x / scale. A row whose slot lies
+ * an E4M3 row gets the scale max|x| / 448 (2^-126 where that rounds to 0) and the codes of x / scale. A row whose slot lies
  * outside the pages, or whose position lies outside the table, is padding: nothing is written for it. Slots must
  * not repeat: of two rows with the same slot, each 16 bytes and each scale may come from either.
  * k_pairs != 0: k rows hold each pair (i, i + head_dim / 2) in adjacent elements, as the K planes of a ctx's cache

@@ -385,7 +385,9 @@ __global__ void __launch_bounds__(PP_THREADS, X == KIE_F32 ? 6 : 8) paged_append
     const unsigned lanes = ((1u << TPH) - 1u) << ((threadIdx.x & 31) / TPH * TPH);
 #pragma unroll
     for (int o = 1; o < TPH; o <<= 1) top = max_nan(top, __shfl_xor_sync(lanes, top, o));
-    const float scale = top == 0.f ? 0x1p-126f : __fdiv_rn(top, 448.f), r = __frcp_rn(scale);
+    float scale = __fdiv_rn(top, 448.f);
+    if (scale == 0.f) scale = 0x1p-126f;  // a row of zeros, or (fp32) of elements up to 448 * 2^-150: all codes are 0
+    const float r = __frcp_rn(scale);
     const bool fast = codes_fast(scale);
     uint8_t *q8 = static_cast<uint8_t *>(dst);
     *reinterpret_cast<uint2 *>(q8 + to) = codes8(lo, scale, r, fast);

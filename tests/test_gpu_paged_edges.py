@@ -1,0 +1,49 @@
+"""Paged-cache operators on the GPU where values, rows and arguments are at their limits: E4M3 scales that underflow,
+V rows of vanishing and infinite scale, infinite K rows, steps in which not every sequence has a row, and prompts that
+do not fit the step they are loaded by."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_oracle as oracle
+import persistent_monokernel_decode_gb300 as kie
+from test_gpu_paged import BF16, E4M3, F16, F32, batch, bits, gen, ints, page_tensors
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    kie.build()
+    yield
+
+
+# ---- append --------------------------------------------------------------------------------------------------
+
+def test_append_of_tiny_rows_into_e4m3():
+    """fp32 rows with maxima from 2^-149 to 2^-110 that also hold zeros. The scale is max|x| / 448 rounded to fp32, 2^-126
+    where that is 0, and no code is NaN. A value is off by half a step of its code (2^-4 of it, or 2^-10 scales), and
+    by what the rounding of the scale, 2^-150 at most, can cut from it: 448 * 2^-150."""
+    n, dh = 40, 64
+    rows = torch.rand((n, 2, dh), generator=torch.Generator().manual_seed(1), dtype=torch.float64) * 2 - 1
+    rows[:, :, 7::3] = 0
+    top = torch.tensor([[2.0 ** e, -1.75 * 2.0 ** e] for e in range(-149, -109)], dtype=torch.float64)
+    rows[:, :, 5] = 1
+    rows = (rows * top[..., None]).float()
+    (kc, vc), (ks, vs) = page_tensors(3, 2, 16, dh, E4M3)
+    kie.paged_append(rows.cuda(), rows.cuda(), kc, vc, torch.arange(n, device="cuda").int(), k_scale=ks, v_scale=vs)
+    scale = (rows.abs().amax(-1).double() / 448).float()
+    assert torch.any(scale == 0) and torch.any((scale > 0) & (scale < 2.0 ** -126)) and torch.any(scale > 2.0 ** -126)
+    scale[scale == 0] = 2.0 ** -126
+    codes = (rows.double() / scale.double()[..., None]).float().clamp(-448, 448).to(E4M3)
+    for got, got_s in ((kc, ks), (vc, vs)):
+        got, got_s = (x.cpu().transpose(1, 2).flatten(0, 1)[:n] for x in (got, got_s))
+        assert torch.equal(got_s, scale)
+        assert not torch.isnan(got.float()).any()
+        assert torch.equal(bits(got), bits(codes))
+        err = (got.double() * got_s.double()[..., None] - rows.double()).abs()
+        assert torch.all(err <= rows.double().abs() * 2 ** -4 + got_s.double()[..., None] * 2 ** -10 + 448 * 2.0 ** -150)
+    out = kie.paged_attention(torch.randn(1, 4, dh, device="cuda"), kc, vc, ints([[0, 1, 2]]), ints([n]), k_scale=ks, v_scale=vs)
+    assert torch.all(torch.isfinite(out))

@@ -41,8 +41,11 @@ constexpr int PA_ROWS = PAGED_MAX_GROUP;
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 // Weights are kept as 2^7 2^(v - ref): an fp16 pair holds them to 2^-25, which is 2^-32 of the largest.
 constexpr float P_BIAS = 7.f, P_LIMIT = 32768.f;
-// Scales of E4M3 value rows count into the reference down to this (log2), so that the plain weights stay finite.
-constexpr float MIN_LOG2_SCALE = -60.f;
+// The scales of E4M3 value rows count into the reference down to MIN_LOG2_SCALE (log2), so that after a move the plain
+// weights, which the sum adds up, are at most 2^67. Rows of smaller scales that come later may outgrow the rest without
+// their weighted values showing it: the reference also moves when a lane's plain weights of a tile pass P_PLAIN. The sums of
+// 2^30 positions then stay below 2^121.
+constexpr float MIN_LOG2_SCALE = -60.f, P_PLAIN = 0x1p90f;
 
 enum { PG_F16 = 0, PG_BF16 = 1, PG_E4M3 = 2 };
 
@@ -744,6 +747,7 @@ paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
         for (int i = 0; i < SUBS; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) far = far || fabsf(w[i][e]) > P_LIMIT;
+        if (KIND == PG_E4M3) far = far || part[0] > P_PLAIN || part[1] > P_PLAIN;
         if (__any_sync(0xffffffffu, far)) {  // move the references to the maxima so far
           float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll

@@ -47,3 +47,42 @@ def test_append_of_tiny_rows_into_e4m3():
         assert torch.all(err <= rows.double().abs() * 2 ** -4 + got_s.double()[..., None] * 2 ** -10 + 448 * 2.0 ** -150)
     out = kie.paged_attention(torch.randn(1, 4, dh, device="cuda"), kc, vc, ints([[0, 1, 2]]), ints([n]), k_scale=ks, v_scale=vs)
     assert torch.all(torch.isfinite(out))
+
+
+# ---- attention -----------------------------------------------------------------------------------------------
+
+def loud_rows(level, count, v_scale, qt, seed=0):
+    """A batch on E4M3 pages (as of `batch`) whose late rows 520, 521, ... score about `level` above the rest in every head,
+    with the given V scale."""
+    q, k, v, table, lens, ks, vs = batch([700] * 100, 4, 4, 64, 16, E4M3, qt, seed=seed, dead=0.0)
+    ks *= 0.02  # the other scores stay below 20
+    row = q.float() * (level * 8.0 / (q.float() ** 2).sum(-1, keepdim=True))  # the operator's scale is 1 / 8
+    codes, scale = oracle.quantise(row)
+    for at in range(520, 520 + count):
+        page, r = table[:, at // 16].long(), at % 16
+        k.view(torch.uint8)[page, :, r] = codes.view(torch.uint8)
+        ks[page, :, r] = scale
+        vs[page, :, r] = v_scale
+    return q, k, v, table, lens, ks, vs
+
+
+@pytest.mark.parametrize("qt", [F32, F16, BF16])
+@pytest.mark.parametrize("v_scale", [0.0, 2.0 ** -126])
+@pytest.mark.parametrize("level", [75, 78, 84, 86, 130, 200])
+@pytest.mark.parametrize("count", [1, 3, 40])
+def test_attention_where_rows_of_vanishing_scale_dominate(count, level, v_scale, qt):
+    """V rows of zeros (as the append stores them) whose weights outweigh the rest by up to e^200.
+
+    To the bounds of the oracle comes what the header says of V scales below 2^-60: weights are held to 2^-32 of the
+    largest weight, with the scales counted as 2^-60 at least, so that n positions of values up to 448 may be off by
+    n * 448 * 2^-31 times the largest p_j max(scale_j, 2^-60)."""
+    q, k, v, table, lens, ks, vs = loud_rows(level, count, v_scale, qt)
+    out, lse = kie.paged_attention(q, k, v, table, lens, k_scale=ks, v_scale=vs, return_lse=True)
+    ref = oracle.attention(q, k, v, table, lens, 0.125, 0, ks, vs)
+    tol_out, tol_lse = oracle.attention_bounds(q, E4M3, *ref)
+    # the loud rows have the largest p, which is at most 1, and a scale of 2^-60 counted; every other row a p below
+    # e^(20 - level) and a scale below 2^4
+    largest = max(2.0 ** -60, 16 * math.exp(20 - level))
+    assert not torch.isnan(out).any()
+    assert torch.all((lse.double() - ref[1]).abs() <= tol_lse)
+    assert torch.all((out.double() - ref[0]).abs() <= tol_out + 700 * 448 * 2.0 ** -31 * largest)

@@ -45,7 +45,8 @@ constexpr float P_BIAS = 7.f, P_LIMIT = 32768.f;
 // weights, which the sum adds up, are at most 2^67. Rows of smaller scales that come later may outgrow the rest without
 // their weighted values showing it: the reference also moves when a lane's plain weights of a tile pass P_PLAIN. The sums of
 // 2^30 positions then stay below 2^121.
-constexpr float MIN_LOG2_SCALE = -60.f, P_PLAIN = 0x1p90f;
+// An infinite scale counts as 2^127: the reference stays finite, and with it the sum and the lse, which do not depend on V.
+constexpr float MIN_LOG2_SCALE = -60.f, MAX_LOG2_SCALE = 127.f, P_PLAIN = 0x1p90f;
 
 enum { PG_F16 = 0, PG_BF16 = 1, PG_E4M3 = 2 };
 
@@ -106,6 +107,8 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+__device__ __forceinline__ float log2_scale(float x) { return fminf(fmaxf(lg2(fabsf(x)), MIN_LOG2_SCALE), MAX_LOG2_SCALE); }
 
 template <int KIND>
 __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -755,8 +758,7 @@ paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if ((live >> (16 * i + g + 8 * (e >> 1))) & 1u)
-                top[e & 1] = fmaxf(top[e & 1], fmaf(s[i][e], rs[e & 1],
-                                                    KIND == PG_E4M3 ? fmaxf(lg2(fabsf(vs[i][e >> 1])), MIN_LOG2_SCALE) : 0.f));
+                top[e & 1] = fmaxf(top[e & 1], fmaf(s[i][e], rs[e & 1], KIND == PG_E4M3 ? log2_scale(vs[i][e >> 1]) : 0.f));
           float f[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {

@@ -86,3 +86,17 @@ def test_attention_where_rows_of_vanishing_scale_dominate(count, level, v_scale,
     assert not torch.isnan(out).any()
     assert torch.all((lse.double() - ref[1]).abs() <= tol_lse)
     assert torch.all((out.double() - ref[0]).abs() <= tol_out + 700 * 448 * 2.0 ** -31 * largest)
+
+
+def test_attention_with_an_infinite_scale_of_a_value_row():
+    """What the append stores for a V row with an infinity: the head's output there is not finite, its lse is (it does not
+    depend on V), and no other head's is touched."""
+    q, k, v, table, lens, ks, vs = batch([300, 90, 300], 8, 4, 64, 16, E4M3, F16, dead=0.0)
+    clean, lse = kie.paged_attention(q, k, v, table, lens, k_scale=ks, v_scale=vs, return_lse=True)
+    vs[table[0, 15].item(), 1, 3] = math.inf
+    out, got = kie.paged_attention(q, k, v, table, lens, k_scale=ks, v_scale=vs, return_lse=True)
+    assert not torch.any(torch.isfinite(out[0, 2:4]))
+    out[0, 2:4] = clean[0, 2:4]
+    assert torch.equal(out, clean)
+    _, tol = oracle.attention_bounds(q, E4M3, *oracle.attention(q, k, torch.zeros_like(v), table, lens, 0.125, 0, ks, ks))
+    assert torch.all((got - lse).abs() <= 2 * tol)

@@ -366,6 +366,11 @@ int kie_paged_append(const kie_paged_append_args *a, void *stream);
  * head_dim contiguous; lse [n_seqs][n_heads]. q_dtype is KIE_F32 (F16 and E4M3 pages), or the pages' own 16-bit
  * type, or either 16-bit type for E4M3 pages. Sums and the softmax are fp32; fp32 queries and the weights p go
  * through the tensor cores as two 16-bit parts (E4M3 value rows whose scale is below 2^-60 with fewer bits).
+ * Infinities and NaN where nothing is attended are of no consequence. Attended ones stay with the heads that attend them:
+ * an infinity in K counts as IEEE arithmetic has it (a score of -inf has weight 0; an fp32 query element 2^39 times
+ * smaller than its head's largest counts as 0), an infinity in V may become NaN in its element of the output, as a NaN
+ * does. Weighted sums are formed of up to 2^15 times the values before the division by the sum of weights, so BF16 values
+ * above 2^96 may overflow.
  * n_seqs * max_blocks * block_size * n_kv_heads must not pass 2^45. out may be q, with the same strides.
  * workspace: kie_paged_attention_workspace bytes, 256-byte aligned, contents arbitrary before and after; calls that
  * may overlap need one each. */

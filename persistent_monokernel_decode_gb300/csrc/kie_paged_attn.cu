@@ -714,7 +714,11 @@ paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
             ks[1] = sm.scale[warp][KIND == PG_E4M3 ? ring : 0][16 * i + g + 8];
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[i][e] = (x[0][e] + x[1][e]) * ks[e >> 1];
+          for (int e = 0; e < 4; ++e) {
+            // an infinity in K makes the product with the queries' second part infinite or NaN: the first alone counts then
+            if (SPLIT && KIND == PG_F16 && !(fabsf(x[1][e]) <= FLT_MAX)) x[1][e] = 0.f;
+            s[i][e] = (x[0][e] + x[1][e]) * ks[e >> 1];
+          }
         }
       }
       ring = ring + 1 == NS ? 0 : ring + 1;

@@ -100,3 +100,45 @@ def test_attention_with_an_infinite_scale_of_a_value_row():
     assert torch.equal(out, clean)
     _, tol = oracle.attention_bounds(q, E4M3, *oracle.attention(q, k, torch.zeros_like(v), table, lens, 0.125, 0, ks, ks))
     assert torch.all((got - lse).abs() <= 2 * tol)
+
+
+@pytest.mark.parametrize("cache,qt", [(F16, F32), (F16, F16), (BF16, BF16)])
+def test_attention_with_infinite_keys(cache, qt):
+    """A score of -inf has weight 0: K rows with an infinity against queries of the other sign there count as left out, a
+    sequence of such rows alone gives zeros and -inf. A score of +inf makes its head NaN, and only that one."""
+    q, k, v, table, lens, ks, vs = batch([300, 40, 20, 90], 4, 2, 64, 16, cache, qt, dead=0.0)
+    q[:, :, 9] = q[:, :, 9].abs() + 0.5
+    finite = k.clone()
+    gone = [torch.arange(0, 300, 7), torch.tensor([39]), torch.arange(20), torch.tensor([], dtype=torch.long)]
+    for b, at in enumerate(gone):
+        at = at.to("cuda")
+        k[table[b].long()[at // 16], :, at % 16, 9] = -math.inf
+    out, lse = kie.paged_attention(q, k, v, table, lens, return_lse=True)
+    assert torch.all(out[2] == 0) and torch.all(lse[2] == -math.inf)
+    for b in (0, 1, 3):  # against the kept positions, moved together
+        kept = torch.tensor([p for p in range(int(lens[b])) if p not in gone[b].tolist()], device="cuda")
+        page, r = table[b].long()[kept // 16], kept % 16
+        n = oracle.ceil_div(kept.numel(), 16)
+        pages = [torch.zeros((n, 16, 2, 64), dtype=cache, device="cuda") for _ in range(2)]
+        for x, y in zip(pages, (finite, v)):
+            x.view(-1, 2, 64)[:kept.numel()] = y[page, :, r]
+        pages = [x.transpose(1, 2) for x in pages]
+        ref = oracle.attention(q[b:b + 1], *pages, torch.arange(n, device="cuda")[None], ints([kept.numel()]), 0.125)
+        tol_out, tol_lse = oracle.attention_bounds(q[b:b + 1], cache, *ref)
+        assert torch.all((out[b:b + 1].double() - ref[0]).abs() <= tol_out), b
+        assert torch.all((lse[b:b + 1].double() - ref[1]).abs() <= tol_lse), b
+    k[table[3, 2].item(), 1, 5, 9] = math.inf
+    again = kie.paged_attention(q, k, v, table, lens)
+    assert torch.all(torch.isnan(again[3, 2:])) and torch.equal(again[3, :2], out[3, :2]) and torch.equal(again[:3], out[:3])
+
+
+@pytest.mark.parametrize("cache,qt", [(F16, F32), (F16, F16), (BF16, BF16)])
+def test_attention_with_infinite_values(cache, qt):
+    """An infinity in V makes its own element of the heads that attend it infinite or NaN, and nothing else."""
+    q, k, v, table, lens, ks, vs = batch([70, 700, 70], 4, 2, 64, 16, cache, qt)
+    clean, lse = kie.paged_attention(q, k, v, table, lens, return_lse=True)
+    v[table[1, 30].item(), 0, 3, 5] = math.inf
+    out, got = kie.paged_attention(q, k, v, table, lens, return_lse=True)
+    assert not torch.any(torch.isfinite(out[1, :2, 5])) and torch.equal(got, lse)
+    out[1, :2, 5] = clean[1, :2, 5]
+    assert torch.equal(out, clean)

@@ -372,6 +372,11 @@ int kie_paged_append(const kie_paged_append_args *a, void *stream);
  * does. Weighted sums are formed of up to 2^15 times the values before the division by the sum of weights, so BF16 values
  * above 2^96 may overflow.
  * n_seqs * max_blocks * block_size * n_kv_heads must not pass 2^45. out may be q, with the same strides.
+ * seqs and positions (both or neither; then lens is NULL) take the rows of a step as kie_paged_extend lists them: query
+ * row t, of n_seqs rows, is the token at positions[t] of the sequence in row seqs[t] of the block table (n_table rows), and
+ * attends to the positions up to its own, [max(0, positions[t] + 1 - window), positions[t] + 1). Sequences without a row,
+ * with several (each reads the pages for itself) and rows in any order are fine; a row with seqs[t] outside [0, n_table) or
+ * a negative position, as extend lists rows that were not admitted, gets zeros and an lse of -inf.
  * workspace: kie_paged_attention_workspace bytes, 256-byte aligned, contents arbitrary before and after; calls that
  * may overlap need one each. */
 typedef struct {
@@ -386,6 +391,8 @@ typedef struct {
   size_t workspace_bytes;
   float scale;
   int n_seqs, n_heads, max_blocks, window, q_dtype;
+  const int32_t *seqs, *positions;
+  int n_table;
 } kie_paged_attention_args;
 int kie_paged_attention(const kie_paged_attention_args *a, void *stream);
 

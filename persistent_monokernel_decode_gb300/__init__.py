@@ -171,7 +171,8 @@ class KiePagedAttentionArgs(ctypes.Structure):
     _fields_ = [("pages", KiePages), ("q", P), ("out", P), ("lse", P), ("q_stride", I64x2), ("out_stride", I64x2),
                 ("block_table", P), ("lens", P), ("table_stride", ctypes.c_int64), ("workspace", P),
                 ("workspace_bytes", ctypes.c_size_t), ("scale", ctypes.c_float)] + \
-               [(n, ctypes.c_int) for n in ("n_seqs", "n_heads", "max_blocks", "window", "q_dtype")]
+               [(n, ctypes.c_int) for n in ("n_seqs", "n_heads", "max_blocks", "window", "q_dtype")] + \
+               [("seqs", P), ("positions", P), ("n_table", ctypes.c_int)]
 
 
 # Every entry point of include/kie.h with its ctypes signature.

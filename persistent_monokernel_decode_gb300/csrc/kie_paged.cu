@@ -578,9 +578,13 @@ int kie_paged_attention(const kie_paged_attention_args *p, void *stream) {
   if (a.pages.dtype == KIE_F16 && a.q_dtype == KIE_BF16) return refuse("F16 pages take F16 or F32 queries");
   if (!(a.scale == a.scale) || a.scale - a.scale != 0.f) return refuse("scale must be finite");
   if (a.n_seqs == 0) return KIE_OK;
-  if (!a.q || !a.out || !a.block_table || !a.lens) return refuse("q, out, block_table or lens is NULL");
-  if (a.n_seqs > 1 && a.table_stride < a.max_blocks) return refuse("table_stride is below max_blocks");
-  if (!ints_aligned({a.block_table, a.lens, a.lse})) return refuse("block_table, lens or lse is not 4-byte aligned");
+  if (!a.q || !a.out || !a.block_table) return refuse("q, out or block_table is NULL");
+  if (!a.seqs != !a.positions) return refuse("seqs and positions go together");
+  if (!a.seqs == !a.lens) return refuse("either lens or seqs and positions must be given, the other NULL");
+  if (a.seqs && a.n_table < 0) return refuse("n_table must be >= 0");
+  if ((a.seqs ? a.n_table : a.n_seqs) > 1 && a.table_stride < a.max_blocks) return refuse("table_stride is below max_blocks");
+  if (!ints_aligned({a.block_table, a.lens, a.seqs, a.positions, a.lse}))
+    return refuse("block_table, lens, seqs, positions or lse is not 4-byte aligned");
   if (!aligned(a.q, paged_dtype_bytes(a.q_dtype)) || !aligned(a.out, paged_dtype_bytes(a.q_dtype)))
     return refuse("q or out is not aligned to its elements");
   if ((double)a.n_seqs * a.max_blocks * a.pages.block_size * a.pages.n_kv_heads > 0x1p45)

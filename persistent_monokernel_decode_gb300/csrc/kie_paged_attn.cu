@@ -1,6 +1,6 @@
 // Attention of one new token per sequence over a paged K/V cache, split over the cache's length and joined.
 //
-// The work is a list of items (sequence, KV head), each a row of units of 64 (E4M3: 128) positions. Every block of the
+// The work is a list of items (query row, KV head), each a row of units of 64 (E4M3: 128) positions. Every block of the
 // grid takes an equal run of the list, whatever items it belongs to, so a ragged batch and a single long sequence load
 // the GPU alike; a block keeps the whole items of its run to itself and publishes the pieces of the (at most two)
 // items that it shares with its neighbours. The last block to publish a piece of an item joins them all (in two levels
@@ -164,15 +164,17 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
 
 // ---- the list of units --------------------------------------------------------------------------------------
 
-// One sequence's span: positions [lo, len), in n units of UNIT positions from `from` on, a multiple of 16 (at least one
-// unit, so that a sequence of no positions still writes its zeros).
+// What query row b attends: positions [lo, len) of its sequence, in n units of UNIT positions from `from` on, a multiple of
+// 16 (at least one unit, so that a row of no positions still writes its zeros). Rows of a step (a.seqs) end with their own
+// position: their positions stand in a.lens here, and those of no sequence find no pages.
 struct Span {
   int lo, len, from, n;
 };
 template <int UNIT>
 __device__ __forceinline__ Span span_of(const kie_paged_attention_args &a, int b) {
   Span s;
-  s.len = min(max(a.lens[b], 0), a.max_blocks * a.pages.block_size);
+  const int own = a.seqs ? 1 : 0;
+  s.len = min(max(a.lens[b], -own), a.max_blocks * a.pages.block_size - own) + own;
   s.lo = a.window > 0 ? max(0, s.len - a.window) : 0;
   s.from = s.lo & ~15;
   s.n = max(1, (int)((unsigned)(s.len - s.from + UNIT - 1) / UNIT));
@@ -541,12 +543,14 @@ paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
   auto first_pos = [&](const Cursor<T::UNIT> &x) { return x.s.from + (x.unit * PA_WARPS + warp) * T::POS; };
   auto fetch_pages = [&]() {  // requested before the issue that uses them
     p_base = p.unit;
+    int seq = p.b;
+    if (a.seqs && p.v < end) seq = a.seqs[p.b];
 #pragma unroll
     for (int i = 0; i < SUBS; ++i) {
       const int pos = first_pos(p) + lane * T::UNIT + 16 * i;
       p_page[i] = -1;
-      if (p.v < end && pos < p.s.len)
-        p_page[i] = a.block_table[p.b * a.table_stride + (bs_shift >= 0 ? (unsigned)pos >> bs_shift : (unsigned)pos / bs)];
+      if (p.v < end && pos < p.s.len && (unsigned)seq < (unsigned)a.n_table)
+        p_page[i] = a.block_table[seq * a.table_stride + (bs_shift >= 0 ? (unsigned)pos >> bs_shift : (unsigned)pos / bs)];
     }
   };
   auto issue = [&](int slot, bool is_v) {
@@ -920,6 +924,11 @@ size_t kie_paged_attention_workspace_bytes(int n_heads, int n_kv_heads, int head
   return kie::pa_header_bytes(blocks) + blocks * kie::PA_PIECES * kie::pa_piece_floats(n_heads / n_kv_heads, head_dim) * 4;
 }
 
-cudaError_t kie_launch_paged_attention(const kie_paged_attention_args &a, int dev, int sms, cudaStream_t stream) {
+cudaError_t kie_launch_paged_attention(const kie_paged_attention_args &args, int dev, int sms, cudaStream_t stream) {
+  kie_paged_attention_args a = args;
+  if (a.seqs)
+    a.lens = a.positions;
+  else
+    a.n_table = a.n_seqs;
   return a.pages.head_dim == 64 ? kie::launch_dh<64>(a, dev, sms, stream) : kie::launch_dh<128>(a, dev, sms, stream);
 }

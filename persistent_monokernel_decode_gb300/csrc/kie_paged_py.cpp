@@ -282,10 +282,10 @@ PyObject *append(PyObject *const *x) {
   return result;
 }
 
-// attention(q, k_cache, v_cache, block_table, lens, scale, window, k_scale, v_scale, out, return_lse)
+// attention(q, k_cache, v_cache, block_table, lens, scale, window, k_scale, v_scale, out, return_lse, seqs, positions)
 PyObject *attention(PyObject *const *x) {
   const at::Tensor &q = tensor(x[0], "q"), &kc = tensor(x[1], "k_cache"), &vc = tensor(x[2], "v_cache"),
-                   &tab = tensor(x[3], "block_table"), &lens = tensor(x[4], "lens");
+                   &tab = tensor(x[3], "block_table");
   const at::Device dev = q.device();
   kie_paged_attention_args a = {};
   a.pages = pages(kc, vc, x[7], x[8], dev);
@@ -295,8 +295,15 @@ PyObject *attention(PyObject *const *x) {
   a.n_heads = size_of(H, "n_heads");
   a.q_dtype = kind(q);
   a.q = rows(q, "q", q.sizes(), q.scalar_type(), dev, a.q_stride);
-  a.lens = ints(lens, "lens", dev, B);
-  a.block_table = table(tab, dev, B);
+  if (x[11] != Py_None || x[12] != Py_None) {
+    need(x[4] == Py_None && x[11] != Py_None && x[12] != Py_None, "either lens or both seqs and positions are needed");
+    a.seqs = ints(tensor(x[11], "seqs"), "seqs", dev, B);
+    a.positions = ints(tensor(x[12], "positions"), "positions", dev, B);
+    a.n_table = size_of(tab.dim() > 0 ? tab.size(0) : 0, "the number of the block table's rows");
+  } else {
+    a.lens = ints(tensor(x[4], "lens"), "lens", dev, B);
+  }
+  a.block_table = table(tab, dev, a.seqs ? a.n_table : B);
   a.table_stride = tab.stride(0);
   a.max_blocks = size_of(tab.size(1), "max_blocks");
   a.window = (int)integer(x[6], "window");
@@ -373,7 +380,7 @@ PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, nullptr},
                          {"extend", FAST(extend, 7), nullptr},
                          {"release", FAST(release, 6), nullptr},
                          {"append", FAST(append, 12), nullptr},
-                         {"attention", FAST(attention, 11), nullptr},
+                         {"attention", FAST(attention, 13), nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -68,14 +68,18 @@ def paged_append(k, v, k_cache, v_cache, slots, *, positions=None, rope=None, q=
 
 
 def paged_attention(q, k_cache, v_cache, block_table, lens, *, scale=None, window: int = 0, k_scale=None, v_scale=None,
-                    out=None, return_lse: bool = False):
+                    out=None, return_lse: bool = False, seqs=None, positions=None):
     """Attention of one new token per sequence over the pages (kie_paged_attention): q [B, n_heads, head_dim], lens
     int32 [B] positions cached (the new token's among them), block_table int32 [B, max_blocks]. scale: 1 /
     sqrt(head_dim) by default; window: only the last `window` positions (0: all). Returns out, or (out, lse) with
     lse fp32 [B, n_heads]. The workspace is allocated by the call, so calls on several streams and captured graphs
-    share none."""
+    share none.
+
+    With seqs and positions (int32 [B], as a PagedStep lists them) and lens None, row t of q is the token at positions[t]
+    of the sequence in row seqs[t] of block_table [R, max_blocks], and attends to the positions up to its own; rows of
+    no sequence (-1) get zeros."""
     return (_ready or _native()).attention(q, k_cache, v_cache, block_table, lens, scale, window, k_scale, v_scale, out,
-                                           return_lse)
+                                           return_lse, seqs, positions)
 
 
 def rope_table(theta: float, head_dim: int, n_pos: int, device=None):
@@ -128,13 +132,19 @@ class PagedCache:
         self._update(*paged_release(done, self.lens, self.block_table, self.free_blocks, self.n_free, self.block_size))
 
     def append(self, l: int, k, v, step: PagedStep, q=None, q_out=None):
-        """Rotate and store layer l's K/V rows of a step; returns the rotated q."""
+        """Rotate and store layer l's K/V rows of a step (packed in its order); returns the rotated q, packed likewise."""
         return paged_append(k, v, slots=step.slots, positions=step.positions, rope=self.rope, q=q, q_out=q_out,
                             **self._layer(l))
 
-    def attention(self, l: int, q, **kw):
-        """Layer l's attention of one new token per sequence: q [max_seqs, n_heads, head_dim] (see paged_attention)."""
-        return paged_attention(q, block_table=self.block_table, lens=self.lens, **self._layer(l), **kw)
+    def attention(self, l: int, q, step: PagedStep | None = None, **kw):
+        """Layer l's attention of a step's rows, q [n_rows, n_heads, head_dim] as `append` returned it, each over its own
+        sequence up to its own position (rows that were not admitted get zeros). Without a step, q [max_seqs, n_heads,
+        head_dim] holds one row per sequence, sequence b's newest token in row b: a step's rows lie like that only if it
+        brought exactly one token for every sequence. See paged_attention."""
+        if step is None:
+            return paged_attention(q, block_table=self.block_table, lens=self.lens, **self._layer(l), **kw)
+        return paged_attention(q, block_table=self.block_table, lens=None, seqs=step.seqs, positions=step.positions,
+                               **self._layer(l), **kw)
 
     def load(self, decoder, step: PagedStep, first_row: int = 0) -> None:
         """Copy the prompt that `decoder` (a Decoder of this model) has prefilled, positions 0 .. position - 1 of

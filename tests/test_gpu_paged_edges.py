@@ -142,3 +142,156 @@ def test_attention_with_infinite_values(cache, qt):
     assert not torch.any(torch.isfinite(out[1, :2, 5])) and torch.equal(got, lse)
     out[1, :2, 5] = clean[1, :2, 5]
     assert torch.equal(out, clean)
+
+
+# ---- rows of a step ------------------------------------------------------------------------------------------
+
+def check_rows(q, k, v, table, seqs, positions, ks=None, vs=None, window=0):
+    """Every row against the plain attention over its own sequence's positions up to its own."""
+    out, lse = kie.paged_attention(q, k, v, table, None, seqs=seqs, positions=positions, window=window, k_scale=ks,
+                                   v_scale=vs, return_lse=True)
+    live = (seqs >= 0) & (seqs < table.shape[0]) & (positions >= 0)
+    lens = torch.where(live, positions.long() + 1, 0)
+    ref = oracle.attention(q, k, v, table[torch.where(live, seqs, 0).long()], lens, q.shape[-1] ** -0.5, window, ks, vs)
+    tol_out, tol_lse = oracle.attention_bounds(q, k.dtype, *ref)
+    assert torch.all((out.double() - ref[0]).abs() <= tol_out)
+    empty = ref[4] == 0
+    assert torch.all(out[empty] == 0) and torch.all(lse[empty] == -math.inf) and torch.all(empty[~live])
+    assert torch.all((lse.double() - ref[1]).abs()[~empty] <= tol_lse[~empty])
+    return out, lse
+
+
+@pytest.mark.parametrize("cache,qt", [(F16, F16), (F16, F32), (BF16, BF16), (E4M3, F32), (E4M3, F16)])
+@pytest.mark.parametrize("window", [0, 20])
+def test_attention_of_the_rows_of_a_step(cache, qt, window):
+    """Rows in any order, several of a sequence, sequences without a row, and rows that belong to none."""
+    lens = [70, 0, 200, 33, 1, 16]
+    q, k, v, table, _, ks, vs = batch(lens, 8, 2, 128, 32, cache, qt)
+    rows = [(2, 199), (0, 69), (0, 68), (-1, 5), (3, 32), (2, 0), (6, 3), (2 ** 31 - 1, 0), (5, -1), (4, 0), (3, 31), (-1, -1),
+            (0, -2 ** 31), (5, 15)] + [(2, p) for p in range(40)]
+    q = torch.randn((len(rows), 8, 128), generator=gen(4), device="cuda").to(qt)
+    check_rows(q, k, v, table, ints([s for s, _ in rows]), ints([p for _, p in rows]), ks, vs, window)
+
+
+def test_attention_of_rows_past_the_table_is_cut_there():
+    q, k, v, table, lens, ks, vs = batch([64, 64], 4, 2, 64, 16, F16, F16)
+    out = kie.paged_attention(q, k, v, table, None, seqs=ints([1, 0]), positions=ints([2 ** 31 - 1, 64]))
+    assert torch.equal(out, kie.paged_attention(q, k, v, table.flip(0), lens))
+
+
+def test_attention_of_rows_as_of_sequences():
+    """The rows 0 .. B - 1 at the sequences' last positions: the same bits as with the lengths."""
+    q, k, v, table, lens, ks, vs = batch([700, 0, 33, 2000], 20, 4, 128, 16, F16, F32)
+    want = kie.paged_attention(q, k, v, table, lens, return_lse=True)
+    got = kie.paged_attention(q, k, v, table, None, seqs=torch.arange(4, device="cuda").int(), positions=lens - 1, return_lse=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", [F16, E4M3])
+def test_a_step_with_idle_refused_and_prompt_rows(dtype):
+    """Sequences that bring nothing, one token, several or too many: every query attends over its own sequence."""
+    from synth.configs import MOE_TINY as M
+    cache = kie.PagedCache(M, n_blocks=9, block_size=16, max_seqs=6, max_blocks=3, dtype=dtype)
+    # step 2: request 1 is longer than its table row, 5 finds no page; step 3: 3 is idle and 5 is refused again
+    for i, (new, n_rows, ok) in enumerate([([5, 16, 0, 31, 1, 0], 60, [1, 1, 1, 1, 1, 1]), ([1, 33, 20, 0, 1, 40], 95, [1, 0, 1, 1, 1, 0]),
+                                           ([1, 1, 1, 0, 1, 40], 48, [1, 1, 1, 1, 1, 0]), ([1, 0, 1, 1, 0, 1], 9, [1] * 6)]):
+        step = cache.extend(ints(new), n_rows)
+        assert step.admitted.tolist() == [bool(x) for x in ok], i
+        g = gen(i)
+        q, k, v = (torch.randn((n_rows, h, M.head_dim), generator=g, device="cuda") for h in (M.n_heads, M.n_kv_heads, M.n_kv_heads))
+        rq = cache.append(0, k, v, step, q=q)
+        dead = step.seqs < 0
+        rq[dead] = math.nan  # what rows that belong to none hold is of no consequence
+        out = cache.attention(0, rq, step)
+        scales = (None, None) if cache.k_scale is None else (cache.k_scale[0], cache.v_scale[0])
+        want, _ = check_rows(rq, cache.k[0], cache.v[0], cache.block_table, step.seqs, step.positions, *scales)
+        assert torch.equal(out, want) and torch.all(out[dead] == 0) and dead.any()
+        seqs = [r for r in range(6) if ok[r] for _ in range(new[r])]
+        assert step.seqs[step.seqs >= 0].tolist() == seqs
+
+
+def test_a_captured_step_follows_its_rows():
+    """One captured step replayed with another set of sequences each time."""
+    from synth.configs import MOE_TINY as M
+    n = 6
+    cache = kie.PagedCache(M, n_blocks=40, block_size=16, max_seqs=n, max_blocks=4)
+    new = ints([1] * n)
+    q, k, v = (torch.randn(n, h, M.head_dim, device="cuda") for h in (M.n_heads, M.n_kv_heads, M.n_kv_heads))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step = cache.extend(new, n)
+        rq = cache.append(0, k, v, step, q=q)
+        out, lse = cache.attention(0, rq, step, return_lse=True)
+    rng = np.random.RandomState(0)
+    for _ in range(12):
+        who = rng.randint(0, 2, n)
+        new.copy_(ints(who.tolist()))
+        k.normal_(), v.normal_()
+        g.replay()
+        assert step.seqs.tolist() == np.flatnonzero(who).tolist() + [-1] * int(n - who.sum())
+        want = check_rows(rq.nan_to_num(), cache.k[0], cache.v[0], cache.block_table, step.seqs, step.positions)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_a_batched_decode_with_waiting_sequences_matches_the_decoder():
+    """Three prompts decoded together where in most steps some sequence waits, and one is refused until another's pages
+    are free: every sequence's logits stay those of a Decoder running it alone."""
+    import synth
+    from synth.configs import TINY as M
+    from test_gpu_paged import f16
+    weights = synth.model_weights(M)
+    w = {k: f16(weights[k]) for k in ("embed", "lm_head", "final_norm")}
+    w["layers"] = [{k: f16(v) for k, v in lay.items()} for lay in weights["layers"]]
+    prompts = [synth.tokens(s, n, M.vocab) for s, n in ((11, 20), (12, 9), (13, 32))]
+    decs = [kie.Decoder(M, weights, max_seq=96) for _ in prompts]
+    cache = kie.PagedCache(M, n_blocks=5, block_size=16, max_seqs=3, max_blocks=6)
+    for d, p in zip(decs, prompts):
+        d.prefill(p)
+    step = cache.extend(ints([len(p) for p in prompts]), sum(len(p) for p in prompts))
+    for d, at in zip(decs, (0, 20, 29)):
+        cache.load(d, step, at)
+    current = [d.logits() for d in decs]
+
+    def rms(x, gain):
+        return x * torch.rsqrt((x * x).mean(-1, keepdim=True) + M.rms_eps) * gain
+
+    def advance(who):
+        """One token of each sequence of `who`; the sequences that were admitted."""
+        toks = [int(np.argmax(current[b])) for b in who]
+        step = cache.extend(ints([int(b in who) for b in range(3)]), 3)
+        x = w["embed"][torch.tensor(toks + [0] * (3 - len(who)), device="cuda")]
+        for l, lay in enumerate(w["layers"]):
+            u = rms(x, lay["attn_norm"])
+            q, k, v = ((u @ lay[n].T).view(3, -1, M.head_dim) for n in ("wq", "wk", "wv"))
+            o = cache.attention(l, cache.append(l, k, v, step, q=q), step)
+            x = x + o.reshape(3, -1) @ lay["wo"].T
+            u = rms(x, lay["ffn_norm"])
+            x = x + (torch.nn.functional.silu(u @ lay["w_gate"].T) * (u @ lay["w_up"].T)) @ lay["w_down"].T
+        logits = (rms(x, w["final_norm"]) @ w["lm_head"].T).cpu().numpy()
+        went = [b for b in who if step.admitted[b]]
+        for row, b in enumerate(who):
+            if b in went:
+                current[b] = decs[b].decode_forced(np.array([toks[row]], dtype=np.int32))[1][0]
+                assert np.max(np.abs(logits[row] - current[b])) <= 2e-2, b
+        return went
+
+    for who in ([0, 1, 2], [0, 2], [1], [1, 2], [2], [0, 1]):
+        # 2 + 1 + 2 pages are all there are: sequence 2 is full at 32 positions and refused
+        assert advance(who) == [b for b in who if b != 2]
+    assert cache.lens.tolist() == [23, 13, 32]
+    cache.release(torch.tensor([True, False, False], device="cuda"))
+    for who in ([1, 2], [2], [1, 2]):
+        assert advance(who) == who
+    assert cache.lens.tolist() == [0, 15, 35]
+    for d in decs:
+        d.close()
+
+
+def test_rows_and_lengths_exclude_each_other():
+    q, k, v, table, lens, _, _ = batch([20, 3], 4, 2, 64, 16, F16, F16)
+    some = ints([0, 1])
+    for bad in (dict(lens=lens, seqs=some, positions=some), dict(lens=None), dict(lens=None, seqs=some),
+                dict(lens=None, positions=some), dict(lens=lens, positions=some), dict(lens=None, seqs=some[:1], positions=some),
+                dict(lens=None, seqs=some, positions=some.long()), dict(lens=None, seqs=some.cpu(), positions=some)):
+        with pytest.raises(ValueError):
+            kie.paged_attention(q, k, v, table, bad.pop("lens"), **bad)

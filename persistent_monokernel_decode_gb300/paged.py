@@ -149,15 +149,23 @@ class PagedCache:
     def load(self, decoder, step: PagedStep, first_row: int = 0) -> None:
         """Copy the prompt that `decoder` (a Decoder of this model) has prefilled, positions 0 .. position - 1 of
         every layer, to the slots of rows first_row .. of a step that extended a sequence by that many tokens.
-        Synchronous, like the prefill."""
+        Synchronous, like the prefill. Raises ValueError, and copies nothing, unless those rows are positions 0 .. position - 1
+        of one admitted sequence and the decoder's cache has this model's layers and heads."""
         torch = _torch()
         n, m, d = decoder.position, self.model, decoder
+        if any(getattr(d.model, x) != getattr(m, x) for x in ("n_layers", "n_kv_heads", "head_dim")):
+            raise ValueError("the decoder's model has other layers or K/V heads")
+        if first_row < 0:
+            raise ValueError("first_row must be >= 0")
         decoder.sync()
         kv = d._kvbuf.view(torch.float16)[:2 * m.n_layers * m.n_kv_heads * d.max_seq * m.head_dim]
         kv = kv.view(m.n_layers, 2, m.n_kv_heads, d.max_seq, m.head_dim)[:, :, :, :n].transpose(2, 3)
         slots = step.slots[first_row:first_row + n]
         if slots.numel() != n:
             raise ValueError("the step has too few rows for the decoder's prompt")
+        seqs, positions = (x[first_row:first_row + n].tolist() for x in (step.seqs, step.positions))
+        if n and (seqs[0] < 0 or seqs != seqs[:1] * n or positions != list(range(n))):
+            raise ValueError("the step's rows are not positions 0 .. position - 1 of one admitted sequence")
         for l in range(m.n_layers):
             paged_append(kv[l, 0], kv[l, 1], slots=slots, k_pairs=True, **self._layer(l))
         torch.cuda.current_stream(self.device).synchronize()  # the decoder may go on, on whatever stream it has

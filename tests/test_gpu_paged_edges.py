@@ -295,3 +295,38 @@ def test_rows_and_lengths_exclude_each_other():
                 dict(lens=None, seqs=some, positions=some.long()), dict(lens=None, seqs=some.cpu(), positions=some)):
         with pytest.raises(ValueError):
             kie.paged_attention(q, k, v, table, bad.pop("lens"), **bad)
+
+
+# ---- prompts of a Decoder ------------------------------------------------------------------------------------
+
+def test_load_refuses_rows_that_are_not_the_prompts():
+    """A decoder that has gone past its prompt, a sequence that was not admitted or not empty, another model's decoder:
+    nothing is copied."""
+    import synth
+    from synth.configs import MOE_TINY, TINY as M
+    dec = kie.Decoder(M, synth.model_weights(M), max_seq=64)
+    dec.prefill(synth.tokens(31, 20, M.vocab))
+    cache = kie.PagedCache(M, n_blocks=4, block_size=16, max_seqs=3, max_blocks=3)
+    step = cache.extend(ints([20, 20, 1]), 41)  # sequence 2 finds no page
+    assert step.admitted.tolist() == [True, True, False]
+    for first in (1, 10, 20 + 1, -41, 40, 2 ** 40):
+        with pytest.raises(ValueError):
+            cache.load(dec, step, first)
+    dec.decode(1)
+    for first in (0, 20):  # 21 positions for 20 rows
+        with pytest.raises(ValueError):
+            cache.load(dec, step, first)
+    assert not cache.k.any() and not cache.v.any()
+    dec.reset()
+    dec.prefill(synth.tokens(31, 1, M.vocab))
+    with pytest.raises(ValueError):
+        cache.load(dec, step, 40)
+    step = cache.extend(ints([0, 1, 0]), 1)
+    with pytest.raises(ValueError):
+        cache.load(dec, step)  # position 20, not 0
+    assert not cache.k.any() and not cache.v.any()
+    other = kie.PagedCache(MOE_TINY, n_blocks=4, block_size=16, max_seqs=1, max_blocks=3)
+    step = other.extend(ints([1]), 1)
+    with pytest.raises(ValueError):
+        other.load(dec, step)
+    dec.close()

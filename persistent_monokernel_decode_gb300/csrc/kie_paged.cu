@@ -589,6 +589,8 @@ int kie_paged_attention(const kie_paged_attention_args *p, void *stream) {
     return refuse("q or out is not aligned to its elements");
   if ((double)a.n_seqs * a.max_blocks * a.pages.block_size * a.pages.n_kv_heads > 0x1p45)
     return refuse("n_seqs * max_blocks * block_size * n_kv_heads must not pass 2^45");
+  if (a.out == a.q && ((a.n_seqs > 1 && a.out_stride[0] != a.q_stride[0]) || (a.n_heads > 1 && a.out_stride[1] != a.q_stride[1])))
+    return refuse("out in place of q needs q's strides");
   int dev, sms;
   if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
   const size_t need = kie_paged_attention_workspace_bytes(a.n_heads, a.pages.n_kv_heads, a.pages.head_dim, sms);

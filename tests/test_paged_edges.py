@@ -23,3 +23,11 @@ def test_attention_of_rows_refuses(change, word):
     for k, v in change.items():
         setattr(a, k, v)
     refused("kie_paged_attention", a, word)
+
+
+@pytest.mark.parametrize("out_stride", [(512, 64), (256, 128), (64, 256)])
+def test_attention_in_place_needs_equal_strides(out_stride):
+    """Another block would read a query that this one has overwritten."""
+    a = attention_args()
+    a.q_stride[:], a.out_stride[:] = (256, 64), out_stride
+    refused("kie_paged_attention", a, "strides")

@@ -337,7 +337,8 @@ int kie_paged_release(const kie_paged_release_args *a, void *stream);
 
 /* K/V rows into their slots: row t of k and v ([n_rows] x [n_kv_heads] x [head_dim], strides {row, head} in
  * elements, head_dim contiguous) goes to slot slots[t] of the pages, and q, if given, to q_out (the same type;
- * q_out may be q with the same strides). All inputs are x_dtype (KIE_F16, KIE_BF16, KIE_F32). With a table
+ * q_out may be q with the same strides, and else must not overlap it). Strides of 0 are refused in what is written (q_out,
+ * pages, scales) where that dimension has more than one entry. All inputs are x_dtype (KIE_F16, KIE_BF16, KIE_F32). With a table
  * rope [n_pos][head_dim / 2] of (cos, sin) fp32 pairs, k and q are rotated first at positions[t] (pairs
  * (i, i + head_dim / 2), in fp32: x_i c - x_j s, x_j c + x_i s); v never. Rows are rounded to the cache's type once;
  * an E4M3 row gets the scale max|x| / 448 (2^-126 where that rounds to 0) and the codes of x / scale. A row whose slot lies
@@ -371,7 +372,8 @@ int kie_paged_append(const kie_paged_append_args *a, void *stream);
  * smaller than its head's largest counts as 0), an infinity in V may become NaN in its element of the output, as a NaN
  * does. Weighted sums are formed of up to 2^15 times the values before the division by the sum of weights, so BF16 values
  * above 2^96 may overflow.
- * n_seqs * max_blocks * block_size * n_kv_heads must not pass 2^45. out may be q, with the same strides.
+ * n_seqs * max_blocks * block_size * n_kv_heads must not pass 2^45. out may be q, with the same strides, and else must not
+ * overlap it; a stride of 0 in out is refused where that dimension has more than one entry.
  * seqs and positions (both or neither; then lens is NULL) take the rows of a step as kie_paged_extend lists them: query
  * row t, of n_seqs rows, is the token at positions[t] of the sequence in row seqs[t] of the block table (n_table rows), and
  * attends to the positions up to its own, [max(0, positions[t] + 1 - window), positions[t] + 1). Sequences without a row,

@@ -460,6 +460,14 @@ bool aligned_rows(const void *p, const int64_t (&stride)[2], int dtype) {
   return aligned(p, 16) && stride[0] % unit == 0 && stride[1] % unit == 0;
 }
 
+// A dimension that is written but has no stride: its elements are one, and which block's value stays is open.
+template <int N>
+bool repeats(const int64_t (&stride)[N], const int (&size)[N]) {
+  for (int i = 0; i < N; ++i)
+    if (stride[i] == 0 && size[i] > 1) return true;
+  return false;
+}
+
 bool sm_count(int *dev, int *sms) {
   return cudaGetDevice(dev) == cudaSuccess &&
          cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) == cudaSuccess;
@@ -539,6 +547,12 @@ int kie_paged_append(const kie_paged_append_args *p, void *stream) {
     return refuse("q_out in place of q needs q's strides");
   const int64_t heads = (a.q ? a.n_heads : 0) + 2ll * a.pages.n_kv_heads, groups = (heads + PP_HEADS - 1) / PP_HEADS;
   if (a.n_rows * groups * PP_HEADS > 1ll << 28) return refuse("too many rows x heads (2^28 at most)");
+  if (a.q && repeats(a.q_out_stride, {a.n_rows, a.n_heads})) return refuse("q_out has a stride of 0 (an expanded tensor)");
+  const kie_pages &pg = a.pages;
+  for (const auto *st : {&pg.k_stride, &pg.v_stride, &pg.k_scale_stride, &pg.v_scale_stride})
+    if ((pg.dtype == KIE_E4M3 || st == &pg.k_stride || st == &pg.v_stride) &&
+        repeats(*st, {pg.n_blocks, pg.n_kv_heads, pg.block_size}))
+      return refuse("pages or scales that are written have a stride of 0 (an expanded tensor)");
   const int tph = a.pages.head_dim / 16;
   const int64_t warps = (a.n_rows + 32 / tph - 1) / (32 / tph) * groups;
   const unsigned grid = (unsigned)((warps * 32 + PP_THREADS - 1) / PP_THREADS);
@@ -591,6 +605,7 @@ int kie_paged_attention(const kie_paged_attention_args *p, void *stream) {
     return refuse("n_seqs * max_blocks * block_size * n_kv_heads must not pass 2^45");
   if (a.out == a.q && ((a.n_seqs > 1 && a.out_stride[0] != a.q_stride[0]) || (a.n_heads > 1 && a.out_stride[1] != a.q_stride[1])))
     return refuse("out in place of q needs q's strides");
+  if (repeats(a.out_stride, {a.n_seqs, a.n_heads})) return refuse("out has a stride of 0 (an expanded tensor)");
   int dev, sms;
   if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
   const size_t need = kie_paged_attention_workspace_bytes(a.n_heads, a.pages.n_kv_heads, a.pages.head_dim, sms);

@@ -31,3 +31,35 @@ def test_attention_in_place_needs_equal_strides(out_stride):
     a = attention_args()
     a.q_stride[:], a.out_stride[:] = (256, 64), out_stride
     refused("kie_paged_attention", a, "strides")
+
+
+@pytest.mark.parametrize("out_stride", [(0, 64), (256, 0)])
+def test_attention_refuses_an_expanded_output(out_stride):
+    a = attention_args()
+    a.out, a.q_stride[:], a.out_stride[:] = 2 * SOME, (256, 64), out_stride
+    refused("kie_paged_attention", a, "stride of 0")
+
+
+def strided_append_args(dtype=0):
+    a = append_args(dtype)
+    a.q_out = 2 * SOME
+    for s in (a.q_stride, a.q_out_stride):
+        s[:] = (256, 64)
+    for s in (a.pages.k_scale_stride, a.pages.v_scale_stride):
+        s[:] = (32, 16, 1)
+    return a
+
+
+@pytest.mark.parametrize("name", ["k_stride", "v_stride", "k_scale_stride", "v_scale_stride"])
+@pytest.mark.parametrize("dim", [0, 1, 2])
+def test_append_refuses_expanded_pages(name, dim):
+    a = strided_append_args(3)
+    getattr(a.pages, name)[dim] = 0
+    refused("kie_paged_append", a, "stride of 0")
+
+
+@pytest.mark.parametrize("dim", [0, 1])
+def test_append_refuses_an_expanded_output(dim):
+    a = strided_append_args()
+    a.q_out_stride[dim] = 0
+    refused("kie_paged_append", a, "stride of 0")

@@ -8,8 +8,10 @@ the extension is not built, or no GPU is present, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import subprocess
+import sys
 from concurrent.futures import ThreadPoolExecutor
 
 import numpy as np
@@ -21,6 +23,7 @@ _INCLUDE = os.path.join(_ROOT, "include")
 _BUILD = os.path.join(_ROOT, "_build")
 LIB_PATH = os.path.join(_HERE, "libkie.so")
 BINDING_PATH, BINDING_SOURCE = os.path.join(_HERE, "_paged.so"), "kie_paged_py.cpp"
+BINDING_ENV_PATH = os.path.join(_BUILD, "_paged.env")  # what _paged.so was compiled against
 SOURCES = ("kie_api.cu", "kie_decode.cu", "kie_gemv.cu", "kie_prefill.cu", "kie_paged.cu", "kie_paged_attn.cu")
 HEADERS = ("kie_layout.h", "kie_device.cuh", "kie_decode.cuh", "kie_prefill.cuh", "kie_tcgemm.cuh", "kie_tcattn.cuh",
            "kie_paged.cuh")
@@ -63,12 +66,36 @@ def binding_cmd() -> list[str]:
             f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
+def _older(path: str, deps) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(f) > os.path.getmtime(path) for f in deps)
+
+
+def _lib_stale() -> bool:
+    return _older(LIB_PATH, [os.path.join(_CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(_INCLUDE, "kie.h")])
+
+
+def _binding_env() -> str | None:
+    """The interpreter and the PyTorch that the binding module is compiled against; None without PyTorch."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return f"{sys.implementation.cache_tag} {torch.__version__} {os.path.dirname(torch.__file__)}"
+
+
+def _binding_stale() -> bool:
+    """The binding is missing, older than its sources, or compiled for another interpreter or PyTorch. False without PyTorch,
+    which nothing in it works without."""
+    env = _binding_env()
+    if env is None:
+        return False
+    if _older(BINDING_PATH, [os.path.join(_CSRC, BINDING_SOURCE), os.path.join(_INCLUDE, "kie.h")]):
         return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    deps = [os.path.join(_CSRC, f) for f in SOURCES + HEADERS + (BINDING_SOURCE,)] + [os.path.join(_INCLUDE, "kie.h")]
-    return any(os.path.getmtime(f) > t for f in deps)
+    try:
+        with open(BINDING_ENV_PATH) as f:
+            return f.read() != env
+    except OSError:
+        return True
 
 
 # The sources a decode launch is built from: the kernel, its ring and GEMV consumer, the packed layout, and the
@@ -89,18 +116,33 @@ def source_digest(files=DECODE_SOURCES) -> str:
 
 
 def build(force: bool = False) -> str:
-    """Compile libkie.so in-tree for sm_103a (the translation units in parallel, then link), and the binding module."""
-    if not force and not _stale():
+    """Compile libkie.so in-tree for sm_103a (the translation units in parallel, then link), and, where PyTorch is
+    installed, the binding module of the paged-cache operators. libkie.so is complete even if the binding does not compile
+    (which raises)."""
+    with_lib, with_binding = force or _lib_stale(), _binding_stale() or (force and _binding_env() is not None)
+    if not with_lib and not with_binding:
         return LIB_PATH
     os.makedirs(_BUILD, exist_ok=True)
+    run = functools.partial(subprocess.run, capture_output=True, text=True)
     with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        results = list(ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), [binding_cmd()] + compile_cmds()))
-    for r in results:
+        binding = ex.submit(run, binding_cmd()) if with_binding else None
+        for r in ex.map(run, compile_cmds() if with_lib else []):
+            if r.returncode != 0:
+                raise RuntimeError("nvcc failed:\n" + r.stdout + r.stderr)
+    if with_lib:
+        r = run(link_cmd())
         if r.returncode != 0:
-            raise RuntimeError(f"{os.path.basename(r.args[0])} failed:\n" + r.stdout + r.stderr)
-    r = subprocess.run(link_cmd(), capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("nvcc link failed:\n" + r.stdout + r.stderr)
+            raise RuntimeError("nvcc link failed:\n" + r.stdout + r.stderr)
+    if with_binding:
+        try:
+            r = binding.result()
+        except OSError as e:  # no compiler
+            raise RuntimeError(f"{LIB_PATH} is built, the paged operators' binding is not: {e}") from e
+        if r.returncode != 0:
+            raise RuntimeError(f"{LIB_PATH} is built, the paged operators' binding is not: {os.path.basename(r.args[0])} "
+                               "failed:\n" + r.stdout + r.stderr)
+        with open(BINDING_ENV_PATH, "w") as f:
+            f.write(_binding_env())
     return LIB_PATH
 
 

@@ -37,7 +37,7 @@ def _native():
         try:
             from . import _paged
         except ImportError as e:
-            raise RuntimeError("the paged operators' binding is missing: run __graft_entry__.build() (or "
+            raise RuntimeError(f"the paged operators' binding cannot be loaded ({e}): run __graft_entry__.build() (or "
                                "persistent_monokernel_decode_gb300.build()) first") from e
         _paged.bind(*[ctypes.cast(getattr(L, "kie_paged_" + n), ctypes.c_void_p).value
                       for n in ("extend", "release", "append", "attention", "attention_workspace", "last_error")], KieError)

@@ -63,3 +63,66 @@ def test_append_refuses_an_expanded_output(dim):
     a = strided_append_args()
     a.q_out_stride[dim] = 0
     refused("kie_paged_append", a, "stride of 0")
+
+
+# ---- the build -----------------------------------------------------------------------------------------------
+
+@pytest.fixture
+def elsewhere(tmp_path, monkeypatch):
+    """build() with stand-ins for the compilers, its outputs in a folder of the test's; returns what has run."""
+    ran = []
+    lib, binding = tmp_path / "libkie.so", tmp_path / "_paged.so"
+    monkeypatch.setattr(kie, "_BUILD", str(tmp_path))
+    monkeypatch.setattr(kie, "LIB_PATH", str(lib))
+    monkeypatch.setattr(kie, "BINDING_PATH", str(binding))
+    monkeypatch.setattr(kie, "BINDING_ENV_PATH", str(tmp_path / "_paged.env"))
+    monkeypatch.setattr(kie, "compile_cmds", lambda: ran.append("lib") or [["true"]])
+    monkeypatch.setattr(kie, "link_cmd", lambda: ["touch", str(lib)])
+    monkeypatch.setattr(kie, "binding_cmd", lambda: ran.append("binding") or ["touch", str(binding)])
+    return ran
+
+
+def test_build_compiles_what_is_missing_or_old(elsewhere):
+    import os
+    kie.build()
+    assert sorted(elsewhere) == ["binding", "lib"]
+    kie.build()
+    assert len(elsewhere) == 2
+    os.remove(kie.BINDING_PATH)
+    kie.build()
+    assert elsewhere[2:] == ["binding"] and os.path.exists(kie.BINDING_PATH)
+    os.utime(kie.LIB_PATH, (0, 0))
+    kie.build()
+    assert elsewhere[3:] == ["lib"]
+    kie.build(force=True)
+    assert sorted(elsewhere[4:]) == ["binding", "lib"]
+
+
+def test_a_binding_of_another_pytorch_is_compiled_anew(elsewhere, monkeypatch):
+    import torch
+    kie.build()
+    monkeypatch.setattr(torch, "__version__", "0.0")
+    kie.build()
+    assert elsewhere[2:] == ["binding"]
+    kie.build()
+    assert len(elsewhere) == 3
+
+
+@pytest.mark.parametrize("cmd", [["false"], ["/nowhere/g++"]])
+def test_the_library_is_complete_where_the_binding_does_not_compile(elsewhere, monkeypatch, cmd):
+    import os
+    monkeypatch.setattr(kie, "binding_cmd", lambda: cmd)
+    with pytest.raises(RuntimeError, match="is built"):
+        kie.build()
+    assert os.path.exists(kie.LIB_PATH)
+    with pytest.raises(RuntimeError):  # and it is not taken for built the next time
+        kie.build()
+
+
+def test_without_pytorch_the_library_alone_is_built(elsewhere, monkeypatch):
+    import os
+    import sys
+    monkeypatch.setitem(sys.modules, "torch", None)
+    kie.build()
+    kie.build()
+    assert elsewhere == ["lib"] and os.path.exists(kie.LIB_PATH) and not os.path.exists(kie.BINDING_PATH)

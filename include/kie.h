@@ -325,7 +325,10 @@ int kie_paged_extend(const kie_paged_extend_args *a, void *stream);
 /* Pages of finished requests (done[r] != 0, bytes) go back on the free list: free_blocks[n_free ...] receives their
  * block_table entries, requests in order, pages in order (those past free_capacity are dropped). lens_out: 0 for the
  * finished, else lens; n_free_out [1]. The table rows stay as they were. lens_out and n_free_out must not be lens
- * and n_free. */
+ * and n_free. Entries are moved as they are, here and in extend: one that is no page of the cache stays on the list
+ * and is handed out again. No access leaves the pages for it: its rows get the slot -1 or one that the append skips, and
+ * the attention leaves its positions out. A page that is released twice is handed out twice, to rows that then overwrite
+ * each other. */
 typedef struct {
   const uint8_t *done;
   const int32_t *lens, *n_free, *block_table;
@@ -343,7 +346,8 @@ int kie_paged_release(const kie_paged_release_args *a, void *stream);
  * (i, i + head_dim / 2), in fp32: x_i c - x_j s, x_j c + x_i s); v never. Rows are rounded to the cache's type once;
  * an E4M3 row gets the scale max|x| / 448 (2^-126 where that rounds to 0) and the codes of x / scale. A row whose slot lies
  * outside the pages, or whose position lies outside the table, is padding: nothing is written for it. Slots must
- * not repeat: of two rows with the same slot, each 16 bytes and each scale may come from either.
+ * not repeat: of two rows with the same slot, each 16 bytes (E4M3: each 8 codes) and each scale may come from either.
+ * n_rows times the heads of k, v and q, their sum rounded up to even, must not pass 2^28.
  * k_pairs != 0: k rows hold each pair (i, i + head_dim / 2) in adjacent elements, as the K planes of a ctx's cache
  * do ([n_layers][2][n_kv_heads][max_seq][head_dim], kie_buffer_sizes), so that a prompt that a ctx has prefilled can
  * be copied into pages; the pages always hold plain order. */

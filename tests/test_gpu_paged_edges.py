@@ -330,3 +330,32 @@ def test_load_refuses_rows_that_are_not_the_prompts():
     with pytest.raises(ValueError):
         other.load(dec, step)
     dec.close()
+
+
+# ---- pages that are none -------------------------------------------------------------------------------------
+
+def test_page_ids_outside_the_pages_pass_through_and_are_left_out():
+    """Release and extend move ids as they are; rows on such a page get no slot, or one that the append skips, and the
+    attention leaves its positions out."""
+    bs, n = 16, 5
+    bad = [-1, n, 2 ** 31 - 1, -2 ** 31]
+    table = ints([[3, bad[0], bad[1], bad[2]], [bad[3], 4, -1, -1]])
+    free = torch.full((12,), 7777, dtype=torch.int32, device="cuda")
+    lens, n_free = kie.paged_release(torch.ones(2, dtype=torch.bool, device="cuda"), ints([64, 17]), table, free, ints([0]), bs)
+    assert free.tolist() == [3, *bad[:3], bad[3], 4] + [7777] * 6 and n_free.tolist() == [6] and lens.tolist() == [0, 0]
+    step = kie.paged_extend(ints([96]), ints([0]), (wide := ints([[-1] * 6])), free, n_free, bs, 96)
+    assert wide.tolist() == [[4, bad[3], bad[2], bad[1], bad[0], 3]] and step.n_free.tolist() == [0]
+    slots = step.slots.tolist()
+    assert slots[:16] == list(range(64, 80)) and slots[80:] == list(range(48, 64))
+    assert all(s == -1 or s >= n * bs for s in slots[16:80])
+    (kc, vc), _ = page_tensors(n, 2, bs, 64, F16)
+    rows = torch.randn((96, 2, 64), generator=gen(1), device="cuda")
+    kie.paged_append(rows, rows, kc, vc, step.slots)
+    for page, at in ((4, 0), (3, 80)):
+        assert torch.equal(kc[page].transpose(0, 1), rows[at:at + 16].half())
+    assert not kc[:3].any() and not vc[:3].any()
+    q = torch.randn((1, 4, 64), generator=gen(2), device="cuda")
+    ref = oracle.attention(q, kc, vc, wide, step.lens, 0.125)
+    assert ref[4].item() == 32
+    out = kie.paged_attention(q, kc, vc, wide, step.lens)
+    assert torch.all((out.double() - ref[0]).abs() <= oracle.attention_bounds(q, F16, *ref)[0])

@@ -18,12 +18,7 @@ __host__ __device__ __forceinline__ int paged_dtype_bytes(int dtype) {
   return dtype == KIE_F32 ? 4 : dtype == KIE_E4M3 ? 1 : 2;
 }
 
-// One element of an activation tensor (uniform dtype) as fp32, and back, rounded to nearest even.
-__device__ __forceinline__ float paged_load(const void *p, int64_t i, int dtype) {
-  if (dtype == KIE_F32) return static_cast<const float *>(p)[i];
-  if (dtype == KIE_F16) return __half2float(static_cast<const __half *>(p)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-}
+// An fp32 value as an element of an activation tensor (uniform dtype), rounded to nearest even.
 __device__ __forceinline__ void paged_store(void *p, int64_t i, int dtype, float v) {
   if (dtype == KIE_F32)
     static_cast<float *>(p)[i] = v;
@@ -31,33 +26,6 @@ __device__ __forceinline__ void paged_store(void *p, int64_t i, int dtype, float
     static_cast<__half *>(p)[i] = __float2half_rn(v);
   else
     static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
-}
-
-// Eight consecutive elements at p + i as fp32; VEC: p + i is aligned for 16-byte accesses.
-template <bool VEC>
-__device__ __forceinline__ void load8(const void *p, int64_t i, int dtype, float (&v)[8]) {
-  if (!VEC) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = paged_load(p, i + e, dtype);
-    return;
-  }
-  if (dtype == KIE_F32) {
-    const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-    const float4 x = s[0], y = s[1];
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-    return;
-  }
-  const uint4 r = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (dtype == KIE_F16) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
-      v[2 * e] = f.x, v[2 * e + 1] = f.y;
-    } else {
-      v[2 * e] = __uint_as_float(w[e] << 16), v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
-  }
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
@@ -69,6 +37,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, int dtype) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+// Eight consecutive elements at p + i; VEC: p + i is aligned for 16-byte accesses.
 template <bool VEC>
 __device__ __forceinline__ void store8(void *p, int64_t i, int dtype, const float (&v)[8]) {
   if (!VEC) {

@@ -297,6 +297,14 @@ def test_rows_and_lengths_exclude_each_other():
             kie.paged_attention(q, k, v, table, bad.pop("lens"), **bad)
 
 
+@pytest.mark.parametrize("cache,qt", [(F16, F32), (E4M3, BF16)])
+def test_attention_of_a_prompt_behind_a_prefix(cache, qt):
+    """Every row of a prompt of 300 behind 130 cached positions, next to a sequence that decodes."""
+    q, k, v, table, _, ks, vs = batch([57, 430], 2, 1, 64, 16, cache, qt)
+    q = torch.randn((301, 2, 64), generator=gen(9), device="cuda").to(qt)
+    check_rows(q, k, v, table, ints([0] + [1] * 300), ints([56] + list(range(130, 430))), ks, vs)
+
+
 # ---- prompts of a Decoder ------------------------------------------------------------------------------------
 
 def test_load_refuses_rows_that_are_not_the_prompts():

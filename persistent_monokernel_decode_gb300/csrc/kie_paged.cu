@@ -48,7 +48,9 @@ __device__ __forceinline__ int clamp_int(long long v) { return (int)(v > INT_MAX
 // requests r = blockIdx.x (mod grid) and the rows [blockIdx.x * per, + per). No block waits for another. One scan does
 // for both sums although a request whose rows do not fit needs no pages: such requests are all behind those that fit.
 // Bound by latency (a load, the scan, a search and a load): 1,025 requests with 84,285 rows, 1.05 MB, take 6.3 us, 256
-// requests with a token each 3.4 us, of which an empty launch is about 2.
+// requests with a token each 3.4 us, of which an empty launch is about 2. Long prompts add to that: one thread takes all
+// pages of a request, one after the other (a load and a store that may alias), 35 ns each. A prompt of 8,192 tokens at
+// page size 16 takes 21 us, one of 131,072 288 us.
 // PER requests to a thread: 1 up to 512 requests (each request's pages are then taken by a thread of its own), else 4.
 template <int PER>
 __global__ void __launch_bounds__(PX_THREADS) paged_extend_kernel(const kie_paged_extend_args a, int per) {
@@ -296,8 +298,9 @@ struct Eight {
 // evaluation gives the same bits, and with them the same E4M3 codes. Bound by HBM where there are many rows (each
 // element is read and written once): 8,192 fp32 rows of 16 + 8 heads, 189 MB, take 31 us, 6.1 TB/s; 16-bit rows take as
 // many instructions for half the bytes and reach 5.0 TB/s (bf16 pages), 4.0-4.5 (E4M3, whose maxima and quotients add a
-// third). Resident blocks that loop with the next row's loads in flight were no faster there (E4M3 14.5 us instead of 14.4
-// for 4,097 rows). Two heads to a thread: one reached 3.8 TB/s on the bf16 rows, four 5.1 but 74 % of two's rate on
+// third); their kernels spill 8 to 12 bytes at the 64 registers that eight blocks leave. Resident blocks that loop with the
+// next row's loads in flight were no faster into E4M3 (14.5 us instead of 14.4 for 4,097 rows) and 4 % faster into bf16
+// pages (8,192 rows 19.8 us instead of 20.7); one form is kept for both. Two heads to a thread: one reached 3.8 TB/s on the bf16 rows, four 5.1 but 74 % of two's rate on
 // fp32 ones. Few rows are a chain of two loads (32 rows 2.0 us, an empty launch included).
 template <int DH, int X, bool VEC>
 __global__ void __launch_bounds__(PP_THREADS, X == KIE_F32 ? 6 : 8) paged_append_kernel(const kie_paged_append_args a) {

@@ -15,11 +15,13 @@
 // and output of a warp's positions stay in registers.
 //
 // No tcgen05: an MMA of 128 rows would have 5 of 128 filled, and at 20 operations a byte of K/V the arithmetic is far
-// from the bound (tensor pipe 14 % busy with fp16, 26 % with E4M3). Bound by HBM where there is much to read: 256
-// sequences of 4,096 positions (bf16, 16 heads over 4 of 128, 2.15 GB) take 309-313 us, 6.9 TB/s, 1.03 of the measured
-// copy rate; E4M3 with 20 heads (1.1 GB) 172 us, 6.4 TB/s. Where there is little, by its chain of latencies: launch,
+// from the bound (tensor pipe 14 % busy with bf16, 27 % with E4M3). Bound by HBM where there is much to read: 256
+// sequences of 4,096 positions (bf16, 16 heads over 4 of 128, 2.15 GB) take 309-313 us, 6.9 TB/s, 1.02 of the measured
+// copy rate. E4M3 is paced by its instructions instead (its loop has no memory stall left; a quarter of its tensor work is
+// the second part of queries that 16-bit types leave zero): 61 ragged sequences, 189 MB, take 39.3 us, 4.8 TB/s; 1.1 GB
+// with 20 heads 172 us, 6.4 TB/s. Where there is little to read it is bound by its chain of latencies: launch,
 // lengths, page ids, K, V, the join of the warps, and for shared items the arrival and the join of the pieces (one
-// sequence of 128 positions 6.0 us, of 1,152 9.6 us, of 8,704 13.7 us).
+// sequence of 128 positions 6.0 us, of 1,152 9.8 us, of 8,704 14.0 us).
 //
 // The reference of the softmax is not the running maximum but a value that stays within 2^8 of it: weights up to 2^15
 // fit in fp16, so it is only moved (with the shuffles and the rescaling that this costs) when a weight passes that.

@@ -374,7 +374,7 @@ int kie_paged_append(const kie_paged_append_args *a, void *stream);
  * Infinities and NaN where nothing is attended are of no consequence. Attended ones stay with the heads that attend them:
  * an infinity in K counts as IEEE arithmetic has it (a score of -inf has weight 0; an fp32 query element 2^39 times
  * smaller than its head's largest counts as 0), an infinity in V may become NaN in its element of the output, as a NaN
- * does. Weighted sums are formed of up to 2^15 times the values before the division by the sum of weights, so BF16 values
+ * does (an infinite E4M3 scale of V: in every element, while lse stays right). Weighted sums are formed of up to 2^15 times the values before the division by the sum of weights, so BF16 values
  * above 2^96 may overflow.
  * n_seqs * max_blocks * block_size * n_kv_heads must not pass 2^45. out may be q, with the same strides, and else must not
  * overlap it; a stride of 0 in out is refused where that dimension has more than one entry.

@@ -300,8 +300,8 @@ struct Eight {
 // many instructions for half the bytes and reach 5.0 TB/s (bf16 pages), 4.0-4.5 (E4M3, whose maxima and quotients add a
 // third); their kernels spill 8 to 12 bytes at the 64 registers that eight blocks leave. Resident blocks that loop with the
 // next row's loads in flight were no faster into E4M3 (14.5 us instead of 14.4 for 4,097 rows) and 4 % faster into bf16
-// pages (8,192 rows 19.8 us instead of 20.7); one form is kept for both. Two heads to a thread: one reached 3.8 TB/s on the bf16 rows, four 5.1 but 74 % of two's rate on
-// fp32 ones. Few rows are a chain of two loads (32 rows 2.0 us, an empty launch included).
+// pages (8,192 rows 19.8 us instead of 20.7); one form is kept for both. Two heads to a thread: one reached 3.8 TB/s on the
+// bf16 rows, four 5.1 but 74 % of two's rate on fp32 ones. Few rows are a chain of two loads (32 rows 2.0 us, an empty launch included).
 template <int DH, int X, bool VEC>
 __global__ void __launch_bounds__(PP_THREADS, X == KIE_F32 ? 6 : 8) paged_append_kernel(const kie_paged_append_args a) {
   begin_after_previous();

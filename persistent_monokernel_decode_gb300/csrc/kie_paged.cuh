@@ -1,5 +1,5 @@
-// Shared by the paged-cache operators: element conversion between the cache and activation types, and the launch
-// functions that the C entry points (kie_paged.cu) call.
+// Shared by the paged-cache operators: rounding to the cache and activation types, and the launch functions that the C entry
+// points (kie_paged.cu) call.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -328,15 +328,78 @@ int kie_paged_extend(const kie_paged_extend_args *a, void *stream);
  * and n_free. Entries are moved as they are, here and in extend: one that is no page of the cache stays on the list
  * and is handed out again. No access leaves the pages for it: its rows get the slot -1 or one that the append skips, and
  * the attention leaves its positions out. A page that is released twice is handed out twice, to rows that then overwrite
- * each other. */
+ * each other.
+ * shares (int32 [n_blocks], NULL if no pages are shared) counts the further holders of each page, as kie_paged_fork keeps
+ * them: then the call is kie_paged_fork with parents[r] = done[r] ? -1 : r. A page goes back only when its last holder is
+ * done, and pages go on the list in the order of their ids; at most KIE_PAGED_MAX_FORK requests. */
 typedef struct {
   const uint8_t *done;
   const int32_t *lens, *n_free, *block_table;
   int64_t table_stride;
   int32_t *free_blocks, *lens_out, *n_free_out;
   int n_seqs, max_blocks, block_size, free_capacity;
+  int32_t *shares;
+  int n_blocks;
 } kie_paged_release_args;
 int kie_paged_release(const kie_paged_release_args *a, void *stream);
+
+/* Several continuations of one prompt: every request r continues what request parents[r] held before the call (a step of
+ * a beam search; new samples of a prompt), sharing its pages. parents[r] = r or >= n_seqs: request r stays as it is;
+ * negative: it ends, as with kie_paged_release. Full pages are shared: shares[page] (int32 [n_blocks], 0 for pages with
+ * one holder or none, so that extend needs no part in it) counts the holders beyond the first. A last page that is filled
+ * only in part is written by the next append, so one continuation keeps it (the request itself, else the lowest r) and
+ * each of the others gets a new page, free_blocks[n_free - 1 - k] for the k-th of them in request order, into which the
+ * rows that are there have to be copied: copy_src[r], copy_dst[r], copy_rows[r] (-1, -1, 0 where there is nothing to
+ * copy), which kie_paged_copy takes as they are. Then pages without a holder (shares below 0) go back on the list, in
+ * the order of their ids and behind the pages that were not taken, with shares 0; those past free_capacity are dropped.
+ * If the new pages are more than n_free (taken within [0, free_capacity]), nothing changes: ok [1] (a byte) is 0, lens_out
+ * = lens, n_free_out = n_free, nothing to copy. Written: the entries of block_table that hold positions of continued
+ * requests (the others stay), shares, free_blocks, lens_out [n_seqs] (the parent's length, 0 where the request ends),
+ * n_free_out [1], ok and the three copy arrays [n_seqs]. lens_out and n_free_out must not be lens and n_free. Entries of
+ * the table that are no pages are moved like the others and counted nowhere. n_seqs <= KIE_PAGED_MAX_FORK; workspace:
+ * n_seqs * max_blocks * 4 bytes, 16-byte aligned, contents arbitrary before and after; calls that may overlap need one each. */
+#define KIE_PAGED_MAX_FORK 16384
+typedef struct {
+  const int32_t *parents, *lens, *n_free;
+  int32_t *block_table;
+  int64_t table_stride;
+  int32_t *shares, *free_blocks, *lens_out, *n_free_out, *copy_src, *copy_dst, *copy_rows;
+  uint8_t *ok;
+  void *workspace;
+  size_t workspace_bytes;
+  int n_seqs, max_blocks, block_size, n_blocks, free_capacity;
+} kie_paged_fork_args;
+int kie_paged_fork(const kie_paged_fork_args *a, void *stream);
+
+/* Pages copied inside a cache, K, V and scales of all layers: for each i, positions 0 .. rows[i] - 1 (rows NULL: all) of
+ * page src[i] to page dst[i]. pages describes layer 0; the others follow k_layer_stride .. v_scale_layer_stride elements
+ * apart (K and V: multiples of 16 bytes, from 0 to below 2^40; not read for one layer). A pair with a page outside [0,
+ * n_blocks), or of a page with itself, is left out. No page may be both a source and a destination, and no two
+ * destinations may be the same. n_pairs * n_layers < 2^30. */
+typedef struct {
+  kie_pages pages;
+  int64_t k_layer_stride, v_layer_stride, k_scale_layer_stride, v_scale_layer_stride;
+  const int32_t *src, *dst, *rows;
+  int n_pairs, n_layers;
+} kie_paged_copy_args;
+int kie_paged_copy(const kie_paged_copy_args *a, void *stream);
+
+/* A cache's pages moved together at its beginning (so that a smaller one can take its place, or its end be given back).
+ * The pages listed in free_blocks[0 .. n_free) are free (entries outside [0, n_blocks) do not count, repeated ones count
+ * once), the other n_live are in use, by the table or by others. Pages in use from n_live on move, in the order of their ids,
+ * to the free ones below it, in theirs: src, dst [n_blocks / 2] list the moves (-1 behind the last) for kie_paged_copy, and
+ * page_map [n_blocks] holds the new id of each page in use, -1 for the free ones, for whoever else knows pages by id. In
+ * place: block_table (the entries of the rows' positions), shares [n_blocks] (0 for free pages) and free_blocks, which is
+ * n_blocks - 1, ..., n_live from the bottom, so that n_live is given next; n_free_out [1] (free_capacity at most) must not
+ * be n_free. The copies have to come before the next append or attention. */
+typedef struct {
+  const int32_t *lens, *n_free;
+  int32_t *block_table;
+  int64_t table_stride;
+  int32_t *shares, *free_blocks, *n_free_out, *src, *dst, *page_map;
+  int n_seqs, max_blocks, block_size, n_blocks, free_capacity;
+} kie_paged_compact_args;
+int kie_paged_compact(const kie_paged_compact_args *a, void *stream);
 
 /* K/V rows into their slots: row t of k and v ([n_rows] x [n_kv_heads] x [head_dim], strides {row, head} in
  * elements, head_dim contiguous) goes to slot slots[t] of the pages, and q, if given, to q_out (the same type;
@@ -401,6 +464,50 @@ typedef struct {
   int n_table;
 } kie_paged_attention_args;
 int kie_paged_attention(const kie_paged_attention_args *a, void *stream);
+
+/* kie_paged_attention for sequences that share their beginnings, whose pages are read once for all of them. `a` is as
+ * for kie_paged_attention, with window 0. The query rows (with lens or with seqs and positions) come in n_groups groups of
+ * neighbours: group g is rows group_start[g] .. group_start[g + 1] - 1 (int32 [n_groups + 1] on the device, taken within
+ * [0, n_seqs], a start below an earlier one as that one), and its positions below prefix_lens[g] (any length; what is
+ * behind a row's own end is left out for that row) are read through the block table row of the longest of its query rows
+ * (the first of those that reach the prefix's end); the positions behind, and those of rows in no group, through each
+ * row's own. Rows of one sequence, a part of a prompt, are
+ * such a group too: its prefix is what was cached before. n_groups <= KIE_PAGED_MAX_GROUPS; n_groups = 0 is
+ * kie_paged_attention. The limits and the treatment of infinities are those of kie_paged_attention; a NaN or an infinity
+ * in a prefix concerns the rows of its group alone.
+ * a.workspace: kie_paged_prefix_attention_workspace bytes, 256-byte aligned, contents arbitrary before and after; calls
+ * that may overlap need one each. */
+#define KIE_PAGED_MAX_GROUPS 4096
+typedef struct {
+  kie_paged_attention_args a;
+  const int32_t *group_start, *prefix_lens;
+  int n_groups;
+} kie_paged_prefix_attention_args;
+int kie_paged_prefix_attention(const kie_paged_prefix_attention_args *a, void *stream);
+
+/* Bytes of kie_paged_prefix_attention's workspace on the current device (0: bad arguments or no device). */
+size_t kie_paged_prefix_attention_workspace(int n_seqs, int n_heads, int n_kv_heads, int head_dim);
+
+/* ---- log probabilities of tokens -------------------------------------------------------------------------
+ * What a program reads off the logits besides the argmax: for each of n_rows rows of `vocab` logits (dtype KIE_F16,
+ * KIE_BF16 or KIE_F32, row_stride elements apart, >= vocab), with p = softmax(logits): logprob [n_rows] = ln p of
+ * tokens[row] (int32; 0 for a token outside [0, vocab), as in padding; tokens and logprob may both be NULL), entropy
+ * [n_rows] = -sum p ln p (may be NULL), and the `top` largest logits in descending order, the lowest id first among equal
+ * ones: top_ids int32, top_logprobs [n_rows][top] (NULL if top is 0). All results fp32. A logit of -inf is a token that
+ * is ruled out: probability 0, ln p = -inf, nothing added to the entropy; a row of only such logits has ln p = -inf
+ * everywhere and entropy 0. A NaN or +inf in a row makes its logprob, entropy and top_logprobs NaN; its top_ids count a
+ * NaN as larger than +inf. 1 <= vocab < 2^30, 0 <= top <= min(vocab, KIE_MAX_TOP). Enqueued on `stream` like the paged
+ * operators, whose kie_paged_last_error holds its messages; nothing is allocated. */
+#define KIE_MAX_TOP 32
+typedef struct {
+  const void *logits;
+  int64_t row_stride;
+  const int32_t *tokens;
+  float *logprob, *entropy, *top_logprobs;
+  int32_t *top_ids;
+  int n_rows, vocab, top, dtype;
+} kie_token_logprobs_args;
+int kie_token_logprobs(const kie_token_logprobs_args *a, void *stream);
 
 /* Bytes of kie_paged_attention's workspace on the current device, for any number of sequences (0: bad arguments or
  * no device). */

@@ -24,7 +24,8 @@ _BUILD = os.path.join(_ROOT, "_build")
 LIB_PATH = os.path.join(_HERE, "libkie.so")
 BINDING_PATH, BINDING_SOURCE = os.path.join(_HERE, "_paged.so"), "kie_paged_py.cpp"
 BINDING_ENV_PATH = os.path.join(_BUILD, "_paged.env")  # what _paged.so was compiled against
-SOURCES = ("kie_api.cu", "kie_decode.cu", "kie_gemv.cu", "kie_prefill.cu", "kie_paged.cu", "kie_paged_attn.cu")
+SOURCES = ("kie_api.cu", "kie_decode.cu", "kie_gemv.cu", "kie_prefill.cu", "kie_paged.cu", "kie_paged_attn.cu",
+           "kie_prefix_attn.cu", "kie_pages.cu", "kie_logprobs.cu")
 HEADERS = ("kie_layout.h", "kie_device.cuh", "kie_decode.cuh", "kie_prefill.cuh", "kie_tcgemm.cuh", "kie_tcattn.cuh",
            "kie_paged.cuh")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -199,7 +200,34 @@ class KiePagedExtendArgs(ctypes.Structure):
 class KiePagedReleaseArgs(ctypes.Structure):
     _fields_ = [(n, P) for n in ("done", "lens", "n_free", "block_table")] + [("table_stride", ctypes.c_int64)] + \
                [(n, P) for n in ("free_blocks", "lens_out", "n_free_out")] + \
-               [(n, ctypes.c_int) for n in ("n_seqs", "max_blocks", "block_size", "free_capacity")]
+               [(n, ctypes.c_int) for n in ("n_seqs", "max_blocks", "block_size", "free_capacity")] + \
+               [("shares", P), ("n_blocks", ctypes.c_int)]
+
+
+class KiePagedForkArgs(ctypes.Structure):
+    _fields_ = [(n, P) for n in ("parents", "lens", "n_free", "block_table")] + [("table_stride", ctypes.c_int64)] + \
+               [(n, P) for n in ("shares", "free_blocks", "lens_out", "n_free_out", "copy_src", "copy_dst", "copy_rows", "ok",
+                                 "workspace")] + [("workspace_bytes", ctypes.c_size_t)] + \
+               [(n, ctypes.c_int) for n in ("n_seqs", "max_blocks", "block_size", "n_blocks", "free_capacity")]
+
+
+class KiePagedCopyArgs(ctypes.Structure):
+    _fields_ = [("pages", KiePages)] + \
+               [(n, ctypes.c_int64) for n in ("k_layer_stride", "v_layer_stride", "k_scale_layer_stride",
+                                              "v_scale_layer_stride")] + \
+               [(n, P) for n in ("src", "dst", "rows")] + [(n, ctypes.c_int) for n in ("n_pairs", "n_layers")]
+
+
+class KiePagedCompactArgs(ctypes.Structure):
+    _fields_ = [(n, P) for n in ("lens", "n_free", "block_table")] + [("table_stride", ctypes.c_int64)] + \
+               [(n, P) for n in ("shares", "free_blocks", "n_free_out", "src", "dst", "page_map")] + \
+               [(n, ctypes.c_int) for n in ("n_seqs", "max_blocks", "block_size", "n_blocks", "free_capacity")]
+
+
+class KieTokenLogprobsArgs(ctypes.Structure):
+    _fields_ = [("logits", P), ("row_stride", ctypes.c_int64)] + \
+               [(n, P) for n in ("tokens", "logprob", "entropy", "top_logprobs", "top_ids")] + \
+               [(n, ctypes.c_int) for n in ("n_rows", "vocab", "top", "dtype")]
 
 
 class KiePagedAppendArgs(ctypes.Structure):
@@ -215,6 +243,10 @@ class KiePagedAttentionArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t), ("scale", ctypes.c_float)] + \
                [(n, ctypes.c_int) for n in ("n_seqs", "n_heads", "max_blocks", "window", "q_dtype")] + \
                [("seqs", P), ("positions", P), ("n_table", ctypes.c_int)]
+
+
+class KiePagedPrefixAttentionArgs(ctypes.Structure):
+    _fields_ = [("a", KiePagedAttentionArgs), ("group_start", P), ("prefix_lens", P), ("n_groups", ctypes.c_int)]
 
 
 # Every entry point of include/kie.h with its ctypes signature.
@@ -256,6 +288,12 @@ SIGNATURES = {
     "kie_paged_append": ([P, P], ctypes.c_int),
     "kie_paged_attention": ([P, P], ctypes.c_int),
     "kie_paged_attention_workspace": ([ctypes.c_int] * 3, ctypes.c_size_t),
+    "kie_paged_prefix_attention": ([P, P], ctypes.c_int),
+    "kie_paged_prefix_attention_workspace": ([ctypes.c_int] * 4, ctypes.c_size_t),
+    "kie_paged_fork": ([P, P], ctypes.c_int),
+    "kie_paged_copy": ([P, P], ctypes.c_int),
+    "kie_paged_compact": ([P, P], ctypes.c_int),
+    "kie_token_logprobs": ([P, P], ctypes.c_int),
     "kie_paged_last_error": ([], ctypes.c_char_p),
 }
 
@@ -540,5 +578,6 @@ def rows_of_cta(M: int, n_cta: int, cta: int):
 
 
 # ---- paged K/V cache for a batch of sequences ----------------------------------------------------------------
-from .paged import (PagedCache, PagedStep, paged_append, paged_attention, paged_extend,  # noqa: E402,F401
-                    paged_release, rope_table)
+from .paged import (PagedCache, PagedFork, PagedMoves, PagedStep, TokenLogprobs, paged_append,  # noqa: E402,F401
+                    paged_attention, paged_compact, paged_copy, paged_extend, paged_fork, paged_prefix_attention,
+                    paged_release, rope_table, token_logprobs)

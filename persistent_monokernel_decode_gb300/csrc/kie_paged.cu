@@ -471,6 +471,50 @@ bool repeats(const int64_t (&stride)[N], const int (&size)[N]) {
   return false;
 }
 
+// What both attentions ask of their arguments, all but the workspace.
+const char *check_attention(const kie_paged_attention_args &a) {
+  if (const char *e = check_pages(a.pages)) return e;
+  if (a.n_seqs < 0 || a.max_blocks < 1 || a.window < 0) return "n_seqs and window must be >= 0 and max_blocks >= 1";
+  if ((int64_t)a.max_blocks * a.pages.block_size > 1 << 30) return "max_blocks * block_size must not pass 2^30";
+  if (a.n_heads < 1 || a.n_heads % a.pages.n_kv_heads) return "n_heads must be a multiple of n_kv_heads";
+  if (a.n_heads / a.pages.n_kv_heads > PAGED_MAX_GROUP) return "more than 8 query heads per KV head";
+  if ((int64_t)a.n_seqs * a.n_heads > INT_MAX) return "n_seqs * n_heads must be below 2^31";
+  if (!activation(a.q_dtype)) return "q is KIE_F16, KIE_BF16 or KIE_F32";
+  if (a.pages.dtype == KIE_BF16 && a.q_dtype != KIE_BF16) return "BF16 pages take BF16 queries";
+  if (a.pages.dtype == KIE_F16 && a.q_dtype == KIE_BF16) return "F16 pages take F16 or F32 queries";
+  if (!(a.scale == a.scale) || a.scale - a.scale != 0.f) return "scale must be finite";
+  if (a.n_seqs == 0) return nullptr;
+  if (!a.q || !a.out || !a.block_table) return "q, out or block_table is NULL";
+  if (!a.seqs != !a.positions) return "seqs and positions go together";
+  if (!a.seqs == !a.lens) return "either lens or seqs and positions must be given, the other NULL";
+  if (a.seqs && a.n_table < 0) return "n_table must be >= 0";
+  if ((a.seqs ? a.n_table : a.n_seqs) > 1 && a.table_stride < a.max_blocks) return "table_stride is below max_blocks";
+  if (!ints_aligned({a.block_table, a.lens, a.seqs, a.positions, a.lse}))
+    return "block_table, lens, seqs, positions or lse is not 4-byte aligned";
+  if (!aligned(a.q, paged_dtype_bytes(a.q_dtype)) || !aligned(a.out, paged_dtype_bytes(a.q_dtype)))
+    return "q or out is not aligned to its elements";
+  if ((double)a.n_seqs * a.max_blocks * a.pages.block_size * a.pages.n_kv_heads > 0x1p45)
+    return "n_seqs * max_blocks * block_size * n_kv_heads must not pass 2^45";
+  if (a.out == a.q && ((a.n_seqs > 1 && a.out_stride[0] != a.q_stride[0]) || (a.n_heads > 1 && a.out_stride[1] != a.q_stride[1])))
+    return "out in place of q needs q's strides";
+  if (repeats(a.out_stride, {a.n_seqs, a.n_heads})) return "out has a stride of 0 (an expanded tensor)";
+  return nullptr;
+}
+
+// Pages that a call writes to.
+const char *check_written_pages(const kie_pages &pg) {
+  for (const auto *st : {&pg.k_stride, &pg.v_stride, &pg.k_scale_stride, &pg.v_scale_stride})
+    if ((pg.dtype == KIE_E4M3 || st == &pg.k_stride || st == &pg.v_stride) &&
+        repeats(*st, {pg.n_blocks, pg.n_kv_heads, pg.block_size}))
+      return "pages or scales that are written have a stride of 0 (an expanded tensor)";
+  return nullptr;
+}
+
+bool heads_fit(int n_heads, int n_kv_heads, int head_dim) {
+  return n_kv_heads >= 1 && n_heads >= 1 && n_heads % n_kv_heads == 0 && n_heads / n_kv_heads <= PAGED_MAX_GROUP &&
+         (head_dim == 64 || head_dim == 128);
+}
+
 bool sm_count(int *dev, int *sms) {
   return cudaGetDevice(dev) == cudaSuccess &&
          cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) == cudaSuccess;
@@ -520,12 +564,32 @@ int kie_paged_release(const kie_paged_release_args *p, void *stream) {
   if (a.n_seqs > 0 && (!a.lens || !a.done || !a.block_table || !a.lens_out)) return refuse("an array of the requests is NULL");
   if (a.free_capacity > 0 && !a.free_blocks) return refuse("free_blocks is NULL");
   if (a.n_seqs > 1 && a.table_stride < a.max_blocks) return refuse("table_stride is below max_blocks");
-  if (!ints_aligned({a.lens, a.n_free, a.block_table, a.free_blocks, a.lens_out, a.n_free_out}))
+  if (a.shares && a.n_blocks < 1) return refuse("shares need n_blocks >= 1");
+  if (a.shares && a.n_seqs > KIE_PAGED_MAX_FORK) return refuse("more than KIE_PAGED_MAX_FORK requests with shared pages");
+  if (!ints_aligned({a.lens, a.n_free, a.block_table, a.free_blocks, a.lens_out, a.n_free_out, a.shares}))
     return refuse("an int32 array is not 4-byte aligned");
   if (a.n_free_out == a.n_free || (a.n_seqs > 0 && a.lens_out == a.lens))
     return refuse("lens_out and n_free_out must not be the inputs");
   int dev, sms;
   if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
+  if (a.shares) {
+    ForkArgs f = {};
+    f.done = a.done;
+    f.lens = a.lens;
+    f.n_free = a.n_free;
+    f.block_table = const_cast<int32_t *>(a.block_table);  // rows that end or stay as they are change nothing in it
+    f.table_stride = a.table_stride;
+    f.shares = a.shares;
+    f.free_blocks = a.free_blocks;
+    f.lens_out = a.lens_out;
+    f.n_free_out = a.n_free_out;
+    f.n_seqs = a.n_seqs;
+    f.max_blocks = a.max_blocks;
+    f.block_size = a.block_size;
+    f.n_blocks = a.n_blocks;
+    f.free_capacity = a.free_capacity;
+    return finish(kie_launch_paged_fork(f, dev, (cudaStream_t)stream), "paged_release");
+  }
   const int teams = PX_THREADS / px_team(a.n_seqs <= PX_THREADS ? 1 : 4);
   const int grid = std::min(sms, std::max(1, (a.n_seqs + teams - 1) / teams));
   auto *kernel = a.n_seqs <= PX_THREADS ? paged_release_kernel<1> : paged_release_kernel<4>;
@@ -551,11 +615,7 @@ int kie_paged_append(const kie_paged_append_args *p, void *stream) {
   const int64_t heads = (a.q ? a.n_heads : 0) + 2ll * a.pages.n_kv_heads, groups = (heads + PP_HEADS - 1) / PP_HEADS;
   if (a.n_rows * groups * PP_HEADS > 1ll << 28) return refuse("too many rows x heads (2^28 at most)");
   if (a.q && repeats(a.q_out_stride, {a.n_rows, a.n_heads})) return refuse("q_out has a stride of 0 (an expanded tensor)");
-  const kie_pages &pg = a.pages;
-  for (const auto *st : {&pg.k_stride, &pg.v_stride, &pg.k_scale_stride, &pg.v_scale_stride})
-    if ((pg.dtype == KIE_E4M3 || st == &pg.k_stride || st == &pg.v_stride) &&
-        repeats(*st, {pg.n_blocks, pg.n_kv_heads, pg.block_size}))
-      return refuse("pages or scales that are written have a stride of 0 (an expanded tensor)");
+  if (const char *e = check_written_pages(a.pages)) return refuse(e);
   const int tph = a.pages.head_dim / 16;
   const int64_t warps = (a.n_rows + 32 / tph - 1) / (32 / tph) * groups;
   const unsigned grid = (unsigned)((warps * 32 + PP_THREADS - 1) / PP_THREADS);
@@ -575,44 +635,128 @@ int kie_paged_append(const kie_paged_append_args *p, void *stream) {
 
 size_t kie_paged_attention_workspace(int n_heads, int n_kv_heads, int head_dim) {
   int dev, sms;
-  if (n_kv_heads < 1 || n_heads < 1 || n_heads % n_kv_heads || n_heads / n_kv_heads > PAGED_MAX_GROUP ||
-      (head_dim != 64 && head_dim != 128) || !sm_count(&dev, &sms))
-    return 0;
+  if (!heads_fit(n_heads, n_kv_heads, head_dim) || !sm_count(&dev, &sms)) return 0;
   return kie_paged_attention_workspace_bytes(n_heads, n_kv_heads, head_dim, sms);
 }
 
 int kie_paged_attention(const kie_paged_attention_args *p, void *stream) {
   if (!p) return refuse("the arguments are NULL");
   const kie_paged_attention_args &a = *p;
-  if (const char *e = check_pages(a.pages)) return refuse(e);
-  if (a.n_seqs < 0 || a.max_blocks < 1 || a.window < 0) return refuse("n_seqs and window must be >= 0 and max_blocks >= 1");
-  if ((int64_t)a.max_blocks * a.pages.block_size > 1 << 30) return refuse("max_blocks * block_size must not pass 2^30");
-  if (a.n_heads < 1 || a.n_heads % a.pages.n_kv_heads) return refuse("n_heads must be a multiple of n_kv_heads");
-  if (a.n_heads / a.pages.n_kv_heads > PAGED_MAX_GROUP) return refuse("more than 8 query heads per KV head");
-  if ((int64_t)a.n_seqs * a.n_heads > INT_MAX) return refuse("n_seqs * n_heads must be below 2^31");
-  if (!activation(a.q_dtype)) return refuse("q is KIE_F16, KIE_BF16 or KIE_F32");
-  if (a.pages.dtype == KIE_BF16 && a.q_dtype != KIE_BF16) return refuse("BF16 pages take BF16 queries");
-  if (a.pages.dtype == KIE_F16 && a.q_dtype == KIE_BF16) return refuse("F16 pages take F16 or F32 queries");
-  if (!(a.scale == a.scale) || a.scale - a.scale != 0.f) return refuse("scale must be finite");
+  if (const char *e = check_attention(a)) return refuse(e);
   if (a.n_seqs == 0) return KIE_OK;
-  if (!a.q || !a.out || !a.block_table) return refuse("q, out or block_table is NULL");
-  if (!a.seqs != !a.positions) return refuse("seqs and positions go together");
-  if (!a.seqs == !a.lens) return refuse("either lens or seqs and positions must be given, the other NULL");
-  if (a.seqs && a.n_table < 0) return refuse("n_table must be >= 0");
-  if ((a.seqs ? a.n_table : a.n_seqs) > 1 && a.table_stride < a.max_blocks) return refuse("table_stride is below max_blocks");
-  if (!ints_aligned({a.block_table, a.lens, a.seqs, a.positions, a.lse}))
-    return refuse("block_table, lens, seqs, positions or lse is not 4-byte aligned");
-  if (!aligned(a.q, paged_dtype_bytes(a.q_dtype)) || !aligned(a.out, paged_dtype_bytes(a.q_dtype)))
-    return refuse("q or out is not aligned to its elements");
-  if ((double)a.n_seqs * a.max_blocks * a.pages.block_size * a.pages.n_kv_heads > 0x1p45)
-    return refuse("n_seqs * max_blocks * block_size * n_kv_heads must not pass 2^45");
-  if (a.out == a.q && ((a.n_seqs > 1 && a.out_stride[0] != a.q_stride[0]) || (a.n_heads > 1 && a.out_stride[1] != a.q_stride[1])))
-    return refuse("out in place of q needs q's strides");
-  if (repeats(a.out_stride, {a.n_seqs, a.n_heads})) return refuse("out has a stride of 0 (an expanded tensor)");
   int dev, sms;
   if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
   const size_t need = kie_paged_attention_workspace_bytes(a.n_heads, a.pages.n_kv_heads, a.pages.head_dim, sms);
   if (!a.workspace || a.workspace_bytes < need || !aligned(a.workspace, 256))
     return refuse("the workspace is NULL, unaligned (256 bytes) or smaller than kie_paged_attention_workspace");
   return finish(kie_launch_paged_attention(a, dev, sms, (cudaStream_t)stream), "paged_attention");
+}
+
+size_t kie_paged_prefix_attention_workspace(int n_seqs, int n_heads, int n_kv_heads, int head_dim) {
+  int dev, sms;
+  if (n_seqs < 0 || !heads_fit(n_heads, n_kv_heads, head_dim) || !sm_count(&dev, &sms)) return 0;
+  return kie_paged_prefix_workspace_bytes(n_seqs, n_heads, n_kv_heads, head_dim, sms);
+}
+
+int kie_paged_prefix_attention(const kie_paged_prefix_attention_args *p, void *stream) {
+  if (!p) return refuse("the arguments are NULL");
+  const kie_paged_attention_args &a = p->a;
+  if (const char *e = check_attention(a)) return refuse(e);
+  if (p->n_groups < 0 || p->n_groups > KIE_PAGED_MAX_GROUPS) return refuse("n_groups must be from 0 to KIE_PAGED_MAX_GROUPS");
+  if (a.window != 0) return refuse("attention of groups takes no window");
+  if (p->n_groups > 0 && (!p->group_start || !p->prefix_lens)) return refuse("group_start or prefix_lens is NULL");
+  if (!ints_aligned({p->group_start, p->prefix_lens})) return refuse("group_start or prefix_lens is not 4-byte aligned");
+  if (a.n_seqs == 0) return KIE_OK;
+  int dev, sms;
+  if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
+  const size_t need = kie_paged_prefix_workspace_bytes(a.n_seqs, a.n_heads, a.pages.n_kv_heads, a.pages.head_dim, sms);
+  if (!a.workspace || a.workspace_bytes < need || !aligned(a.workspace, 256))
+    return refuse("the workspace is NULL, unaligned (256 bytes) or smaller than kie_paged_prefix_attention_workspace");
+  return finish(p->n_groups ? kie_launch_paged_prefix(*p, dev, sms, (cudaStream_t)stream)
+                            : kie_launch_paged_attention(a, dev, sms, (cudaStream_t)stream), "paged_prefix_attention");
+}
+
+int kie_paged_fork(const kie_paged_fork_args *p, void *stream) {
+  if (!p) return refuse("the arguments are NULL");
+  const kie_paged_fork_args &a = *p;
+  if (a.n_seqs < 0 || a.max_blocks < 1 || a.free_capacity < 0 || a.n_blocks < 1)
+    return refuse("n_seqs and free_capacity must be >= 0, max_blocks and n_blocks >= 1");
+  if (a.n_seqs > KIE_PAGED_MAX_FORK) return refuse("n_seqs must not pass KIE_PAGED_MAX_FORK");
+  if (a.block_size < PAGED_ROWS || a.block_size % PAGED_ROWS) return refuse("block_size must be a positive multiple of 16");
+  if ((int64_t)a.max_blocks * a.block_size > INT_MAX) return refuse("max_blocks * block_size must be below 2^31");
+  if (!a.n_free || !a.n_free_out || !a.ok || !a.shares) return refuse("n_free, n_free_out, ok or shares is NULL");
+  if (a.n_seqs > 0 && (!a.parents || !a.lens || !a.block_table || !a.lens_out || !a.copy_src || !a.copy_dst || !a.copy_rows))
+    return refuse("an array of the requests is NULL");
+  if (a.free_capacity > 0 && !a.free_blocks) return refuse("free_blocks is NULL");
+  if (a.n_seqs > 1 && a.table_stride < a.max_blocks) return refuse("table_stride is below max_blocks");
+  if (!ints_aligned({a.parents, a.lens, a.n_free, a.block_table, a.shares, a.free_blocks, a.lens_out, a.n_free_out, a.copy_src,
+                     a.copy_dst, a.copy_rows}))
+    return refuse("an int32 array is not 4-byte aligned");
+  if (a.n_free_out == a.n_free || (a.n_seqs > 0 && (a.lens_out == a.lens || a.lens_out == a.parents)))
+    return refuse("lens_out and n_free_out must not be the inputs");
+  if (a.n_seqs > 0 && (!a.workspace || !aligned(a.workspace, 16) || a.workspace_bytes < (size_t)a.n_seqs * a.max_blocks * 4))
+    return refuse("the workspace is NULL, unaligned (16 bytes) or smaller than n_seqs * max_blocks * 4 bytes");
+  int dev, sms;
+  if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
+  ForkArgs f = {};
+  static_cast<kie_paged_fork_args &>(f) = a;
+  return finish(kie_launch_paged_fork(f, dev, (cudaStream_t)stream), "paged_fork");
+}
+
+int kie_paged_copy(const kie_paged_copy_args *p, void *stream) {
+  if (!p) return refuse("the arguments are NULL");
+  const kie_paged_copy_args &a = *p;
+  if (const char *e = check_pages(a.pages)) return refuse(e);
+  const kie_pages &pg = a.pages;
+  if (a.n_pairs < 0 || a.n_layers < 1) return refuse("n_pairs must be >= 0 and n_layers >= 1");
+  if ((int64_t)a.n_pairs * a.n_layers >= 1 << 30) return refuse("n_pairs * n_layers must be below 2^30");
+  if ((int64_t)pg.n_kv_heads * pg.block_size * (pg.head_dim / 8) > INT_MAX) return refuse("the pages are too large");
+  const int unit = 16 / paged_dtype_bytes(pg.dtype);
+  if (a.n_layers > 1) {
+    for (const int64_t s : {a.k_layer_stride, a.v_layer_stride})
+      if (s <= 0 || s >= 1ll << 40 || s % unit) return refuse("layer strides are multiples of 16 bytes, above 0 and below 2^40");
+    for (const int64_t s : {a.k_scale_layer_stride, a.v_scale_layer_stride})
+      if (pg.dtype == KIE_E4M3 && (s <= 0 || s >= 1ll << 40)) return refuse("layer strides of scales are above 0 and below 2^40");
+  }
+  if (const char *e = check_written_pages(pg)) return refuse(e);
+  if (a.n_pairs == 0) return KIE_OK;
+  if (!a.src || !a.dst) return refuse("src or dst is NULL");
+  if (!ints_aligned({a.src, a.dst, a.rows})) return refuse("an int32 array is not 4-byte aligned");
+  return finish(kie_launch_paged_copy(a, (cudaStream_t)stream), "paged_copy");
+}
+
+int kie_paged_compact(const kie_paged_compact_args *p, void *stream) {
+  if (!p) return refuse("the arguments are NULL");
+  const kie_paged_compact_args &a = *p;
+  if (a.n_seqs < 0 || a.max_blocks < 1 || a.free_capacity < 0 || a.n_blocks < 1)
+    return refuse("n_seqs and free_capacity must be >= 0, max_blocks and n_blocks >= 1");
+  if (a.block_size < PAGED_ROWS || a.block_size % PAGED_ROWS) return refuse("block_size must be a positive multiple of 16");
+  if ((int64_t)a.max_blocks * a.block_size > INT_MAX) return refuse("max_blocks * block_size must be below 2^31");
+  if (!a.n_free || !a.n_free_out || !a.shares || !a.page_map) return refuse("n_free, n_free_out, shares or page_map is NULL");
+  if (a.n_blocks > 1 && (!a.src || !a.dst)) return refuse("src or dst is NULL");
+  if (a.n_seqs > 0 && (!a.lens || !a.block_table)) return refuse("an array of the requests is NULL");
+  if (a.free_capacity > 0 && !a.free_blocks) return refuse("free_blocks is NULL");
+  if (a.n_seqs > 1 && a.table_stride < a.max_blocks) return refuse("table_stride is below max_blocks");
+  if (!ints_aligned({a.lens, a.n_free, a.block_table, a.shares, a.free_blocks, a.n_free_out, a.src, a.dst, a.page_map}))
+    return refuse("an int32 array is not 4-byte aligned");
+  if (a.n_free_out == a.n_free) return refuse("n_free_out must not be n_free");
+  return finish(kie_launch_paged_compact(a, (cudaStream_t)stream), "paged_compact");
+}
+
+int kie_token_logprobs(const kie_token_logprobs_args *p, void *stream) {
+  if (!p) return refuse("the arguments are NULL");
+  const kie_token_logprobs_args &a = *p;
+  if (a.n_rows < 0 || a.vocab < 1 || a.vocab >= 1 << 30) return refuse("n_rows must be >= 0 and vocab from 1 to below 2^30");
+  if (a.top < 0 || a.top > KIE_MAX_TOP || a.top > a.vocab) return refuse("top must be from 0 to KIE_MAX_TOP and at most vocab");
+  if (!activation(a.dtype)) return refuse("logits are KIE_F16, KIE_BF16 or KIE_F32");
+  if (a.n_rows > 1 && (a.row_stride < a.vocab || a.row_stride >= 1ll << 40)) return refuse("row_stride is below vocab, or not below 2^40");
+  if (!a.tokens != !a.logprob) return refuse("tokens and logprob go together");
+  if (a.n_rows == 0) return KIE_OK;
+  if (!a.logits) return refuse("logits is NULL");
+  if (a.top > 0 && (!a.top_ids || !a.top_logprobs)) return refuse("top_ids or top_logprobs is NULL");
+  if (!aligned(a.logits, paged_dtype_bytes(a.dtype))) return refuse("logits is not aligned to its elements");
+  if (!ints_aligned({a.tokens, a.logprob, a.entropy, a.top_ids, a.top_logprobs})) return refuse("an array is not 4-byte aligned");
+  int dev, sms;
+  if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
+  return finish(kie_launch_token_logprobs(a, sms, (cudaStream_t)stream), "token_logprobs");
 }

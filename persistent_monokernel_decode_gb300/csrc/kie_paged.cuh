@@ -85,5 +85,45 @@ cudaError_t launch_after_previous(K kernel, unsigned grid, unsigned threads, siz
 
 }  // namespace kie
 
+namespace kie {
+
+// A fork, or (done given, in the place of parents) the release of rows whose pages are shared.
+struct ForkArgs : kie_paged_fork_args {
+  const uint8_t *done;
+};
+
+// An attention of groups with a common prefix, as its kernels take it. The kernel of the prefixes leaves, for each query
+// row, how many of its positions the group has read for it, and what came of them.
+struct PrefixArgs : kie_paged_attention_args {
+  const int32_t *group_start, *prefix_lens;
+  int n_groups;
+  int32_t *row_lo;
+  float *prefix;
+};
+
+// The kernels find the rows' ends in lens, be they lengths or a step's positions, and the number of table rows in n_table.
+inline kie_paged_attention_args rows_in_lens(kie_paged_attention_args a) {
+  if (a.seqs)
+    a.lens = a.positions;
+  else
+    a.n_table = a.n_seqs;
+  return a;
+}
+
+// Positions of query row b. Rows of a step (a.seqs) end with their own position.
+__device__ __forceinline__ int row_len(const kie_paged_attention_args &a, int b) {
+  const int own = a.seqs ? 1 : 0;
+  return min(max(a.lens[b], -own), a.max_blocks * a.pages.block_size - own) + own;
+}
+
+}  // namespace kie
+
+cudaError_t kie_launch_paged_fork(const kie::ForkArgs &a, int dev, cudaStream_t stream);
+cudaError_t kie_launch_paged_compact(const kie_paged_compact_args &a, cudaStream_t stream);
+cudaError_t kie_launch_paged_copy(const kie_paged_copy_args &a, cudaStream_t stream);
+cudaError_t kie_launch_token_logprobs(const kie_token_logprobs_args &a, int sms, cudaStream_t stream);
+cudaError_t kie_launch_paged_suffix(const kie::PrefixArgs &a, int dev, int sms, cudaStream_t stream);
+cudaError_t kie_launch_paged_prefix(const kie_paged_prefix_attention_args &a, int dev, int sms, cudaStream_t stream);
+size_t kie_paged_prefix_workspace_bytes(int n_seqs, int n_heads, int n_kv_heads, int head_dim, int sms);
 cudaError_t kie_launch_paged_attention(const kie_paged_attention_args &a, int dev, int sms, cudaStream_t stream);
 size_t kie_paged_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim, int sms);

@@ -28,6 +28,7 @@
 #include <float.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kie_device.cuh"
 #include "kie_paged.cuh"
@@ -172,12 +173,14 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
 struct Span {
   int lo, len, from, n;
 };
-template <int UNIT>
-__device__ __forceinline__ Span span_of(const kie_paged_attention_args &a, int b) {
+template <int UNIT, class A>
+__device__ __forceinline__ Span span_of(const A &a, int b) {
   Span s;
-  const int own = a.seqs ? 1 : 0;
-  s.len = min(max(a.lens[b], -own), a.max_blocks * a.pages.block_size - own) + own;
-  s.lo = a.window > 0 ? max(0, s.len - a.window) : 0;
+  s.len = row_len(a, b);
+  if constexpr (std::is_same<A, PrefixArgs>::value)
+    s.lo = a.row_lo[b];  // the positions before are the group's
+  else
+    s.lo = a.window > 0 ? max(0, s.len - a.window) : 0;
   s.from = s.lo & ~15;
   s.n = max(1, (int)((unsigned)(s.len - s.from + UNIT - 1) / UNIT));
   return s;
@@ -195,7 +198,8 @@ template <int UNIT>
 struct Cursor {
   Span s;
   int b, h, unit, v;
-  __device__ __forceinline__ void next(const kie_paged_attention_args &a) {
+  template <class A>
+  __device__ __forceinline__ void next(const A &a) {
     ++v;
     if (++unit < s.n) return;
     unit = 0;
@@ -214,8 +218,8 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
 // The number of places of this block's run (*end; 0 behind the list's end), the cursor at its first unit, and the
 // places of a full run (*per_block). Every thread gets the same; two block barriers. The cursor may stand at or past
 // *end: no units.
-template <int UNIT>
-__device__ __forceinline__ void locate(const kie_paged_attention_args &a, Cursor<UNIT> *c, int *end, long long *per_block) {
+template <int UNIT, class A>
+__device__ __forceinline__ void locate(const A &a, Cursor<UNIT> *c, int *end, long long *per_block) {
   __shared__ long long s_warp[PA_WARPS];
   __shared__ int s_b, s_h;
   __shared__ int s_off;
@@ -401,10 +405,25 @@ __device__ __forceinline__ void join_pieces(const Pieces &piece, int n, int grou
     if (me.r0 + q * S::STEP < group) put(me.r0 + q * S::STEP, me.d, acc[q], top[q], sum[q]);
 }
 
+// The positions that the row's group has read for it join its own.
+template <int DH>
+__device__ __forceinline__ void add_prefix(const PrefixArgs &a, int b, int64_t head, int d, float4 &acc, float &M, float &L) {
+  if (a.row_lo[b] <= 0) return;
+  const int64_t at = (int64_t)b * a.n_heads + head;
+  const float4 y = *reinterpret_cast<const float4 *>(a.prefix + at * DH + d);
+  const float2 ml = *reinterpret_cast<const float2 *>(a.prefix + (int64_t)a.n_seqs * a.n_heads * DH + 2 * at);
+  const float mn = fmaxf(M, ml.x), ref = mn == -INFINITY ? 0.f : mn, f = ex2(M - ref), g = ex2(ml.x - ref);
+  acc.x = fmaf(y.x, g, acc.x * f), acc.y = fmaf(y.y, g, acc.y * f);
+  acc.z = fmaf(y.z, g, acc.z * f), acc.w = fmaf(y.w, g, acc.w * f);
+  L = fmaf(ml.y, g, L * f);
+  M = mn;
+}
+
 // Four dimensions of a query head's output from its weighted sum, and its lse from the reference M (log2 units) and the
 // sum of weights L: zeros and -inf where nothing was attended. vec: the output is aligned for one store of four.
-__device__ __forceinline__ void finish4(const kie_paged_attention_args &a, bool vec, int b, int64_t head, int d, float4 acc,
-                                        float M, float L) {
+template <int DH, class A>
+__device__ __forceinline__ void finish4(const A &a, bool vec, int b, int64_t head, int d, float4 acc, float M, float L) {
+  if constexpr (std::is_same<A, PrefixArgs>::value) add_prefix<DH>(a, b, head, d, acc, M, L);
   const float inv = L == 0.f ? 0.f : rcp(L);
   const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
   const int64_t to = b * a.out_stride[0] + head * a.out_stride[1] + d;
@@ -432,15 +451,15 @@ __device__ __forceinline__ void put_piece(float *p, int group, int r, int d, flo
 
 // After this block has written its piece of item (b, h), whose `units` units begin at place v of the list: whoever of
 // the blocks that share it comes last joins the pieces.
-template <int DH>
-__device__ __forceinline__ void publish(const kie_paged_attention_args &a, unsigned long long call, int b, int h, long long v,
+template <int DH, class A>
+__device__ __forceinline__ void publish(const A &a, unsigned long long call, int b, int h, long long v,
                                         int units, long long per_block) {
   const Workspace ws(a, DH);
   const int first = (int)divide(v, per_block), last = (int)divide(v + units - 1, per_block);
   const int group = a.n_heads / a.pages.n_kv_heads, n = last - first + 1;
   const bool vec = out_vec(a);
   const auto finish = [&](int r, int d, float4 acc, float M, float L) {
-    finish4(a, vec, b, (int64_t)h * group + r, d, acc, M, L);
+    finish4<DH>(a, vec, b, (int64_t)h * group + r, d, acc, M, L);
   };
   const size_t step = PA_PIECES * ws.piece;
   if (n <= PA_ONE_LEVEL) {
@@ -499,9 +518,9 @@ __device__ __forceinline__ int join_col(int r, int d) {
   return d ^ (((r >> 1) & 3) << (KIND == PG_E4M3 ? 4 : 3));
 }
 
-template <int KIND, int DH, bool SPLIT>
+template <int KIND, int DH, bool SPLIT, class A>
 __global__ void __launch_bounds__(PA_THREADS, PaTile<KIND, DH>::BLOCKS)
-paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
+paged_attn_kernel(const A a, unsigned long long call) {
   using T = PaTile<KIND, DH>;
   using Sm = PaSmem<KIND, DH>;
   constexpr int NS = T::NS, CH = T::CH, ROW = T::ROW, ES = T::ES, SUBS = T::SUBS, LOADS = T::LOADS;
@@ -876,7 +895,7 @@ paged_attn_kernel(const kie_paged_attention_args a, unsigned long long call) {
           acc.z = fmaf(y.z, f[w], acc.z), acc.w = fmaf(y.w, f[w], acc.w);
         }
         if (whole)
-          finish4(a, vec, b, (int64_t)h * group + r, me.d, acc, M, L);
+          finish4<DH>(a, vec, b, (int64_t)h * group + r, me.d, acc, M, L);
         else
           put_piece<DH>(piece, group, r, me.d, acc, M, L);
       }
@@ -896,23 +915,23 @@ unsigned long long call_number() {
   return calls.fetch_add(0x3c6ef372fe94faull, std::memory_order_relaxed) & ((1ull << 56) - 1);
 }
 
-template <int KIND, int DH, bool SPLIT>
-cudaError_t launch(const kie_paged_attention_args &a, int dev, int sms, cudaStream_t stream) {
+template <int KIND, int DH, bool SPLIT, class A>
+cudaError_t launch(const A &a, int dev, int sms, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};  // devices whose limit of dynamic shared memory is raised
   const int smem = sizeof(PaSmem<KIND, DH>);
   const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
   if (!bit || !(ready.load(std::memory_order_relaxed) & bit)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(paged_attn_kernel<KIND, DH, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(paged_attn_kernel<KIND, DH, SPLIT, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  return launch_after_previous(paged_attn_kernel<KIND, DH, SPLIT>, sms * PaTile<KIND, DH>::BLOCKS, PA_THREADS, smem, stream, a,
+  return launch_after_previous(paged_attn_kernel<KIND, DH, SPLIT, A>, sms * PaTile<KIND, DH>::BLOCKS, PA_THREADS, smem, stream, a,
                                call_number());
 }
 
-template <int DH>
-cudaError_t launch_dh(const kie_paged_attention_args &a, int dev, int sms, cudaStream_t stream) {
+template <int DH, class A>
+cudaError_t launch_dh(const A &a, int dev, int sms, cudaStream_t stream) {
   if (a.pages.dtype == KIE_BF16) return launch<PG_BF16, DH, false>(a, dev, sms, stream);
   if (a.pages.dtype == KIE_E4M3) return launch<PG_E4M3, DH, true>(a, dev, sms, stream);
   return a.q_dtype == KIE_F32 ? launch<PG_F16, DH, true>(a, dev, sms, stream) : launch<PG_F16, DH, false>(a, dev, sms, stream);
@@ -927,10 +946,10 @@ size_t kie_paged_attention_workspace_bytes(int n_heads, int n_kv_heads, int head
 }
 
 cudaError_t kie_launch_paged_attention(const kie_paged_attention_args &args, int dev, int sms, cudaStream_t stream) {
-  kie_paged_attention_args a = args;
-  if (a.seqs)
-    a.lens = a.positions;
-  else
-    a.n_table = a.n_seqs;
+  const kie_paged_attention_args a = kie::rows_in_lens(args);
+  return a.pages.head_dim == 64 ? kie::launch_dh<64>(a, dev, sms, stream) : kie::launch_dh<128>(a, dev, sms, stream);
+}
+
+cudaError_t kie_launch_paged_suffix(const kie::PrefixArgs &a, int dev, int sms, cudaStream_t stream) {
   return a.pages.head_dim == 64 ? kie::launch_dh<64>(a, dev, sms, stream) : kie::launch_dh<128>(a, dev, sms, stream);
 }

@@ -1,8 +1,10 @@
 """A paged K/V cache for a batch of sequences: the ``kie_paged_*`` operators of include/kie.h on CUDA tensors.
 
-``paged_extend``, ``paged_append``, ``paged_attention`` and ``paged_release`` check types, shapes and devices, allocate
-their outputs with PyTorch and launch on the current stream of the tensors' device, without synchronising. What they
-marshal per call is done in native code (csrc/kie_paged_py.cpp). They are for inference: no gradients pass through them.
+``paged_extend``, ``paged_append``, ``paged_attention`` and ``paged_release``, and for sequences that share pages
+``paged_fork``, ``paged_copy``, ``paged_compact`` and ``paged_prefix_attention``, with ``token_logprobs`` beside them,
+check types, shapes and devices, allocate their outputs with PyTorch and launch on the current stream of the tensors'
+device, without synchronising. What they marshal per call is done in native code (csrc/kie_paged_py.cpp). They are for
+inference: no gradients pass through them.
 ``PagedCache`` holds the pages and tables that such a program keeps.
 """
 from __future__ import annotations
@@ -25,6 +27,34 @@ class PagedStep(NamedTuple):
     seqs: object
 
 
+class PagedFork(NamedTuple):
+    """What paged_fork computed (CUDA tensors): lens per request, n_free, ok (bool [1]), and the rows to copy for each
+    request, as paged_copy takes them."""
+    lens: object
+    n_free: object
+    ok: object
+    copy_src: object
+    copy_dst: object
+    copy_rows: object
+
+
+class PagedMoves(NamedTuple):
+    """What paged_compact computed (CUDA tensors): n_free; the moves src -> dst (-1 behind the last); page_map, the new id
+    of each page (-1: free)."""
+    n_free: object
+    src: object
+    dst: object
+    page_map: object
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs computed: logprob, entropy [N]; top_ids, top_logprobs [N, top]."""
+    logprob: object
+    entropy: object
+    top_ids: object
+    top_logprobs: object
+
+
 _ready = None
 
 
@@ -39,8 +69,10 @@ def _native():
         except ImportError as e:
             raise RuntimeError(f"the paged operators' binding cannot be loaded ({e}): run __graft_entry__.build() (or "
                                "persistent_monokernel_decode_gb300.build()) first") from e
-        _paged.bind(*[ctypes.cast(getattr(L, "kie_paged_" + n), ctypes.c_void_p).value
-                      for n in ("extend", "release", "append", "attention", "attention_workspace", "last_error")], KieError)
+        names = ("paged_extend", "paged_release", "paged_append", "paged_attention", "paged_attention_workspace",
+                 "paged_last_error", "paged_prefix_attention", "paged_prefix_attention_workspace", "paged_fork", "paged_copy",
+                 "paged_compact", "token_logprobs")
+        _paged.bind(*[ctypes.cast(getattr(L, "kie_" + n), ctypes.c_void_p).value for n in names], KieError)
         _ready = _paged
     return _ready
 
@@ -52,10 +84,40 @@ def paged_extend(new_lens, lens, block_table, free_blocks, n_free, block_size: i
     return PagedStep(*(_ready or _native()).extend(new_lens, lens, block_table, free_blocks, n_free, block_size, n_rows))
 
 
-def paged_release(done, lens, block_table, free_blocks, n_free, block_size: int):
+def paged_release(done, lens, block_table, free_blocks, n_free, block_size: int, shares=None):
     """Pages of the requests with done[r] (bool [R]) back onto free_blocks, in place (kie_paged_release). Returns
-    (lens, n_free): 0 for the finished requests, and the new number of free pages."""
-    return (_ready or _native()).release(done, lens, block_table, free_blocks, n_free, block_size)
+    (lens, n_free): 0 for the finished requests, and the new number of free pages. With shares (int32 [n_blocks], as
+    paged_fork keeps it) a page goes back when its last holder is done."""
+    return (_ready or _native()).release(done, lens, block_table, free_blocks, n_free, block_size, shares)
+
+
+def paged_fork(parents, lens, block_table, shares, free_blocks, n_free, block_size: int) -> PagedFork:
+    """Request r continues what request parents[r] (int32 [R]) held before the call, sharing its full pages; one of its own
+    number, or one from R on, leaves it as it is, a negative one ends it (kie_paged_fork). block_table, free_blocks and
+    shares (int32 [n_blocks]: the holders of each page beyond the first, zeros at first) are updated in place; the rows of
+    half-filled pages have to be copied by paged_copy(f.copy_src, f.copy_dst, ..., rows=f.copy_rows) before the next
+    append. If the free pages do not suffice, ok is False and nothing has changed."""
+    return PagedFork(*(_ready or _native()).fork(parents, lens, block_table, shares, free_blocks, n_free, block_size))
+
+
+def paged_copy(src, dst, k_cache, v_cache, *, rows=None, k_scale=None, v_scale=None) -> None:
+    """Pages src[i] to dst[i] (int32) inside a cache: k_cache and v_cache of all layers [n_layers, n_blocks, n_kv_heads,
+    block_size, head_dim], or of one, and their scales; rows (int32): only the first positions of each (kie_paged_copy).
+    Pairs with a page that is none, such as -1, are left out."""
+    (_ready or _native()).copy(src, dst, k_cache, v_cache, rows, k_scale, v_scale)
+
+
+def paged_compact(lens, block_table, shares, free_blocks, n_free, block_size: int) -> PagedMoves:
+    """The pages in use renumbered to lie at the cache's beginning (kie_paged_compact): block_table, shares and free_blocks
+    are updated in place, and paged_copy(m.src, m.dst, ...) has to move what they hold before the next append or attention."""
+    return PagedMoves(*(_ready or _native()).compact(lens, block_table, shares, free_blocks, n_free, block_size))
+
+
+def token_logprobs(logits, tokens, *, top: int = 0) -> TokenLogprobs:
+    """Log probabilities of tokens (int32 [N]; 0.0 where a token is none, such as -1) under softmax(logits), logits
+    float16, bfloat16 or float32 [N, vocab] with contiguous rows; the entropy of each row; and its `top` (32 at most) most
+    probable tokens in descending order, the lowest id first among equal ones (kie_token_logprobs)."""
+    return TokenLogprobs(*(_ready or _native()).logprobs(logits, tokens, top))
 
 
 def paged_append(k, v, k_cache, v_cache, slots, *, positions=None, rope=None, q=None, q_out=None, k_scale=None,
@@ -82,6 +144,16 @@ def paged_attention(q, k_cache, v_cache, block_table, lens, *, scale=None, windo
                                            return_lse, seqs, positions)
 
 
+def paged_prefix_attention(q, k_cache, v_cache, block_table, lens, group_start, prefix_lens, *, scale=None, k_scale=None,
+                           v_scale=None, out=None, return_lse: bool = False, seqs=None, positions=None):
+    """paged_attention (without a window) for rows that share beginnings, which are read once for all of them
+    (kie_paged_prefix_attention): rows group_start[g] .. group_start[g + 1] - 1 of q (int32 [G + 1]) have the same first
+    prefix_lens[g] positions (int32 [G]), read through the block table row of the group's longest row. Rows outside the
+    groups attend as in paged_attention."""
+    return (_ready or _native()).prefix_attention(q, k_cache, v_cache, block_table, lens, scale, 0, k_scale, v_scale, out,
+                                                  return_lse, seqs, positions, group_start, prefix_lens)
+
+
 def rope_table(theta: float, head_dim: int, n_pos: int, device=None):
     """(cos, sin) of p * theta^(-2i / head_dim) for positions p < n_pos, in fp64 rounded to fp32 [n_pos, head_dim/2, 2]:
     the table that the decoder builds for itself."""
@@ -95,9 +167,10 @@ class PagedCache:
     """K/V pages of every layer of a model for up to max_seqs sequences, with their block table, lengths and free
     list, all on the GPU at fixed addresses. A step: ``extend`` (pages and slots for the new tokens), then per layer ``append`` and
     ``attention``; ``release`` takes finished sequences' pages back; ``load`` copies a prompt that a Decoder has
-    prefilled."""
+    prefilled. With shared=True sequences may share pages: ``fork`` lets sequences continue others."""
 
-    def __init__(self, model, n_blocks: int, block_size: int, max_seqs: int, max_blocks: int, dtype=None):
+    def __init__(self, model, n_blocks: int, block_size: int, max_seqs: int, max_blocks: int, dtype=None,
+                 shared: bool = False):
         torch = _torch()
         self.model, self.block_size = model, block_size
         self.device = torch.device("cuda", torch.cuda.current_device())
@@ -112,6 +185,7 @@ class PagedCache:
         self.lens = torch.zeros(max_seqs, **ints)
         self.free_blocks = torch.arange(n_blocks - 1, -1, -1, **ints)  # page 0 is given first
         self.n_free = torch.full((1,), n_blocks, **ints)
+        self.shares = torch.zeros(n_blocks, **ints) if shared else None  # holders of each page beyond the first
 
     def _layer(self, l: int) -> dict:
         scales = {} if self.k_scale is None else {"k_scale": self.k_scale[l], "v_scale": self.v_scale[l]}
@@ -129,22 +203,48 @@ class PagedCache:
 
     def release(self, done) -> None:
         """Take back the pages of the sequences with done (bool [max_seqs])."""
-        self._update(*paged_release(done, self.lens, self.block_table, self.free_blocks, self.n_free, self.block_size))
+        self._update(*paged_release(done, self.lens, self.block_table, self.free_blocks, self.n_free, self.block_size,
+                                    self.shares))
+
+    def _copy(self, src, dst, rows=None) -> None:
+        paged_copy(src, dst, self.k, self.v, rows=rows, k_scale=self.k_scale, v_scale=self.v_scale)
+
+    def fork(self, parents) -> PagedFork:
+        """Let sequence r go on from what sequence parents[r] (int32 [max_seqs]) holds; r itself leaves it as it is, -1 ends
+        it. See paged_fork; where ok is False in the result, pages did not suffice and nothing has changed."""
+        if self.shares is None:
+            raise ValueError("sequences can be forked in a PagedCache of shared=True only")
+        f = paged_fork(parents, self.lens, self.block_table, self.shares, self.free_blocks, self.n_free, self.block_size)
+        self._copy(f.copy_src, f.copy_dst, f.copy_rows)
+        self._update(f.lens, f.n_free)
+        return f
+
+    def compact(self) -> PagedMoves:
+        """Move the pages in use to the beginning of the cache: afterwards they are pages 0 .. n_blocks - n_free - 1. See
+        paged_compact; page_map in the result gives the new id of each page."""
+        torch = _torch()
+        shares = self.shares if self.shares is not None else torch.zeros(self.k.shape[1], dtype=torch.int32, device=self.device)
+        m = paged_compact(self.lens, self.block_table, shares, self.free_blocks, self.n_free, self.block_size)
+        self._copy(m.src, m.dst)
+        self.n_free.copy_(m.n_free)
+        return m
 
     def append(self, l: int, k, v, step: PagedStep, q=None, q_out=None):
         """Rotate and store layer l's K/V rows of a step (packed in its order); returns the rotated q, packed likewise."""
         return paged_append(k, v, slots=step.slots, positions=step.positions, rope=self.rope, q=q, q_out=q_out,
                             **self._layer(l))
 
-    def attention(self, l: int, q, step: PagedStep | None = None, **kw):
+    def attention(self, l: int, q, step: PagedStep | None = None, *, groups=None, **kw):
         """Layer l's attention of a step's rows, q [n_rows, n_heads, head_dim] as `append` returned it, each over its own
         sequence up to its own position (rows that were not admitted get zeros). Without a step, q [max_seqs, n_heads,
         head_dim] holds one row per sequence, sequence b's newest token in row b: a step's rows lie like that only if it
-        brought exactly one token for every sequence. See paged_attention."""
-        if step is None:
-            return paged_attention(q, block_table=self.block_table, lens=self.lens, **self._layer(l), **kw)
-        return paged_attention(q, block_table=self.block_table, lens=None, seqs=step.seqs, positions=step.positions,
-                               **self._layer(l), **kw)
+        brought exactly one token for every sequence. See paged_attention. groups = (group_start, prefix_lens): neighbouring
+        rows of q share beginnings, which are read once; see paged_prefix_attention."""
+        rows = {"lens": self.lens} if step is None else {"lens": None, "seqs": step.seqs, "positions": step.positions}
+        if groups is None:
+            return paged_attention(q, block_table=self.block_table, **rows, **self._layer(l), **kw)
+        return paged_prefix_attention(q, block_table=self.block_table, group_start=groups[0], prefix_lens=groups[1], **rows,
+                                      **self._layer(l), **kw)
 
     def load(self, decoder, step: PagedStep, first_row: int = 0) -> None:
         """Copy the prompt that `decoder` (a Decoder of this model) has prefilled, positions 0 .. position - 1 of

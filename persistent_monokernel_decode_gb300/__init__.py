@@ -26,8 +26,8 @@ BINDING_PATH, BINDING_SOURCE = os.path.join(_HERE, "_paged.so"), "kie_paged_py.c
 BINDING_ENV_PATH = os.path.join(_BUILD, "_paged.env")  # what _paged.so was compiled against
 SOURCES = ("kie_api.cu", "kie_decode.cu", "kie_gemv.cu", "kie_prefill.cu", "kie_paged.cu", "kie_paged_attn.cu",
            "kie_prefix_attn.cu", "kie_pages.cu", "kie_logprobs.cu")
-HEADERS = ("kie_layout.h", "kie_device.cuh", "kie_decode.cuh", "kie_prefill.cuh", "kie_tcgemm.cuh", "kie_tcattn.cuh",
-           "kie_paged.cuh")
+HEADERS = ("kie_layout.h", "kie_device.cuh", "kie_decode.cuh", "kie_prefill.cuh", "kie_tc.cuh", "kie_tcgemm.cuh",
+           "kie_tcattn.cuh", "kie_paged.cuh")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 KIE_OK, KIE_ERR_INVALID, KIE_ERR_OOM, KIE_ERR_CAPACITY = 0, -1, -2, -3

@@ -92,13 +92,25 @@ struct ForkArgs : kie_paged_fork_args {
   const uint8_t *done;
 };
 
-// An attention of groups with a common prefix, as its kernels take it. The kernel of the prefixes leaves, for each query
-// row, how many of its positions the group has read for it, and what came of them.
+// Attention of groups with a common prefix (kie_prefix_attn.cu): the prefixes' kernel works on a list of items (group, tile
+// of its rows, KV head) of PX_ITEM_COST places and one for each unit of positions. Block i takes the places from i *
+// per_block on and leaves a piece of each item whose units it had: the weighted sum of V, unnormalised, for `rows` rows, at
+// prefix[slot * DH], dimensions in groups of eight [DH / 8][rows][8], and at prefix_ml[slot + row] the reference (log2
+// units) and the sum of weights; slot = row.slot + head * row.rows + 128 i.
+constexpr int PX_ITEM_COST = 2, PX_MIN_RUN = 4;
+struct PrefixRow {
+  long long place;  // of the first head's item in the list
+  int lo, units;    // positions that the group has read for the row; units of an item
+  int slot, rows, local, unused;  // the row's query heads are rows local .. of the tile
+};
 struct PrefixArgs : kie_paged_attention_args {
   const int32_t *group_start, *prefix_lens;
   int n_groups;
-  int32_t *row_lo;
+  int32_t *row_lo;  // lo of each row
+  PrefixRow *rows;
+  long long *per_block;
   float *prefix;
+  float2 *prefix_ml;
 };
 
 // The kernels find the rows' ends in lens, be they lengths or a step's positions, and the number of table rows in n_table.

@@ -405,25 +405,50 @@ __device__ __forceinline__ void join_pieces(const Pieces &piece, int n, int grou
     if (me.r0 + q * S::STEP < group) put(me.r0 + q * S::STEP, me.d, acc[q], top[q], sum[q]);
 }
 
-// The positions that the row's group has read for it join its own.
+// The pieces that the row's group has for query head r of KV head h join the row's own sums, in their order.
 template <int DH>
-__device__ __forceinline__ void add_prefix(const PrefixArgs &a, int b, int64_t head, int d, float4 &acc, float &M, float &L) {
-  if (a.row_lo[b] <= 0) return;
-  const int64_t at = (int64_t)b * a.n_heads + head;
-  const float4 y = *reinterpret_cast<const float4 *>(a.prefix + at * DH + d);
-  const float2 ml = *reinterpret_cast<const float2 *>(a.prefix + (int64_t)a.n_seqs * a.n_heads * DH + 2 * at);
-  const float mn = fmaxf(M, ml.x), ref = mn == -INFINITY ? 0.f : mn, f = ex2(M - ref), g = ex2(ml.x - ref);
-  acc.x = fmaf(y.x, g, acc.x * f), acc.y = fmaf(y.y, g, acc.y * f);
-  acc.z = fmaf(y.z, g, acc.z * f), acc.w = fmaf(y.w, g, acc.w * f);
-  L = fmaf(ml.y, g, L * f);
-  M = mn;
+__device__ __forceinline__ void add_prefix(const PrefixArgs &a, int b, int h, int r, int d, float4 &acc, float &M, float &L) {
+  const PrefixRow row = a.rows[b];
+  if (row.lo <= 0) return;
+  const long long per = *a.per_block, place = row.place + (long long)h * (row.units + PX_ITEM_COST) + PX_ITEM_COST;
+  const int first = (int)divide(place, per), n = (int)divide(place + row.units - 1, per) - first + 1;
+  const int64_t slot = row.slot + h * row.rows + (int64_t)128 * first;
+  const float *o = a.prefix + slot * DH + (int64_t)(d >> 3) * row.rows * 8 + (row.local + r) * 8 + (d & 7);
+  const float2 *ml = a.prefix_ml + slot + row.local + r;
+  constexpr int BATCH = 8;
+  for (int i0 = 0; i0 < n; i0 += BATCH) {
+    float2 w[BATCH];
+    float4 y[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      const int64_t i = min(i0 + k, n - 1);
+      w[k] = __ldcg(ml + 128 * i);
+      y[k] = __ldcg(reinterpret_cast<const float4 *>(o + 128 * DH * i));
+    }
+    float mn = M;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k)
+      if (i0 + k < n) mn = fmaxf(mn, w[k].x);
+    const float ref = mn == -INFINITY ? 0.f : mn, f0 = ex2(M - ref);
+    L *= f0, acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k)
+      if (i0 + k < n) {
+        const float f = ex2(w[k].x - ref);
+        L = fmaf(w[k].y, f, L);
+        acc.x = fmaf(y[k].x, f, acc.x), acc.y = fmaf(y[k].y, f, acc.y);
+        acc.z = fmaf(y[k].z, f, acc.z), acc.w = fmaf(y[k].w, f, acc.w);
+      }
+    M = mn;
+  }
 }
 
 // Four dimensions of a query head's output from its weighted sum, and its lse from the reference M (log2 units) and the
 // sum of weights L: zeros and -inf where nothing was attended. vec: the output is aligned for one store of four.
 template <int DH, class A>
-__device__ __forceinline__ void finish4(const A &a, bool vec, int b, int64_t head, int d, float4 acc, float M, float L) {
-  if constexpr (std::is_same<A, PrefixArgs>::value) add_prefix<DH>(a, b, head, d, acc, M, L);
+__device__ __forceinline__ void finish4(const A &a, bool vec, int b, int h, int r, int d, float4 acc, float M, float L) {
+  if constexpr (std::is_same<A, PrefixArgs>::value) add_prefix<DH>(a, b, h, r, d, acc, M, L);
+  const int64_t head = (int64_t)h * (a.n_heads / a.pages.n_kv_heads) + r;
   const float inv = L == 0.f ? 0.f : rcp(L);
   const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
   const int64_t to = b * a.out_stride[0] + head * a.out_stride[1] + d;
@@ -459,7 +484,7 @@ __device__ __forceinline__ void publish(const A &a, unsigned long long call, int
   const int group = a.n_heads / a.pages.n_kv_heads, n = last - first + 1;
   const bool vec = out_vec(a);
   const auto finish = [&](int r, int d, float4 acc, float M, float L) {
-    finish4<DH>(a, vec, b, (int64_t)h * group + r, d, acc, M, L);
+    finish4<DH>(a, vec, b, h, r, d, acc, M, L);
   };
   const size_t step = PA_PIECES * ws.piece;
   if (n <= PA_ONE_LEVEL) {
@@ -895,7 +920,7 @@ paged_attn_kernel(const A a, unsigned long long call) {
           acc.z = fmaf(y.z, f[w], acc.z), acc.w = fmaf(y.w, f[w], acc.w);
         }
         if (whole)
-          finish4<DH>(a, vec, b, (int64_t)h * group + r, me.d, acc, M, L);
+          finish4<DH>(a, vec, b, h, r, me.d, acc, M, L);
         else
           put_piece<DH>(piece, group, r, me.d, acc, M, L);
       }

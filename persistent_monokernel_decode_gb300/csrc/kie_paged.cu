@@ -672,8 +672,10 @@ int kie_paged_prefix_attention(const kie_paged_prefix_attention_args *p, void *s
   const size_t need = kie_paged_prefix_workspace_bytes(a.n_seqs, a.n_heads, a.pages.n_kv_heads, a.pages.head_dim, sms);
   if (!a.workspace || a.workspace_bytes < need || !aligned(a.workspace, 256))
     return refuse("the workspace is NULL, unaligned (256 bytes) or smaller than kie_paged_prefix_attention_workspace");
-  return finish(p->n_groups ? kie_launch_paged_prefix(*p, dev, sms, (cudaStream_t)stream)
-                            : kie_launch_paged_attention(a, dev, sms, (cudaStream_t)stream), "paged_prefix_attention");
+  const cudaError_t e = p->n_groups ? kie_launch_paged_prefix(*p, dev, sms, (cudaStream_t)stream)
+                                    : kie_launch_paged_attention(a, dev, sms, (cudaStream_t)stream);
+  if (e == cudaErrorInvalidPitchValue) return refuse("no tensor map can be made of the pages' strides");
+  return finish(e, "paged_prefix_attention");
 }
 
 int kie_paged_fork(const kie_paged_fork_args *p, void *stream) {

@@ -103,6 +103,11 @@ struct PrefixRow {
   int lo, units;    // positions that the group has read for the row; units of an item
   int slot, rows, local, unused;  // the row's query heads are rows local .. of the tile
 };
+// Where the pieces of a row's query heads of one KV head are: n of them, 128 slots apart.
+struct PrefixPieces {
+  long long slot;
+  int n, rows, local;
+};
 struct PrefixArgs : kie_paged_attention_args {
   const int32_t *group_start, *prefix_lens;
   int n_groups;

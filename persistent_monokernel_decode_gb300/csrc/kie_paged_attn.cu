@@ -75,6 +75,7 @@ struct PaSmem {
   float scale[PA_WARPS][KIND == PG_E4M3 ? T::NS : 1][32];
   float4 m[PA_ROWS], l[PA_ROWS];  // of a row: the four warps'
   uint32_t live[PA_WARPS][T::NS];
+  PrefixPieces prefix;  // of the item at work
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
@@ -173,11 +174,11 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
 struct Span {
   int lo, len, from, n;
 };
-template <int UNIT, class A>
-__device__ __forceinline__ Span span_of(const A &a, int b) {
+template <int UNIT, class Args>
+__device__ __forceinline__ Span span_of(const Args &a, int b) {
   Span s;
   s.len = row_len(a, b);
-  if constexpr (std::is_same<A, PrefixArgs>::value)
+  if constexpr (std::is_same<Args, PrefixArgs>::value)
     s.lo = a.row_lo[b];  // the positions before are the group's
   else
     s.lo = a.window > 0 ? max(0, s.len - a.window) : 0;
@@ -198,8 +199,8 @@ template <int UNIT>
 struct Cursor {
   Span s;
   int b, h, unit, v;
-  template <class A>
-  __device__ __forceinline__ void next(const A &a) {
+  template <class Args>
+  __device__ __forceinline__ void next(const Args &a) {
     ++v;
     if (++unit < s.n) return;
     unit = 0;
@@ -218,8 +219,8 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
 // The number of places of this block's run (*end; 0 behind the list's end), the cursor at its first unit, and the
 // places of a full run (*per_block). Every thread gets the same; two block barriers. The cursor may stand at or past
 // *end: no units.
-template <int UNIT, class A>
-__device__ __forceinline__ void locate(const A &a, Cursor<UNIT> *c, int *end, long long *per_block) {
+template <int UNIT, class Args>
+__device__ __forceinline__ void locate(const Args &a, Cursor<UNIT> *c, int *end, long long *per_block) {
   __shared__ long long s_warp[PA_WARPS];
   __shared__ int s_b, s_h;
   __shared__ int s_off;
@@ -405,17 +406,13 @@ __device__ __forceinline__ void join_pieces(const Pieces &piece, int n, int grou
     if (me.r0 + q * S::STEP < group) put(me.r0 + q * S::STEP, me.d, acc[q], top[q], sum[q]);
 }
 
-// The pieces that the row's group has for query head r of KV head h join the row's own sums, in their order.
+// The pieces that the row's group has for its query heads join the row's own sums, in their order.
 template <int DH>
-__device__ __forceinline__ void add_prefix(const PrefixArgs &a, int b, int h, int r, int d, float4 &acc, float &M, float &L) {
-  const PrefixRow row = a.rows[b];
-  if (row.lo <= 0) return;
-  const long long per = *a.per_block, place = row.place + (long long)h * (row.units + PX_ITEM_COST) + PX_ITEM_COST;
-  const int first = (int)divide(place, per), n = (int)divide(place + row.units - 1, per) - first + 1;
-  const int64_t slot = row.slot + h * row.rows + (int64_t)128 * first;
-  const float *o = a.prefix + slot * DH + (int64_t)(d >> 3) * row.rows * 8 + (row.local + r) * 8 + (d & 7);
-  const float2 *ml = a.prefix_ml + slot + row.local + r;
-  constexpr int BATCH = 8;
+__device__ __forceinline__ void add_prefix(const PrefixArgs &a, const PrefixPieces &p, int r, int d, float4 &acc, float &M, float &L) {
+  const int n = p.n;
+  const float *o = a.prefix + p.slot * DH + (int64_t)(d >> 3) * p.rows * 8 + (p.local + r) * 8 + (d & 7);
+  const float2 *ml = a.prefix_ml + p.slot + p.local + r;
+  constexpr int BATCH = 12;
   for (int i0 = 0; i0 < n; i0 += BATCH) {
     float2 w[BATCH];
     float4 y[BATCH];
@@ -445,9 +442,10 @@ __device__ __forceinline__ void add_prefix(const PrefixArgs &a, int b, int h, in
 
 // Four dimensions of a query head's output from its weighted sum, and its lse from the reference M (log2 units) and the
 // sum of weights L: zeros and -inf where nothing was attended. vec: the output is aligned for one store of four.
-template <int DH, class A>
-__device__ __forceinline__ void finish4(const A &a, bool vec, int b, int h, int r, int d, float4 acc, float M, float L) {
-  if constexpr (std::is_same<A, PrefixArgs>::value) add_prefix<DH>(a, b, h, r, d, acc, M, L);
+template <int DH, class Args>
+__device__ __forceinline__ void finish4(const Args &a, const PrefixPieces &prefix, bool vec, int b, int h, int r, int d, float4 acc,
+                                        float M, float L) {
+  if constexpr (std::is_same<Args, PrefixArgs>::value) add_prefix<DH>(a, prefix, r, d, acc, M, L);
   const int64_t head = (int64_t)h * (a.n_heads / a.pages.n_kv_heads) + r;
   const float inv = L == 0.f ? 0.f : rcp(L);
   const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
@@ -476,15 +474,15 @@ __device__ __forceinline__ void put_piece(float *p, int group, int r, int d, flo
 
 // After this block has written its piece of item (b, h), whose `units` units begin at place v of the list: whoever of
 // the blocks that share it comes last joins the pieces.
-template <int DH, class A>
-__device__ __forceinline__ void publish(const A &a, unsigned long long call, int b, int h, long long v,
+template <int DH, class Args>
+__device__ __forceinline__ void publish(const Args &a, const PrefixPieces &prefix, unsigned long long call, int b, int h, long long v,
                                         int units, long long per_block) {
   const Workspace ws(a, DH);
   const int first = (int)divide(v, per_block), last = (int)divide(v + units - 1, per_block);
   const int group = a.n_heads / a.pages.n_kv_heads, n = last - first + 1;
   const bool vec = out_vec(a);
   const auto finish = [&](int r, int d, float4 acc, float M, float L) {
-    finish4<DH>(a, vec, b, h, r, d, acc, M, L);
+    finish4<DH>(a, prefix, vec, b, h, r, d, acc, M, L);
   };
   const size_t step = PA_PIECES * ws.piece;
   if (n <= PA_ONE_LEVEL) {
@@ -543,9 +541,9 @@ __device__ __forceinline__ int join_col(int r, int d) {
   return d ^ (((r >> 1) & 3) << (KIND == PG_E4M3 ? 4 : 3));
 }
 
-template <int KIND, int DH, bool SPLIT, class A>
+template <int KIND, int DH, bool SPLIT, class Args>
 __global__ void __launch_bounds__(PA_THREADS, PaTile<KIND, DH>::BLOCKS)
-paged_attn_kernel(const A a, unsigned long long call) {
+paged_attn_kernel(const Args a, unsigned long long call) {
   using T = PaTile<KIND, DH>;
   using Sm = PaSmem<KIND, DH>;
   constexpr int NS = T::NS, CH = T::CH, ROW = T::ROW, ES = T::ES, SUBS = T::SUBS, LOADS = T::LOADS;
@@ -663,6 +661,9 @@ paged_attn_kernel(const A a, unsigned long long call) {
         [&](int i) { return 16 * (i >> 1) + (KIND == PG_E4M3 ? 4 * t + 2 * (i & 1) : 2 * t + 8 * (i & 1)); }, raw);
   };
   request_q(c.b, c.h);
+  PrefixRow row;
+  long long prefix_per = 1;
+  if constexpr (std::is_same<Args, PrefixArgs>::value) row = a.rows[c.b], prefix_per = *a.per_block;
   set_head();
   fetch_pages();
 #pragma unroll 1
@@ -680,6 +681,16 @@ paged_attn_kernel(const A a, unsigned long long call) {
 
   for (;;) {  // an item, or this block's part of it
     const int units = min(c.s.n - c.unit, end - c.v);
+    if constexpr (std::is_same<Args, PrefixArgs>::value) {
+      if (threadIdx.x == 0) {  // seen by the others behind the join's barrier
+        const long long place = row.place + (long long)c.h * (row.units + PX_ITEM_COST) + PX_ITEM_COST;
+        const long long first = divide(place, prefix_per);
+        sm.prefix.slot = row.slot + (long long)c.h * row.rows + 128 * first;
+        sm.prefix.n = row.lo > 0 ? (int)(divide(place + row.units - 1, prefix_per) - first) + 1 : 0;
+        sm.prefix.rows = row.rows;
+        sm.prefix.local = row.local;
+      }
+    }
     {  // its query heads as B fragments
       float down = 1.f;
       if (!SPLIT) {
@@ -875,7 +886,10 @@ paged_attn_kernel(const A a, unsigned long long call) {
     c.v += units - 1;
     c.next(a);
     const bool done = c.v >= end;
-    if (!done) request_q(c.b, c.h);  // the next item's queries arrive while this one is finished
+    if (!done) {  // the next item's queries arrive while this one is finished
+      request_q(c.b, c.h);
+      if constexpr (std::is_same<Args, PrefixArgs>::value) row = a.rows[c.b];
+    }
     {
       __syncwarp();  // every lane is done with the slot
       float *join = reinterpret_cast<float *>(sm.ring[warp][used]);
@@ -920,12 +934,12 @@ paged_attn_kernel(const A a, unsigned long long call) {
           acc.z = fmaf(y.z, f[w], acc.z), acc.w = fmaf(y.w, f[w], acc.w);
         }
         if (whole)
-          finish4<DH>(a, vec, b, h, r, me.d, acc, M, L);
+          finish4<DH>(a, sm.prefix, vec, b, h, r, me.d, acc, M, L);
         else
           put_piece<DH>(piece, group, r, me.d, acc, M, L);
       }
       if (!whole)
-        publish<DH>(a, call, b, h, v, n, per_block);
+        publish<DH>(a, sm.prefix, call, b, h, v, n, per_block);
       __syncthreads();  // the next half may land in the slot, and the next item's sums in theirs
       if (done) break;
     }
@@ -940,23 +954,23 @@ unsigned long long call_number() {
   return calls.fetch_add(0x3c6ef372fe94faull, std::memory_order_relaxed) & ((1ull << 56) - 1);
 }
 
-template <int KIND, int DH, bool SPLIT, class A>
-cudaError_t launch(const A &a, int dev, int sms, cudaStream_t stream) {
+template <int KIND, int DH, bool SPLIT, class Args>
+cudaError_t launch(const Args &a, int dev, int sms, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};  // devices whose limit of dynamic shared memory is raised
   const int smem = sizeof(PaSmem<KIND, DH>);
   const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
   if (!bit || !(ready.load(std::memory_order_relaxed) & bit)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(paged_attn_kernel<KIND, DH, SPLIT, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(paged_attn_kernel<KIND, DH, SPLIT, Args>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  return launch_after_previous(paged_attn_kernel<KIND, DH, SPLIT, A>, sms * PaTile<KIND, DH>::BLOCKS, PA_THREADS, smem, stream, a,
+  return launch_after_previous(paged_attn_kernel<KIND, DH, SPLIT, Args>, sms * PaTile<KIND, DH>::BLOCKS, PA_THREADS, smem, stream, a,
                                call_number());
 }
 
-template <int DH, class A>
-cudaError_t launch_dh(const A &a, int dev, int sms, cudaStream_t stream) {
+template <int DH, class Args>
+cudaError_t launch_dh(const Args &a, int dev, int sms, cudaStream_t stream) {
   if (a.pages.dtype == KIE_BF16) return launch<PG_BF16, DH, false>(a, dev, sms, stream);
   if (a.pages.dtype == KIE_E4M3) return launch<PG_E4M3, DH, true>(a, dev, sms, stream);
   return a.q_dtype == KIE_F32 ? launch<PG_F16, DH, true>(a, dev, sms, stream) : launch<PG_F16, DH, false>(a, dev, sms, stream);

@@ -8,13 +8,15 @@
 // that it has part in. The kernel of the rows' own positions joins the pieces where it finishes a row: hundreds of blocks
 // there read them side by side.
 //
-// In a block four warps load K and V tiles into a ring (cp.async, or through registers where E4M3 codes become fp16), one
-// thread issues the MMAs, and four warps hold the softmax: thread = row = TMEM lane, so its maxima and sums need no
-// shuffles. S is double-buffered in TMEM, so that the scores of the next tile are formed while this one's weights are;
-// the weights go back over the scores, as the TMEM operand of the second product. As in kie_paged_attn.cu, the softmax's
-// reference stays within 2^8 of the running maximum and O is only rescaled when a weight would pass 2^15, weights and fp32
-// queries are two 16-bit parts, and the sum of weights is of the weights before they are rounded.
+// In a block one warp brings K and V tiles into a ring by TMA (two more turn E4M3 codes into fp16 on the way), one thread
+// issues the MMAs, and four warps hold the softmax: thread = row = TMEM lane, so its maxima and sums need no shuffles. S is
+// double-buffered in TMEM, so that the scores of the next tile are formed while this one's weights are; the weights go back
+// over the scores, as the TMEM operand of the second product. As in kie_paged_attn.cu, the softmax's reference stays within
+// 2^8 of the running maximum and O is only rescaled when a weight would pass 2^15, weights and fp32 queries are two 16-bit
+// parts, and the sum of weights is of the weights before they are rounded.
+#include <cuda.h>
 #include <float.h>
+#include <limits.h>
 
 #include <algorithm>
 #include <atomic>
@@ -27,12 +29,13 @@ namespace kie {
 namespace {
 
 constexpr int PX_M = 128, PX_N = 64;       // rows of a tile, positions of a unit
-constexpr int PX_SOFT = 4, PX_LOAD = 4;    // warps; one more issues the MMAs
-constexpr int PX_THREADS = 32 * (PX_SOFT + PX_LOAD + 1);
-constexpr int PX_LOADERS = 32 * PX_LOAD;
-// Depth of what is kept per unit besides K and V. The loaders are at most NS <= 5 halves ahead of the oldest one in use, so
-// at most three units ahead of the one whose weights are formed.
-constexpr int PX_TILES = 4;
+// Warps: the softmax's four, the loader, two that convert codes, the one that issues the MMAs. Eight, so that two blocks get
+// 128 registers a thread.
+constexpr int PX_SOFT = 4, PX_LOADER = 4, PX_CONVERT = 5, PX_CONVERTERS = 2, PX_ISSUER = 7;
+constexpr int PX_THREADS = 256;
+// Depth of what is kept per unit besides K and V. The loader is at most NS + RAW <= 6 halves ahead of the oldest one in use,
+// so at most four units ahead of the one whose weights are formed.
+constexpr int PX_TILES = 8;
 constexpr uint32_t PX_TMEM = 256;          // columns: S twice, O
 constexpr unsigned long long PX_TIMEOUT_NS = 2000000000ull;
 constexpr float LOG2E = 1.4426950408889634f;
@@ -43,22 +46,27 @@ enum { PG_F16 = 0, PG_BF16 = 1, PG_E4M3 = 2 };
 
 template <int KIND, int DH, bool SPLIT>
 struct PxShape {
-  static constexpr int Q_BYTES = PX_M * DH * 2 * (SPLIT ? 2 : 1), SLOT = PX_N * DH * 2;
-  // Two blocks fit an SM but where fp32 queries meet E4M3 pages of 128, whose scales are 1 KB too many
+  static constexpr int Q_BYTES = PX_M * DH * 2 * (SPLIT ? 2 : 1), SLOT = PX_N * DH * 2, CODES = PX_N * DH;
+  // Two blocks fit an SM but where fp32 queries meet E4M3 pages of 128
   static constexpr int BLOCKS = SPLIT && KIND == PG_E4M3 && DH == 128 ? 1 : 2;
-  static constexpr int NS = DH == 64 || BLOCKS == 1 ? 5 : SPLIT ? 3 : KIND == PG_E4M3 ? 4 : 5;  // ring slots
+  static constexpr int NS = KIND == PG_E4M3 ? 3 : SPLIT && DH == 128 ? 3 : 5;  // ring slots
+  static constexpr int RAW = KIND == PG_E4M3 ? 3 : 1;                          // of codes as they come
 };
 
 template <int KIND, int DH, bool SPLIT>
 struct PxSmem {
   using T = PxShape<KIND, DH, SPLIT>;
+  static constexpr bool E4M3 = KIND == PG_E4M3;
   uint8_t q[T::Q_BYTES];         // [part][64-dim block][row][128 B], 16-byte chunks swizzled by the row
   uint8_t ring[T::NS][T::SLOT];  // [64-dim block][position][128 B], the same
-  float scale[KIND == PG_E4M3 ? PX_TILES : 1][3][KIND == PG_E4M3 ? PX_N : 1];  // of K, of V, log2 of V's
+  uint8_t raw[E4M3 ? T::RAW : 1][E4M3 ? T::CODES : 16];  // [position][DH]
+  float scale[E4M3 ? PX_TILES : 1][3][E4M3 ? PX_N : 1];  // of K, of V, log2 of V's
   uint32_t live[PX_TILES];       // bit i: positions 16 i .. 16 i + 15 lie on a page
   float rs[PX_M];                // score scale of a row, in log2 units
-  uint64_t full[T::NS], empty[T::NS], unit[PX_TILES], s_full[2], p_full[2], pv_done;
-  unsigned long long best;       // of the group's rows: reach, and the first row that has it
+  uint64_t full[T::NS], empty[T::NS], unit[PX_TILES], s_full[2], p_full[2], pv_done[2], fix, raw_full[T::RAW], raw_empty[T::RAW];
+  long long place, sums[PX_THREADS / 32];  // the first item's place in the list; scratch of the sums over the block
+  int g, edge[2];                // its group, and that one's rows
+  int reach;                     // positions of the prefix that the longest row of the group has
   uint32_t tmem;
   int failed;
 };
@@ -84,6 +92,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// True in one lane of the (converged) warp. The compiler knows that no more than one thread is at what is behind it.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 // tcgen05.mma with A in TMEM.
 __device__ __forceinline__ void tc_mma_ts(uint32_t dtmem, uint32_t atmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
   asm volatile(
@@ -103,6 +118,13 @@ __device__ __forceinline__ uint64_t px_desc(uint32_t saddr, uint32_t lead) {
 __host__ __device__ constexpr uint32_t px_idesc(int n, bool bf16, bool b_mn) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(PX_M >> 4) << 24);
+}
+
+// Eight floats, a whole sector, to a 32-byte aligned address.
+__device__ __forceinline__ void store8(float *p, const float *v) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+               "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -132,13 +154,13 @@ __device__ __forceinline__ uint32_t e4m3x2(uint32_t two) {
   return r;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// A box of the tensor behind a map, at these coordinates, into shared memory; what lies outside the tensor becomes zeros.
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
+      : "memory");
 }
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -162,6 +184,13 @@ __device__ __forceinline__ bool px_wait(uint64_t *bar, uint32_t parity, int *fai
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *failed) {
   return __all_sync(0xffffffffu, px_wait(bar, parity, failed)) != 0;
 }
+
+// K and V of the cache as tensors of four dimensions: dims, and three that order tells, two bits each (0 position, 1 head, 2
+// page); boxes of `rows` positions.
+struct PrefixMaps {
+  CUtensorMap k, v;
+  int order[2], rows;
+};
 
 // ---- the list ------------------------------------------------------------------------------------------------
 
@@ -191,9 +220,13 @@ __device__ __forceinline__ int length_of(const PrefixArgs &a, int b) {
   return (unsigned)sequence_of(a, b) < (unsigned)a.n_table ? row_len(a, b) : 0;
 }
 
+__device__ __forceinline__ long long divide_up(long long a, unsigned b) {  // a 64-bit division takes a few hundred cycles
+  a += b - 1;
+  return (a >> 32) == 0 ? (long long)((unsigned)a / b) : a / b;
+}
+
 // Sums over the block in thread order: v becomes the sum of the threads' before this one, *all of all.
-__device__ __forceinline__ long long sum_before(long long v, long long *all) {
-  __shared__ long long s_warp[PX_THREADS / 32];
+__device__ __forceinline__ long long sum_before(long long v, long long *s_warp, long long *all) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long up = v;
 #pragma unroll
@@ -213,9 +246,39 @@ __device__ __forceinline__ long long sum_before(long long v, long long *all) {
   return before;
 }
 
+// The E neighbouring elements of a query that start at `at`, as they are: fp32 (WIDE) or two to a word; zeros if not live.
+template <bool WIDE, int E>
+__device__ __forceinline__ void load_query(const PrefixArgs &a, bool vec, bool live, int64_t at, uint32_t (&w)[WIDE ? E : E / 2]) {
+  constexpr int N = WIDE ? E : E / 2;
+#pragma unroll
+  for (int e = 0; e < N; ++e) w[e] = 0u;
+  if (!live) return;
+  if (vec) {
+    const void *p = static_cast<const uint8_t *>(a.q) + at * (WIDE ? 4 : 2);
+    if (N == 4) {
+      const uint4 x = *static_cast<const uint4 *>(p);
+      w[0] = x.x, w[N > 1 ? 1 : 0] = x.y, w[N > 2 ? 2 : 0] = x.z, w[N - 1] = x.w;
+    } else if (N == 2) {
+      const uint2 x = *static_cast<const uint2 *>(p);
+      w[0] = x.x, w[N - 1] = x.y;
+    } else {
+      w[0] = *static_cast<const uint32_t *>(p);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      w[e] = WIDE ? static_cast<const uint32_t *>(a.q)[at + e]
+                  : static_cast<const uint16_t *>(a.q)[at + 2 * e] | (uint32_t) static_cast<const uint16_t *>(a.q)[at + 2 * e + 1] << 16;
+  }
+}
+
 // ---- the three roles of a block, for units u0 .. u0 + n - 1 of an item -------------------------------------------
 // `tiles` and `halves` count the units, and the halves of them in the ring, of the items before. The halves' order is that
 // of their use: K0, K1, V0, K2, V1, .., V(n - 1).
+
+// A wait by parity tells a phase of a barrier from the one before it only: whoever waits here knows that the one before is
+// over, and the next one cannot end before it has gone on. (Hence two barriers for S, for P and for what follows P, each
+// taking every second unit.)
 
 // Slot of a half, and the parity of its round through the ring.
 template <int NS>
@@ -224,21 +287,38 @@ struct Half {
   __device__ __forceinline__ explicit Half(uint32_t i) : slot(i % NS), round(i / NS & 1u) {}
 };
 
+// Half i of n units: its unit, and whether it is V.
+__device__ __forceinline__ int unit_of(int i, int n, bool *is_v) {
+  if (i == 0) return *is_v = false, 0;
+  if (i == 2 * n - 1) return *is_v = true, n - 1;
+  *is_v = !(i & 1);
+  return (i & 1) ? (i + 1) / 2 : i / 2 - 1;
+}
+
+// One warp. Finds the group's longest row (the first of them), through whose table row the prefix is read, and loads, without
+// waiting for the queries. Returns the number of units, all of them with positions.
 template <int KIND, int DH, bool SPLIT>
-__device__ __forceinline__ void load_item(const PrefixArgs &a, PxSmem<KIND, DH, SPLIT> &sm, int lt, int h, int source, int reach,
-                                          int u0, int n, uint32_t tiles, uint32_t halves) {
+__device__ __forceinline__ int load_item(const PrefixArgs &a, const PrefixMaps &maps, PxSmem<KIND, DH, SPLIT> &sm, const Group &x,
+                                         int h, int u0, int u1, uint32_t tiles, uint32_t halves, uint32_t &fixes) {
   using T = PxShape<KIND, DH, SPLIT>;
   constexpr bool CODES = KIND == PG_E4M3;
-  constexpr int NS = T::NS, ES = CODES ? 1 : 2, CH = DH * ES / 16;      // 16-byte chunks of a cache row
-  constexpr int STEP = PX_LOADERS / CH, LOADS = PX_N / STEP;            // rows that the loaders take at once, and how often
-  constexpr int LAG = NS > 3 ? 2 : 1;  // halves whose copies are on their way when the next one's begin
-  const int warp = lt >> 5, lane = lt & 31, row0 = lt / CH, chunk = lt % CH;
-  const int *pages = a.block_table + sequence_of(a, source) * a.table_stride;
+  constexpr int NS = CODES ? T::RAW : T::NS, KB = CODES ? 1 : DH / 64;
+  constexpr uint32_t BYTES = CODES ? T::CODES : T::SLOT;
+  const int lane = threadIdx.x & 31;
+  int reach = 0, source = x.start;
+#pragma unroll 2
+  for (int b = x.start + lane; b < x.end; b += 32) {
+    const int len = min(x.prefix, length_of(a, b));
+    if (len > reach) reach = len, source = b;
+  }
+  const int mine = reach;
+  reach = __reduce_max_sync(0xffffffffu, reach);
+  source = __reduce_min_sync(0xffffffffu, mine == reach ? source : INT_MAX);
+  if (lane == 0) sm.reach = reach;
+  asm volatile("bar.arrive 1, 256;" ::: "memory");  // the others, once the queries are there
+  const int n = max(0, min(u1, (reach + PX_N - 1) / PX_N) - u0);
+  const int *pages = a.block_table + (n > 0 ? sequence_of(a, source) : 0) * a.table_stride;
   const unsigned bs = a.pages.block_size;
-  const uint8_t *base[2] = {static_cast<const uint8_t *>(a.pages.k) + (int64_t)h * a.pages.k_stride[1] * ES + 16 * chunk,
-                            static_cast<const uint8_t *>(a.pages.v) + (int64_t)h * a.pages.v_stride[1] * ES + 16 * chunk};
-  const int64_t page_step[2] = {a.pages.k_stride[0] * ES, a.pages.v_stride[0] * ES};
-  const int64_t row_step[2] = {a.pages.k_stride[2] * ES, a.pages.v_stride[2] * ES};
 
   // lane: page and place in it of 16 positions, of eight units from `batch` on and of the eight behind them
   int batch = u0, page_a, at_a, page_b, at_b;
@@ -247,202 +327,191 @@ __device__ __forceinline__ void load_item(const PrefixArgs &a, PxSmem<KIND, DH, 
     const unsigned j = (unsigned)pos / bs;
     *at = pos - (int)(j * bs);
     *page = unit < u0 + n && pos < reach ? pages[j] : -1;
+    if ((unsigned)*page >= (unsigned)a.pages.n_blocks) *page = -1;
   };
   fetch(u0, &page_a, &at_a);
   fetch(u0 + 8, &page_b, &at_b);
-  struct Places {
-    int page[4], at[4];
-    uint32_t live;
-  };
-  const auto places = [&](int unit) {  // of a unit's four groups of 16 positions; units come in order
-    if (unit >= batch + 8) {
-      batch += 8;
-      page_a = page_b, at_a = at_b;
-      fetch(batch + 8, &page_b, &at_b);
-    }
-    Places p;
-    p.live = 0;
+  const int runs = PX_N / maps.rows;  // boxes of maps.rows positions by 128 bytes
+  uint64_t *const full = CODES ? sm.raw_full : sm.full, *const empty = CODES ? sm.raw_empty : sm.empty;
+  const uint32_t ring = smem_u32(CODES ? &sm.raw[0][0] : &sm.ring[0][0]);
+  int page0 = -1, at0 = 0, page1 = -1, at1 = 0;  // lane i: run i of the last even and the last odd unit, for their V
+  float ks[2], vs[2];         // E4M3: the next unit's scales, positions lane and lane + 32
+  const auto request_scales = [&](int unit) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      p.page[i] = __shfl_sync(0xffffffffu, page_a, (unit - batch) * 4 + i);
-      p.at[i] = __shfl_sync(0xffffffffu, at_a, (unit - batch) * 4 + i);
-      if ((unsigned)p.page[i] < (unsigned)a.pages.n_blocks) p.live |= 1u << i;
+    for (int k = 0; k < 2; ++k) {
+      const int row = lane + 32 * k, from = (unit - batch) * 4 + (row >> 4);
+      const int page = __shfl_sync(0xffffffffu, page_a, from & 31), off = __shfl_sync(0xffffffffu, at_a, from & 31) + (row & 15);
+      ks[k] = vs[k] = 0.f;
+      if (page >= 0 && unit * PX_N + row < reach) {
+        ks[k] = a.pages.k_scale[page * a.pages.k_scale_stride[0] + h * a.pages.k_scale_stride[1] + off * a.pages.k_scale_stride[2]];
+        vs[k] = a.pages.v_scale[page * a.pages.v_scale_stride[0] + h * a.pages.v_scale_stride[1] + off * a.pages.v_scale_stride[2]];
+      }
     }
-    return p;
   };
-  // Row row0 + i STEP of a unit lies in its group (i STEP + row0) / 16; with rows of 64 codes that depends on the thread.
-  const auto source_of = [&](const Places &p, int unit, int i, int v, bool *live) {
-    const int row = row0 + i * STEP;
-    int page = p.page[(i * STEP) >> 4], at = p.at[(i * STEP) >> 4];
-    uint32_t bit = (p.live >> ((i * STEP) >> 4)) & 1u;
-    if (STEP > 16 && row0 >= 16) {
-      page = p.page[((i * STEP) >> 4) + 1], at = p.at[((i * STEP) >> 4) + 1];
-      bit = (p.live >> (((i * STEP) >> 4) + 1)) & 1u;
+  const auto turn_to = [&](int unit) {
+    if (unit < batch + 8) return;
+    batch += 8;
+    page_a = page_b, at_a = at_b;
+    fetch(batch + 8, &page_b, &at_b);
+  };
+  if (CODES && n > 0) request_scales(u0);
+  const auto load = [&](int i) {
+    bool is_v;
+    const int u = unit_of(i, n, &is_v), unit = u0 + u;
+    const uint32_t half = halves + i, slot = half % NS;
+    if (!warp_wait(&empty[slot], (half / NS & 1u) ^ 1u, &sm.failed)) return false;
+    int page = u & 1 ? page1 : page0, at = u & 1 ? at1 : at0;
+    uint32_t live = 0;
+    if (!is_v) {
+      turn_to(unit);
+      live = __ballot_sync(0xffffffffu, page_a >= 0) >> ((unit - batch) * 4) & 15u;
+      const int from = (unit - batch) * 4 + lane * (maps.rows >> 4);
+      page = __shfl_sync(0xffffffffu, page_a, from & 31);
+      at = __shfl_sync(0xffffffffu, at_a, from & 31);
+      if (u & 1)
+        page1 = page, at1 = at;
+      else
+        page0 = page, at0 = at;
     }
-    *live = bit && unit * PX_N + row < reach;
-    return base[v] + (*live ? page * page_step[v] + (at + (row & 15)) * row_step[v] : 0);
+    // rows of V behind the end would meet weights of 0 as whatever they hold: they become zeros before the MMA may begin
+    const int tail = reach - unit * PX_N;
+    const bool mend = !CODES && is_v && tail < PX_N;
+    uint64_t *const bar = mend ? &sm.fix : &full[slot];
+    const CUtensorMap *const map = is_v ? &maps.v : &maps.k;
+    const int order = maps.order[is_v];
+    const bool one = elect_one();
+    if (one) mbar_arrive_expect_tx(bar, BYTES);
+    uint32_t to = ring + slot * BYTES;
+#pragma unroll 1
+    for (int run = 0; run < runs; ++run, to += maps.rows * (CODES ? DH : 128)) {
+      const int p = __shfl_sync(0xffffffffu, page, run), y = __shfl_sync(0xffffffffu, at, run);
+      const int z = p >= 0 ? p : a.pages.n_blocks;
+      const auto coordinate = [&](int what) { return (what & 3) == 0 ? y : (what & 3) == 1 ? h : z; };
+      if (one) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+          tma_box(to + kb * (PX_N * 128), map, kb * 64, coordinate(order), coordinate(order >> 2), coordinate(order >> 4), bar);
+      }
+    }
+    __syncwarp();
+    if (mend) {
+      if (!warp_wait(&sm.fix, fixes++ & 1u, &sm.failed)) return false;
+      for (int k = tail * 8 + lane; k < PX_N * 8; k += 32)
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+          *reinterpret_cast<uint4 *>(&sm.ring[CODES ? 0 : slot][b * (PX_N * 128) + k * 16]) = make_uint4(0u, 0u, 0u, 0u);
+      fence_async_proxy();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[slot]);
+    }
+    if (!is_v) {
+      const uint32_t k = (tiles + u) % PX_TILES;
+      if (CODES) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sm.scale[CODES ? k : 0][0][CODES ? lane + 32 * e : 0] = ks[e];
+          sm.scale[CODES ? k : 0][1][CODES ? lane + 32 * e : 0] = vs[e];
+          sm.scale[CODES ? k : 0][2][CODES ? lane + 32 * e : 0] = log2_scale(vs[e]);
+        }
+        __syncwarp();
+      }
+      if (lane == 0) {
+        sm.live[k] = live;
+        mbar_arrive(&sm.unit[k]);
+      }
+    }
+    if (CODES && !is_v && u + 1 < n) {
+      turn_to(unit + 1);
+      request_scales(unit + 1);
+    }
+    return true;
   };
-  const auto wait_empty = [&](uint32_t half) {
-    const Half<NS> x(half);
-    return warp_wait(&sm.empty[x.slot], x.round ^ 1u, &sm.failed);
-  };
-  const auto announce = [&](uint32_t half) {  // this warp's part of it is in place
+#pragma unroll 1
+  for (int i = 0; i < 2 * n; ++i)
+    if (!load(i)) break;
+  return n;
+}
+
+// PX_CONVERTERS warps: codes of the raw ring into fp16 in the other one, positions from the prefix's end on as zeros.
+template <int KIND, int DH, bool SPLIT>
+__device__ __forceinline__ void convert_item(PxSmem<KIND, DH, SPLIT> &sm, int ct, int reach, int u0, int n, uint32_t halves) {
+  using T = PxShape<KIND, DH, SPLIT>;
+  constexpr int CH = DH / 16, THREADS = 32 * PX_CONVERTERS, STEP = THREADS / CH, NS = T::NS, RAW = T::RAW;
+  const int row0 = ct / CH, chunk = ct % CH, c = 2 * (chunk & 3), lane = ct & 31;
+  for (int i = 0; i < 2 * n; ++i) {
+    bool is_v;
+    const int tail = reach - (u0 + unit_of(i, n, &is_v)) * PX_N;
+    const uint32_t half = halves + i;
+    if (!warp_wait(&sm.raw_full[half % RAW], half / RAW & 1u, &sm.failed)) return;
+    if (!warp_wait(&sm.empty[half % NS], (half / NS & 1u) ^ 1u, &sm.failed)) return;
+    const uint8_t *from = sm.raw[half % RAW] + chunk * 16;
+    uint8_t *slot = sm.ring[half % NS] + (chunk >> 2) * (PX_N * 128);
+#pragma unroll
+    for (int k = 0; k < PX_N / STEP; ++k) {
+      const int row = row0 + k * STEP;
+      uint4 w = *reinterpret_cast<const uint4 *>(from + row * DH);
+      if (row >= tail) w = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4 *>(slot + row * 128 + ((c ^ (row & 7)) << 4)) =
+          make_uint4(e4m3x2(w.x & 0xffffu), e4m3x2(w.x >> 16), e4m3x2(w.y & 0xffffu), e4m3x2(w.y >> 16));
+      *reinterpret_cast<uint4 *>(slot + row * 128 + (((c + 1) ^ (row & 7)) << 4)) =
+          make_uint4(e4m3x2(w.z & 0xffffu), e4m3x2(w.z >> 16), e4m3x2(w.w & 0xffffu), e4m3x2(w.w >> 16));
+    }
     fence_async_proxy();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.full[half % NS]);
-  };
-
-  uint32_t half = halves;
-  if constexpr (!CODES) {
-    const uint32_t ring = smem_u32(sm.ring);
-    const auto copy = [&](const Places &p, int unit, int v) {
-      if (!wait_empty(half)) return false;
-#pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        bool live;
-        const uint8_t *src = source_of(p, unit, i, v, &live);
-        const int row = row0 + i * STEP;
-        cp_async16(ring + (half % NS) * T::SLOT + (chunk >> 3) * (PX_N * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4), src, live);
-      }
-      cp_commit();
-      if (half - halves >= LAG) {
-        cp_wait<LAG>();
-        announce(half - LAG);
-      }
-      ++half;
-      return true;
-    };
-    Places before = {};
-    bool ok = true;
-    for (int u = 0; u <= n && ok; ++u) {
-      Places p = {};
-      if (u < n) {
-        p = places(u0 + u);
-        ok = copy(p, u0 + u, 0);
-        if (warp == 0 && lane == 0) {
-          sm.live[(tiles + u) % PX_TILES] = p.live;
-          mbar_arrive(&sm.unit[(tiles + u) % PX_TILES]);
-        }
-      }
-      if (u > 0) ok = ok && copy(before, u0 + u - 1, 1);
-      before = p;
-    }
-    cp_wait<0>();
-    if (ok)
-      for (uint32_t i = max(halves, half - min(half, (uint32_t)LAG)); i < half; ++i) announce(i);
-  } else {
-    // E4M3: codes through registers, on their way while the half before them is converted
-    uint4 code[2][LOADS];
-    float ks = 0.f, vs = 0.f;  // scales of position lt of the unit, for the first PX_N loaders
-    const auto request = [&](const Places &p, int unit, int v) {
-#pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        bool live;
-        const uint8_t *src = source_of(p, unit, i, v, &live);
-        code[v][i] = live ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    const auto request_scales = [&](const Places &p, int unit) {
-      if (lt >= PX_N) return;
-      int page = p.page[0], at = p.at[0];
-#pragma unroll
-      for (int i = 1; i < 4; ++i)
-        if (lt >> 4 == i) page = p.page[i], at = p.at[i];
-      ks = vs = 0.f;
-      if ((p.live >> (lt >> 4) & 1u) && unit * PX_N + lt < reach) {
-        const int off = at + (lt & 15);
-        ks = a.pages.k_scale[page * a.pages.k_scale_stride[0] + h * a.pages.k_scale_stride[1] + off * a.pages.k_scale_stride[2]];
-        vs = a.pages.v_scale[page * a.pages.v_scale_stride[0] + h * a.pages.v_scale_stride[1] + off * a.pages.v_scale_stride[2]];
-      }
-    };
-    const auto store = [&](int v) {
-      if (!wait_empty(half)) return false;
-      uint8_t *slot = sm.ring[half % NS];
-#pragma unroll
-      for (int i = 0; i < LOADS; ++i) {
-        const int row = row0 + i * STEP, c = 2 * (chunk & 3);
-        uint8_t *to = slot + (chunk >> 2) * (PX_N * 128) + row * 128;
-        const uint4 w = code[v][i];
-        *reinterpret_cast<uint4 *>(to + ((c ^ (row & 7)) << 4)) =
-            make_uint4(e4m3x2(w.x & 0xffffu), e4m3x2(w.x >> 16), e4m3x2(w.y & 0xffffu), e4m3x2(w.y >> 16));
-        *reinterpret_cast<uint4 *>(to + (((c + 1) ^ (row & 7)) << 4)) =
-            make_uint4(e4m3x2(w.z & 0xffffu), e4m3x2(w.z >> 16), e4m3x2(w.w & 0xffffu), e4m3x2(w.w >> 16));
-      }
-      announce(half);
-      ++half;
-      return true;
-    };
-    Places p = {};
-    if (n > 0) {
-      p = places(u0);
-      request(p, u0, 0);
-      request_scales(p, u0);
-    }
-    bool ok = true;
-    for (int u = 0; u <= n && ok; ++u) {
-      const Places mine = p;
-      if (u < n) {
-        ok = store(0);
-        const uint32_t i = (tiles + u) % PX_TILES;
-        if (ok && lt < PX_N) {
-          sm.scale[i][0][lt] = ks;
-          sm.scale[i][CODES ? 1 : 0][lt] = vs;
-          sm.scale[i][CODES ? 2 : 0][lt] = log2_scale(vs);
-          if (lt == 0) sm.live[i] = mine.live;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.unit[i]);
-        }
-        if (u + 1 < n) {
-          p = places(u0 + u + 1);
-          request(p, u0 + u + 1, 0);
-          request_scales(p, u0 + u + 1);
-        }
-      }
-      if (u > 0) ok = ok && store(1);
-      if (u < n) request(mine, u0 + u, 1);
+    if (lane == 0) {
+      mbar_arrive(&sm.full[half % NS]);
+      mbar_arrive(&sm.raw_empty[half % RAW]);
     }
   }
 }
 
-// One thread.
+// One warp, an elected lane of which issues.
 template <int KIND, int DH, bool SPLIT>
 __device__ __forceinline__ void multiply_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_t tmem, int n, uint32_t tiles, uint32_t halves) {
   constexpr int NS = PxShape<KIND, DH, SPLIT>::NS, KB = DH / 64;
   constexpr uint32_t S_DESC = px_idesc(PX_N, KIND == PG_BF16, false), O_DESC = px_idesc(DH, KIND == PG_BF16, true);
-  const uint32_t q = smem_u32(sm.q);
+  // descriptors of the first step; those of the others are 16-byte units further (addresses stay below 2^18)
+  const uint64_t q0 = px_desc(smem_u32(sm.q), 16), k0 = px_desc(smem_u32(sm.ring), 16), v0 = px_desc(smem_u32(sm.ring), PX_N * 128);
+  constexpr uint32_t SLOT = PxShape<KIND, DH, SPLIT>::SLOT / 16;
   uint32_t half = halves;
+#pragma unroll 1
   for (int j = 0; j <= n; ++j) {
     if (j < n) {  // S = Q K^T
       const uint32_t tile = tiles + j, to = tmem + (tile & 1u) * PX_N;
       const Half<NS> x(half);
-      if (!px_wait(&sm.full[x.slot], x.round, &sm.failed)) return;
-      if (j >= 2 && !px_wait(&sm.pv_done, tile & 1u, &sm.failed)) return;  // unit j - 2 is done with the buffer
+      if (!warp_wait(&sm.full[x.slot], x.round, &sm.failed)) return;
+      if (j >= 2 && !warp_wait(&sm.pv_done[tile & 1u], (tile - 2) >> 1 & 1u, &sm.failed)) return;  // unit j - 2 is done with it
       tc_fence_after();
-      const uint32_t k = smem_u32(sm.ring[x.slot]);
+      if (elect_one()) {
+        const uint64_t k = k0 + x.slot * SLOT;
 #pragma unroll
-      for (int p = 0; p < (SPLIT ? 2 : 1); ++p)
+        for (int p = 0; p < (SPLIT ? 2 : 1); ++p)
 #pragma unroll
-        for (int s = 0; s < DH / 16; ++s)
-          tc_mma(to, px_desc(q + (p * KB + s / 4) * (PX_M * 128) + s % 4 * 32, 16), px_desc(k + s / 4 * (PX_N * 128) + s % 4 * 32, 16),
-                 S_DESC, p || s ? 1u : 0u);
-      tc_commit(&sm.empty[x.slot]);
-      tc_commit(&sm.s_full[tile & 1u]);
+          for (int s = 0; s < DH / 16; ++s)
+            tc_mma(to, q0 + (p * KB + s / 4) * (PX_M * 8) + s % 4 * 2, k + s / 4 * (PX_N * 8) + s % 4 * 2, S_DESC, p || s ? 1u : 0u);
+        tc_commit(&sm.empty[x.slot]);
+        tc_commit(&sm.s_full[tile & 1u]);
+      }
+      __syncwarp();
       ++half;
     }
     if (j > 0) {  // O += P V
       const uint32_t tile = tiles + j - 1, p = tmem + (tile & 1u) * PX_N;
       const Half<NS> x(half);
-      if (!px_wait(&sm.p_full[tile & 1u], tile >> 1 & 1u, &sm.failed)) return;
-      if (!px_wait(&sm.full[x.slot], x.round, &sm.failed)) return;
+      if (!warp_wait(&sm.p_full[tile & 1u], tile >> 1 & 1u, &sm.failed)) return;
+      if (!warp_wait(&sm.full[x.slot], x.round, &sm.failed)) return;
       tc_fence_after();
-      const uint32_t v = smem_u32(sm.ring[x.slot]);
+      if (elect_one()) {
+        const uint64_t v = v0 + x.slot * SLOT;
 #pragma unroll
-      for (int s = 0; s < PX_N / 16; ++s)
+        for (int s = 0; s < PX_N / 16; ++s)
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
-          tc_mma_ts(tmem + 2 * PX_N, p + s * 16 + part * 8, px_desc(v + s * 2048, PX_N * 128), O_DESC, j > 1 || s || part ? 1u : 0u);
-      tc_commit(&sm.empty[x.slot]);
-      tc_commit(&sm.pv_done);
+          for (int part = 0; part < 2; ++part)
+            tc_mma_ts(tmem + 2 * PX_N, p + s * 16 + part * 8, v + s * 128, O_DESC, j > 1 || s || part ? 1u : 0u);
+        tc_commit(&sm.empty[x.slot]);
+        tc_commit(&sm.pv_done[tile & 1u]);
+      }
+      __syncwarp();
       ++half;
     }
   }
@@ -453,7 +522,7 @@ __device__ __forceinline__ void multiply_item(PxSmem<KIND, DH, SPLIT> &sm, uint3
 template <int KIND, int DH, bool SPLIT>
 __device__ __forceinline__ bool soften_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_t tmem, int row, bool rows, int lim, int u0, int n,
                                             uint32_t tiles, float *m_out, float *l_out) {
-  const float rs = sm.rs[row];
+  const float rs = lim > 0 ? sm.rs[row] : 1.f;
   const uint32_t t_o = tmem + 2 * PX_N;
   const int lane = row & 31;
   float m = -INFINITY, l = 0.f;
@@ -465,74 +534,76 @@ __device__ __forceinline__ bool soften_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_
     tc_fence_after();
     if (rows) {
       const uint32_t live = sm.live[tile % PX_TILES];
-      float s[2][32];
-      tmem_ld32(t_s, s[0]);
-      tmem_ld32(t_s + 32, s[1]);
-      tmem_wait_ld();
-      if (KIND == PG_E4M3) {
-        const float *ks = sm.scale[KIND == PG_E4M3 ? tile % PX_TILES : 0][0];
+      const bool whole = __all_sync(0xffffffffu, left >= PX_N && live == 15u);
+      const float *scale = &sm.scale[KIND == PG_E4M3 ? tile % PX_TILES : 0][0][0];  // E4M3: of K, V, log2 of V's
+      // 32 positions at a time, twice over, in loops: most blocks come here a few times only, and code that is not there yet
+      // costs more than reading the scores again
+      const auto scores = [&](int c, float(&s)[32]) {
+        tmem_ld32(t_s + c, s);
+        tmem_wait_ld();
+        if (KIND == PG_E4M3) {
 #pragma unroll
-        for (int e = 0; e < PX_N; ++e) s[e / 32][e % 32] *= ks[KIND == PG_E4M3 ? e : 0];
-      }
-      if (!__all_sync(0xffffffffu, left >= PX_N && live == 15u)) {
+          for (int e = 0; e < 32; ++e) s[e] *= scale[c + e];
+        }
+        if (!whole) {
 #pragma unroll
-        for (int e = 0; e < PX_N; ++e)
-          if (e >= left || !(live >> (e / 16) & 1u)) s[e / 32][e % 32] = -INFINITY;
-      }
+          for (int e = 0; e < 32; ++e)
+            if (c + e >= left || !(live >> ((c + e) >> 4) & 1u)) s[e] = -INFINITY;
+        }
+      };
       float top = -INFINITY;
-      if (KIND == PG_E4M3) {
-        const float *ls = sm.scale[KIND == PG_E4M3 ? tile % PX_TILES : 0][KIND == PG_E4M3 ? 2 : 0];
+#pragma unroll 1
+      for (int c = 0; c < PX_N; c += 32) {
+        float s[32];
+        scores(c, s);
 #pragma unroll
-        for (int e = 0; e < PX_N; ++e) top = fmaxf(top, fmaf(s[e / 32][e % 32], rs, ls[KIND == PG_E4M3 ? e : 0]));
-      } else {
-#pragma unroll
-        for (int e = 0; e < PX_N; ++e) top = fmaxf(top, s[e / 32][e % 32]);
-        top *= rs;
+        for (int e = 0; e < 32; ++e) top = fmaxf(top, KIND == PG_E4M3 ? fmaf(s[e], rs, scale[2 * PX_N + c + e]) : s[e]);
       }
+      if (KIND != PG_E4M3) top *= rs;
       const bool far = top > m + P_STEP;
       if (__any_sync(0xffffffffu, far)) {
         const float mn = far ? top : m, f = far && m != -INFINITY ? ex2(m - mn) : 1.f;
         m = mn;
         l *= f;
         if (j > 0) {
-          if (!warp_wait(&sm.pv_done, (tile - 1) & 1u, &sm.failed)) return false;
+          if (!warp_wait(&sm.pv_done[(tile - 1) & 1u], (tile - 1) >> 1 & 1u, &sm.failed)) return false;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < DH; c += 32) {
-            float o[32];
-            tmem_ld32(t_o + c, o);
-            tmem_wait_ld();
+          for (int c = 0; c < DH; c += 16) {
+            float o[16];
+            tmem_ld16(t_o + c, o);
+            uint32_t w[16];
 #pragma unroll
-            for (int k = 0; k < 32; k += 16) {
-              uint32_t w[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[k + e] * f);
-              tmem_st16(t_o + c + k, w);
-            }
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
+            tmem_st16(t_o + c, w);
           }
         }
       }
       const float bias = P_BIAS - (m == -INFINITY ? 0.f : m);
       float part[2] = {0.f, 0.f};
+#pragma unroll 1
+      for (int c = 0; c < PX_N; c += 32) {
+        float s[32];
+        scores(c, s);
 #pragma unroll
-      for (int c = 0; c < PX_N; c += 16) {  // the weights of 16 positions: eight columns of first parts, eight of second ones
-        uint32_t w[16];
+        for (int k = 0; k < 32; k += 16) {  // the weights of 16 positions: eight columns of first parts, eight of second ones
+          uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          float y[2];
+          for (int e = 0; e < 16; e += 2) {
+            float y[2];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int at = c + e + k;
-            y[k] = ex2(fmaf(s[at / 32][at % 32], rs, bias));
-            part[k] += y[k];
-            if (KIND == PG_E4M3) y[k] *= sm.scale[KIND == PG_E4M3 ? tile % PX_TILES : 0][KIND == PG_E4M3 ? 1 : 0][KIND == PG_E4M3 ? at : 0];
+            for (int i = 0; i < 2; ++i) {
+              y[i] = ex2(fmaf(s[k + e + i], rs, bias));
+              part[i] += y[i];
+              if (KIND == PG_E4M3) y[i] *= scale[PX_N + c + k + e + i];
+            }
+            const uint32_t hi = pack16<KIND>(y[0], y[1]);
+            const float2 b = unpack16<KIND>(hi);
+            w[e / 2] = hi;
+            w[8 + e / 2] = pack16<KIND>(y[0] - b.x, y[1] - b.y);
           }
-          const uint32_t hi = pack16<KIND>(y[0], y[1]);
-          const float2 b = unpack16<KIND>(hi);
-          w[e / 2] = hi;
-          w[8 + e / 2] = pack16<KIND>(y[0] - b.x, y[1] - b.y);
+          tmem_st16(t_s + c + k, w);
         }
-        tmem_st16(t_s + c, w);
       }
       l += part[0] + part[1];
       tmem_wait_st();
@@ -541,9 +612,7 @@ __device__ __forceinline__ bool soften_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.p_full[tile & 1u]);
   }
-  // the last two: a barrier tells a phase from the one before it only, and so far no more than unit n - 3 is known to be done
-  if (n > 1 && !warp_wait(&sm.pv_done, (tiles + n) & 1u, &sm.failed)) return false;
-  if (n > 0 && !warp_wait(&sm.pv_done, (tiles + n - 1) & 1u, &sm.failed)) return false;
+  if (n > 0 && !warp_wait(&sm.pv_done[(tiles + n - 1) & 1u], (tiles + n - 1) >> 1 & 1u, &sm.failed)) return false;
   *m_out = m;
   *l_out = l;
   return true;
@@ -551,86 +620,203 @@ __device__ __forceinline__ bool soften_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_
 
 // ---- the kernel ----------------------------------------------------------------------------------------------
 
+// The rows of queries of an item, in the layout of an MMA operand, by every warp but the loader.
 template <int KIND, int DH, bool SPLIT>
-__global__ void __launch_bounds__(PX_THREADS, PxShape<KIND, DH, SPLIT>::BLOCKS) prefix_kernel(const PrefixArgs a) {
+__device__ __forceinline__ void stage_queries(const PrefixArgs &a, PxSmem<KIND, DH, SPLIT> &sm, int first, int h, int group, int rows) {
+  constexpr int KB = DH / 64, E = DH / 32, AHEAD = 4, WARPS = PX_THREADS / 32 - 1, CH = DH / 8;
+  const int w = threadIdx.x >> 5, warp = w < PX_LOADER ? w : w - 1, lane = threadIdx.x & 31;
+  const bool bf16_q = a.q_dtype == KIE_BF16;
+  const int size = paged_dtype_bytes(a.q_dtype);
+  const uintptr_t odd = (uintptr_t)a.q | (uintptr_t)(a.q_stride[0] * size) | (uintptr_t)(a.q_stride[1] * size);
+  if (!SPLIT && !(KIND == PG_E4M3 && bf16_q) && a.scale > 0.f && odd % 16 == 0) {  // as they are, 16 bytes at a time
+    if (lane == 0)
+      for (int r = warp; r < rows; r += WARPS) sm.rs[r] = fmaxf(a.scale, FLT_MIN) * LOG2E;
+    const uint16_t *q = static_cast<const uint16_t *>(a.q) + (int64_t)first * a.q_stride[0] + (int64_t)h * group * a.q_stride[1];
+#pragma unroll 4
+    for (int i = warp * 32 + lane; i < rows * CH; i += 32 * WARPS) {
+      const int r = i / CH, c = i % CH;
+      const uint4 x = *reinterpret_cast<const uint4 *>(q + r / group * a.q_stride[0] + r % group * a.q_stride[1] + c * 8);
+      *reinterpret_cast<uint4 *>(sm.q + (c >> 3) * (PX_M * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
+    }
+    return;
+  }
+  // a warp takes a row at a time, a lane E neighbouring elements of it; the loads of four rows are on their way together
+  const bool vec = odd % (E * size) == 0;
+#pragma unroll 1
+  for (int r0 = warp; r0 < rows; r0 += AHEAD * WARPS) {
+    uint32_t raw[AHEAD][SPLIT ? E : E / 2];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int r = r0 + k * WARPS;
+      const int64_t at = (int64_t)(first + r / group) * a.q_stride[0] + (int64_t)(h * group + r % group) * a.q_stride[1] + lane * E;
+      load_query<SPLIT, E>(a, vec, r < rows, at, raw[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int r = r0 + k * WARPS;
+      if (r >= rows) break;
+      float q[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) q[e] = SPLIT ? __uint_as_float(raw[k][SPLIT ? e : 0]) : 0.f;
+      if (!SPLIT) {
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          const float2 f = bf16_q ? unpack16<PG_BF16>(raw[k][e]) : unpack16<PG_F16>(raw[k][e]);
+          q[2 * e] = f.x, q[2 * e + 1] = f.y;
+        }
+      }
+      // Where 16 bits do not hold every query, the row's largest element is brought to [2^13, 2^14) by a power of two. The
+      // sign of the scale goes into the queries, so that the largest score is the largest product.
+      float up = a.scale < 0.f ? -1.f : 1.f, rs = fmaxf(fabsf(a.scale), FLT_MIN) * LOG2E;
+      if (SPLIT || (KIND == PG_E4M3 && bf16_q)) {
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(q[e]));
+        top = warp_max(top);
+        int e2 = 0;
+        if (top > 0.f && top <= FLT_MAX) e2 = max(-120, min(120, 140 - (int)(__float_as_uint(top) >> 23)));
+        up *= __int_as_float((127 + e2) << 23);
+        rs *= __int_as_float((127 - e2) << 23);
+      }
+      if (lane == 0) sm.rs[r] = rs;
+      uint32_t hi[E / 2], lo[E / 2];
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        const float u = q[2 * e] * up, v = q[2 * e + 1] * up;
+        if (!SPLIT) {
+          hi[e] = pack16<KIND>(u, v);
+          lo[e] = 0u;
+        } else {
+          // The first part is cut off, not rounded, and a remainder of 0 becomes the least there is: both parts then have
+          // the sign of the query, and an infinity in K gives the score that it should instead of NaN.
+          const float f[2] = {u, v};
+          uint16_t parts[2][2];
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const __half b = __float2half_rz(f[s]);
+            uint16_t low = __half_as_ushort(__float2half_rn(f[s] - __half2float(b)));
+            if ((low & 0x7fffu) == 0) low = (uint16_t)((__float_as_uint(f[s]) >> 16 & 0x8000u) | 1u);
+            if ((__half_as_ushort(b) & 0x7fffu) == 0) low = 0;
+            parts[0][s] = __half_as_ushort(b);
+            parts[1][s] = low;
+          }
+          hi[e] = parts[0][0] | (uint32_t)parts[0][1] << 16;
+          lo[e] = parts[1][0] | (uint32_t)parts[1][1] << 16;
+        }
+      }
+      const int byte = lane * E * 2;  // of the row; 128 bytes to a block
+      uint8_t *to = sm.q + (byte >> 7) * (PX_M * 128) + r * 128 + ((((byte >> 4) & 7) ^ (r & 7)) << 4) + (byte & 15);
+#pragma unroll
+      for (int p = 0; p < (SPLIT ? 2 : 1); ++p) {
+        const uint32_t(&y)[E / 2] = p ? lo : hi;
+        if (E == 4)
+          *reinterpret_cast<uint2 *>(to + p * KB * PX_M * 128) = make_uint2(y[0], y[E / 2 - 1]);
+        else
+          *reinterpret_cast<uint32_t *>(to + p * KB * PX_M * 128) = y[0];
+      }
+    }
+  }
+}
+
+template <int KIND, int DH, bool SPLIT>
+__global__ void __launch_bounds__(PX_THREADS, PxShape<KIND, DH, SPLIT>::BLOCKS)
+prefix_kernel(const PrefixArgs a, const __grid_constant__ PrefixMaps maps) {
   using T = PxShape<KIND, DH, SPLIT>;
   using Sm = PxSmem<KIND, DH, SPLIT>;
-  constexpr int NS = T::NS, KB = DH / 64;  // 64-dim blocks of a row
+  constexpr int NS = T::NS;
   extern __shared__ __align__(1024) uint8_t px_raw[];
   Sm &sm = *reinterpret_cast<Sm *>(px_raw);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5;
   const int heads = a.pages.n_kv_heads, group = a.n_heads / heads, members = PX_M / group;
-  wait_for_previous();
-
-  // ---- where this block's run begins, and (each row by one block) what the join has to know of a row
-  __shared__ long long s_place;  // of the item, in the list
-  __shared__ int s_g, s_edge[2];
-  long long total, per, v0;
-  {
-    int *starts = reinterpret_cast<int *>(px_raw);  // [n_groups + 1]; the ring and queries are not in use yet
-    long long *base = reinterpret_cast<long long *>(px_raw + (KIE_PAGED_MAX_GROUPS + 4) * 4);
-    const int G = a.n_groups;
-    for (int g = tid; g <= G; g += PX_THREADS) starts[g] = clamp_start(a, g);
-    __syncthreads();
-    bool falls = false;
-    for (int g = tid; g < G; g += PX_THREADS) falls |= starts[g + 1] < starts[g];
-    if (__syncthreads_or(falls)) {
-      if (tid == 0)
-        for (int g = 0; g < G; ++g) starts[g + 1] = max(starts[g + 1], starts[g]);
-      __syncthreads();
-    }
-    const int each = (G + PX_THREADS - 1) / PX_THREADS, g0 = min(tid * each, G), g1 = min(g0 + each, G);
-    long long mine = 0;
-    for (int g = g0; g < g1; ++g) mine += places_of(a, group_of(a, g, starts[g], starts[g + 1]), members);
-    long long at = sum_before(mine, &total);
-    per = max((total + gridDim.x - 1) / gridDim.x, (long long)PX_MIN_RUN);
-    v0 = blockIdx.x * per;
-    for (int g = g0; g < g1; ++g) {
-      const long long n = places_of(a, group_of(a, g, starts[g], starts[g + 1]), members);
-      base[g] = at;
-      if (v0 >= at && v0 < at + n) s_g = g, s_place = at, s_edge[0] = starts[g], s_edge[1] = starts[g + 1];
-      at += n;
-    }
-    __syncthreads();
-    for (int b = blockIdx.x * PX_THREADS + tid; b < a.n_seqs; b += gridDim.x * PX_THREADS) {
-      int lo = 0, hi = G + 1;  // the number of starts that are not behind the row
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (starts[mid] <= b)
-          lo = mid + 1;
-        else
-          hi = mid;
-      }
-      const int g = lo - 1;
-      PrefixRow row = {};
-      if (g >= 0 && g < G) {
-        const Group x = group_of(a, g, starts[g], starts[g + 1]);
-        const int t = (b - x.start) / members, first = x.start + t * members;
-        row.lo = min(x.prefix, length_of(a, b));
-        row.units = x.units;
-        row.place = base[g] + (long long)t * heads * (x.units + PX_ITEM_COST);
-        row.slot = first * a.n_heads;
-        row.rows = min(members, x.end - first) * group;
-        row.local = (b - first) * group;
-      }
-      a.row_lo[b] = row.lo;
-      a.rows[b] = row;
-    }
-    if (blockIdx.x == 0 && tid == 0) *a.per_block = per;
-    __syncthreads();
-  }
-  if (v0 >= total) return;
-  const long long v1 = min(v0 + per, total);
-
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(&sm.full[i], PX_LOAD), mbar_init(&sm.empty[i], 1);
-    for (int i = 0; i < PX_TILES; ++i) mbar_init(&sm.unit[i], KIND == PG_E4M3 ? PX_N / 32 : 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&sm.s_full[i], 1), mbar_init(&sm.p_full[i], PX_SOFT);
-    mbar_init(&sm.pv_done, 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&sm.full[i], KIND == PG_E4M3 ? PX_CONVERTERS : 1), mbar_init(&sm.empty[i], 1);
+    for (int i = 0; i < T::RAW; ++i) mbar_init(&sm.raw_full[i], 1), mbar_init(&sm.raw_empty[i], PX_CONVERTERS);
+    for (int i = 0; i < PX_TILES; ++i) mbar_init(&sm.unit[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.s_full[i], 1), mbar_init(&sm.p_full[i], PX_SOFT), mbar_init(&sm.pv_done[i], 1);
+    mbar_init(&sm.fix, 1);
     fence_barrier_init();
     sm.failed = 0;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.v) : "memory");
   }
-  if (warp == 0) {
+  wait_for_previous();
+
+  // ---- where this block's run begins
+  const int G = a.n_groups, each = (G + PX_THREADS - 1) / PX_THREADS, g0 = min(tid * each, G), g1 = min(g0 + each, G);
+  int *starts = reinterpret_cast<int *>(px_raw);  // [n_groups + 1]; the ring and queries are not in use yet
+  bool falls = false;
+  long long mine = 0, total;
+  for (int g = g0; g < g1; ++g) {
+    const int start = clamp_start(a, g), end = clamp_start(a, g + 1);
+    falls |= end < start;
+    mine += places_of(a, group_of(a, g, start, end), members);
+  }
+  falls = __syncthreads_or(falls);
+  const auto start_of = [&](int g) { return falls ? starts[g] : clamp_start(a, g); };
+  if (falls) {  // a start below an earlier one counts as that one
+    for (int g = tid; g <= G; g += PX_THREADS) starts[g] = clamp_start(a, g);
+    __syncthreads();
+    if (tid == 0)
+      for (int g = 0; g < G; ++g) starts[g + 1] = max(starts[g + 1], starts[g]);
+    __syncthreads();
+    mine = 0;
+    for (int g = g0; g < g1; ++g) mine += places_of(a, group_of(a, g, start_of(g), start_of(g + 1)), members);
+  }
+  const long long before = sum_before(mine, sm.sums, &total);
+  const long long per = max(divide_up(total, gridDim.x), (long long)PX_MIN_RUN), v0 = blockIdx.x * per, v1 = min(v0 + per, total);
+  if (v0 >= before && v0 < before + mine) {
+    long long at = before;
+    int g = g0;
+    for (;; ++g) {
+      const long long n = places_of(a, group_of(a, g, start_of(g), start_of(g + 1)), members);
+      if (v0 < at + n) break;
+      at += n;
+    }
+    sm.g = g, sm.place = at, sm.edge[0] = start_of(g), sm.edge[1] = start_of(g + 1);
+  }
+  // What the join has to know of a row: by the last blocks, which have the least to do
+  const int rows0 = (int)(gridDim.x - 1 - blockIdx.x) * PX_THREADS;
+  for (int b0 = rows0; b0 < a.n_seqs; b0 += gridDim.x * PX_THREADS) {
+    long long *base = reinterpret_cast<long long *>(px_raw + (KIE_PAGED_MAX_GROUPS + 4) * 4);
+    if (b0 == rows0) {
+      long long at = before;
+      for (int g = g0; g < g1; ++g) {
+        if (!falls) starts[g] = clamp_start(a, g);
+        base[g] = at;
+        at += places_of(a, group_of(a, g, start_of(g), start_of(g + 1)), members);
+      }
+      if (tid == 0 && !falls) starts[G] = clamp_start(a, G);
+      __syncthreads();
+    }
+    const int b = b0 + tid;
+    if (b >= a.n_seqs) continue;
+    int lo = 0, hi = G + 1;  // the number of starts that are not behind the row
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (starts[mid] <= b)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    const int g = lo - 1;
+    PrefixRow row = {};
+    if (g >= 0 && g < G) {
+      const Group x = group_of(a, g, starts[g], starts[g + 1]);
+      const int t = (b - x.start) / members, first = x.start + t * members;
+      row.lo = min(x.prefix, length_of(a, b));
+      row.units = x.units;
+      row.place = base[g] + (long long)t * heads * (x.units + PX_ITEM_COST);
+      row.slot = first * a.n_heads;
+      row.rows = min(members, x.end - first) * group;
+      row.local = (b - first) * group;
+    }
+    a.row_lo[b] = row.lo;
+    a.rows[b] = row;
+  }
+  if (blockIdx.x == 0 && tid == 0) *a.per_block = per;
+  if (v0 >= total) return;
+
+  if (warp == PX_ISSUER) {
     tmem_alloc(&sm.tmem, PX_TMEM);
     tmem_relinquish();
   }
@@ -640,20 +826,14 @@ __global__ void __launch_bounds__(PX_THREADS, PxShape<KIND, DH, SPLIT>::BLOCKS) 
   const uint32_t tmem = sm.tmem, t_o = tmem + 2 * PX_N;
   const uint32_t my_lanes = (uint32_t)((warp & 3) * 32) << 16;
 
-  uint32_t tiles = 0, halves = 0;  // units of all items so far; halves of them (K or V) in the ring
-  int g = s_g;
-  Group x = group_of(a, g, s_edge[0], s_edge[1]);
-  const bool bf16_q = a.q_dtype == KIE_BF16;
-  const bool q_vec = [&] {
-    const int size = paged_dtype_bytes(a.q_dtype);
-    return ((uintptr_t)a.q | (uintptr_t)(a.q_stride[0] * size) | (uintptr_t)(a.q_stride[1] * size)) % (DH / 32 * size) == 0;
-  }();
-
-  long long place = s_place;
+  uint32_t tiles = 0, halves = 0, fixes = 0;  // units of all items so far; halves of them (K or V) in the ring; mended halves
+  int g = sm.g;
+  Group x = group_of(a, g, sm.edge[0], sm.edge[1]);
+  long long place = sm.place;
   int item;  // of the group: tile * heads + head
   {
-    const int span = x.units + PX_ITEM_COST;
-    item = (int)((v0 - place) / span);
+    const unsigned span = x.units + PX_ITEM_COST;
+    item = (int)(divide_up(v0 - place + 1, span) - 1);
     place += (long long)item * span;
   }
   for (;;) {
@@ -662,144 +842,48 @@ __global__ void __launch_bounds__(PX_THREADS, PxShape<KIND, DH, SPLIT>::BLOCKS) 
     const int rows = min(members, x.end - first) * group;
     const int u0 = (int)max(0ll, v0 - place - PX_ITEM_COST), u1 = (int)min((long long)x.units, v1 - place - PX_ITEM_COST);
     if (u1 > u0) {
-      // the group's longest row (the first of them): its pages are read
-      if (tid == 0) sm.best = 0;
-      __syncthreads();
-      unsigned long long mine = 0;
-      for (int b = x.start + tid; b < x.end; b += PX_THREADS)
-        mine = max(mine, (unsigned long long)min(x.prefix, length_of(a, b)) << 32 | (uint32_t)~b);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) mine = max(mine, __shfl_xor_sync(0xffffffffu, mine, o));
-      if (lane == 0) atomicMax(&sm.best, mine);
-      // queries: a warp takes a row at a time, a lane DH / 32 neighbouring elements of it
-      for (int r = warp; r < PX_M; r += PX_THREADS / 32) {
-        constexpr int E = DH / 32;
-        float q[E];
-        const int64_t at = (int64_t)(first + r / group) * a.q_stride[0] + (int64_t)(h * group + r % group) * a.q_stride[1] + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) q[e] = 0.f;
-        if (r < rows) {
-          if (a.q_dtype == KIE_F32) {
-            const float *p = static_cast<const float *>(a.q) + at;
-            if (q_vec && E == 4) {
-              const float4 w = *reinterpret_cast<const float4 *>(p);
-              q[0] = w.x, q[1] = w.y, q[E - 2] = w.z, q[E - 1] = w.w;
-            } else {
-#pragma unroll
-              for (int e = 0; e < E; ++e) q[e] = p[e];
-            }
-          } else {
-            const uint16_t *p = static_cast<const uint16_t *>(a.q) + at;
-            uint32_t w[E / 2];
-            if (q_vec && E == 4) {
-              const uint2 y = *reinterpret_cast<const uint2 *>(p);
-              w[0] = y.x, w[E / 2 - 1] = y.y;
-            } else if (q_vec) {
-              w[0] = *reinterpret_cast<const uint32_t *>(p);
-            } else {
-#pragma unroll
-              for (int e = 0; e < E / 2; ++e) w[e] = p[2 * e] | (uint32_t)p[2 * e + 1] << 16;
-            }
-#pragma unroll
-            for (int e = 0; e < E / 2; ++e) {
-              const float2 f = bf16_q ? unpack16<PG_BF16>(w[e]) : unpack16<PG_F16>(w[e]);
-              q[2 * e] = f.x, q[2 * e + 1] = f.y;
-            }
-          }
-        }
-        // Where 16 bits do not hold every query, the row's largest element is brought to [2^13, 2^14) by a power of two. The
-        // sign of the scale goes into the queries, so that the largest score is the largest product.
-        float up = a.scale < 0.f ? -1.f : 1.f, rs = fmaxf(fabsf(a.scale), FLT_MIN) * LOG2E;
-        if (SPLIT || (KIND == PG_E4M3 && bf16_q)) {
-          float top = 0.f;
-#pragma unroll
-          for (int e = 0; e < E; ++e) top = fmaxf(top, fabsf(q[e]));
-          top = warp_max(top);
-          int e2 = 0;
-          if (top > 0.f && top <= FLT_MAX) e2 = max(-120, min(120, 140 - (int)(__float_as_uint(top) >> 23)));
-          up *= __int_as_float((127 + e2) << 23);
-          rs *= __int_as_float((127 - e2) << 23);
-        }
-        if (lane == 0) sm.rs[r] = rs;
-        uint32_t hi[E / 2], lo[E / 2];
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-          const float u = q[2 * e] * up, w = q[2 * e + 1] * up;
-          if (!SPLIT) {
-            hi[e] = pack16<KIND>(u, w);
-            lo[e] = 0u;
-          } else {
-            // The first part is cut off, not rounded, and a remainder of 0 becomes the least there is: both parts then
-            // have the sign of the query, and an infinity in K gives the score that it should instead of NaN.
-            const float f[2] = {u, w};
-            uint16_t parts[2][2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const __half b = __float2half_rz(f[k]);
-              const float rest = f[k] - __half2float(b);
-              __half c = __float2half_rn(rest);
-              const uint16_t sign = (__float_as_uint(f[k]) >> 16) & 0x8000u;
-              uint16_t low = __half_as_ushort(c);
-              if ((low & 0x7fffu) == 0) low = sign | 1u;
-              if ((__half_as_ushort(b) & 0x7fffu) == 0) low = 0;
-              parts[0][k] = __half_as_ushort(b);
-              parts[1][k] = low;
-            }
-            hi[e] = parts[0][0] | (uint32_t)parts[0][1] << 16;
-            lo[e] = parts[1][0] | (uint32_t)parts[1][1] << 16;
-          }
-        }
-        const int byte = lane * E * 2;  // of the row; 128 bytes to a block
-        uint8_t *to = sm.q + (byte >> 7) * (PX_M * 128) + r * 128 + ((((byte >> 4) & 7) ^ (r & 7)) << 4) + (byte & 15);
-#pragma unroll
-        for (int p = 0; p < (SPLIT ? 2 : 1); ++p) {
-          const uint32_t(&w)[E / 2] = p ? lo : hi;
-          if (E == 4)
-            *reinterpret_cast<uint2 *>(to + p * KB * PX_M * 128) = make_uint2(w[0], w[E / 2 - 1]);
-          else
-            *reinterpret_cast<uint32_t *>(to + p * KB * PX_M * 128) = w[0];
-        }
-      }
-      fence_async_proxy();
-      __syncthreads();
-      const int reach = (int)(sm.best >> 32), source = (int)~(uint32_t)sm.best;
-      const int u_end = min(u1, (reach + PX_N - 1) / PX_N), n = max(0, u_end - u0);  // units with positions
-
-      if (warp >= PX_SOFT && warp < PX_SOFT + PX_LOAD) {
-        load_item<KIND, DH, SPLIT>(a, sm, tid - 32 * PX_SOFT, h, source, reach, u0, n, tiles, halves);
-      } else if (warp == PX_SOFT + PX_LOAD) {
-        if (lane == 0) multiply_item<KIND, DH, SPLIT>(sm, tmem, n, tiles, halves);
-        __syncwarp();
+      int n;
+      if (warp == PX_LOADER) {
+        n = load_item<KIND, DH, SPLIT>(a, maps, sm, x, h, u0, u1, tiles, halves, fixes);
       } else {
         const int lim = tid < rows ? min(x.prefix, length_of(a, first + tid / group)) : 0;
-        float m = -INFINITY, l = 0.f;
-        const bool ok = soften_item<KIND, DH, SPLIT>(sm, tmem + my_lanes, tid, warp * 32 < rows, lim, u0, n, tiles, &m, &l);
-        // the piece: eight dimensions of a row at a time, rows side by side
-        const int64_t slot = (int64_t)first * a.n_heads + h * rows + (int64_t)PX_M * blockIdx.x;
-        float *to = a.prefix + slot * DH + 8 * tid;
-        if (ok && n > 0) tc_fence_after();
+        stage_queries<KIND, DH, SPLIT>(a, sm, first, h, group, rows);
+        fence_async_proxy();
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const int reach = sm.reach;
+        n = max(0, min(u1, (reach + PX_N - 1) / PX_N) - u0);
+        if (warp == PX_ISSUER) {
+          multiply_item<KIND, DH, SPLIT>(sm, tmem, n, tiles, halves);
+        } else if (warp >= PX_SOFT) {
+          if constexpr (KIND == PG_E4M3) convert_item<KIND, DH, SPLIT>(sm, tid - 32 * PX_CONVERT, reach, u0, n, halves);
+        } else {
+          float m = -INFINITY, l = 0.f;
+          const bool ok = soften_item<KIND, DH, SPLIT>(sm, tmem + my_lanes, tid, warp * 32 < rows, lim, u0, n, tiles, &m, &l);
+          // the piece: eight dimensions of a row at a time, rows side by side
+          const int64_t slot = (int64_t)first * a.n_heads + h * rows + (int64_t)PX_M * blockIdx.x;
+          float *to = a.prefix + slot * DH + 8 * tid;
+          tc_fence_after();
+          if (warp * 32 < rows) {
 #pragma unroll 1
-        for (int c = 0; c < DH; c += 32) {
-          float o[32];
-          if (ok && n > 0) {
-            tmem_ld32(t_o + my_lanes + c, o);
-            tmem_wait_ld();
-          } else {
+            for (int c = 0; c < DH; c += 32) {
+              float o[32];
+              if (ok && n > 0) {
+                tmem_ld32(t_o + my_lanes + c, o);
+                tmem_wait_ld();
+              } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.f;
-          }
-          if (tid < rows) {
+                for (int e = 0; e < 32; ++e) o[e] = 0.f;
+              }
+              if (tid < rows) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              float4 *p = reinterpret_cast<float4 *>(to + (int64_t)(c + e) * rows);
-              p[0] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-              p[1] = make_float4(o[e + 4], o[e + 5], o[e + 6], o[e + 7]);
+                for (int e = 0; e < 32; e += 8) store8(to + (int64_t)(c + e) * rows, &o[e]);
+              }
             }
           }
+          // a wait that ran out shows as NaN in every result that it concerns
+          if (tid < rows) a.prefix_ml[slot + tid] = make_float2(ok ? m - P_BIAS : 0.f, ok ? l : __int_as_float(0x7fc00000));
+          tc_fence_before();
         }
-        // a wait that ran out shows as NaN in every result that it concerns
-        if (tid < rows) a.prefix_ml[slot + tid] = make_float2(ok ? m - P_BIAS : 0.f, ok ? l : __int_as_float(0x7fc00000));
-        tc_fence_before();
       }
       tiles += n;
       halves += 2 * n;
@@ -821,14 +905,63 @@ __global__ void __launch_bounds__(PX_THREADS, PxShape<KIND, DH, SPLIT>::BLOCKS) 
     }
   }
   let_next_begin();
-  if (warp == 0) tmem_dealloc(tmem, PX_TMEM);
+  if (warp == PX_ISSUER) tmem_dealloc(tmem, PX_TMEM);
+}
+
+// cuTensorMapEncodeTiled of the driver that is there.
+decltype(&cuTensorMapEncodeTiled) tensor_map_encode() {
+  static const auto encode = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(p);
+  }();
+  return encode;
+}
+
+// The pages as a tensor [page][head][position][dim] of any order of the first three, dimensions by rising stride. Rows of 16
+// bits come in boxes of 64 dims, in the layout of an MMA operand; codes as they are.
+bool make_map(CUtensorMap *map, int *order, const kie_pages &pg, bool v, int rows) {
+  const int64_t *st = v ? pg.v_stride : pg.k_stride;
+  const int es = paged_dtype_bytes(pg.dtype);
+  struct Dim {
+    int what;  // 0 position, 1 head, 2 page
+    cuuint64_t size, stride;
+  } d[3] = {{0, (cuuint64_t)pg.block_size, (cuuint64_t)st[2] * es},
+            {1, (cuuint64_t)pg.n_kv_heads, (cuuint64_t)st[1] * es},
+            {2, (cuuint64_t)pg.n_blocks, (cuuint64_t)st[0] * es}};
+  for (Dim &x : d)
+    if (x.size == 1) x.stride = (cuuint64_t)pg.head_dim * es;  // not stepped over, whatever it is
+  std::stable_sort(d, d + 3, [](const Dim &x, const Dim &y) { return x.stride < y.stride; });
+  cuuint64_t size[4] = {(cuuint64_t)pg.head_dim}, stride[3];
+  cuuint32_t box[4] = {pg.dtype == KIE_E4M3 ? (cuuint32_t)pg.head_dim : 64u}, step[4] = {1, 1, 1, 1};
+  *order = d[0].what | d[1].what << 2 | d[2].what << 4;
+  for (int i = 0; i < 3; ++i) {
+    size[i + 1] = d[i].size;
+    stride[i] = d[i].stride;
+    box[i + 1] = d[i].what == 0 ? rows : 1;
+  }
+  const auto encode = tensor_map_encode();
+  return encode && encode(map, pg.dtype == KIE_E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4,
+                          v ? pg.v : pg.k, size, stride, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          pg.dtype == KIE_E4M3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int KIND, int DH, bool SPLIT>
 cudaError_t launch(const PrefixArgs &a, int dev, int sms, cudaStream_t stream) {
+  const int bs = a.pages.block_size;
+  PrefixMaps maps;
+  maps.rows = bs % 64 == 0 ? 64 : bs % 32 == 0 ? 32 : 16;  // a box lies in one page
+  if (!make_map(&maps.k, &maps.order[0], a.pages, false, maps.rows) || !make_map(&maps.v, &maps.order[1], a.pages, true, maps.rows))
+    return cudaErrorInvalidPitchValue;
   static std::atomic<uint64_t> ready{0};  // devices whose limit of dynamic shared memory is raised
   using T = PxShape<KIND, DH, SPLIT>;
-  static_assert(sizeof(PxSmem<KIND, DH, SPLIT>) >= (KIE_PAGED_MAX_GROUPS + 4) * 4 + KIE_PAGED_MAX_GROUPS * 8, "the list's arrays");
+  using Sm = PxSmem<KIND, DH, SPLIT>;
+  static_assert(offsetof(Sm, live) >= (KIE_PAGED_MAX_GROUPS + 4) * 4 + KIE_PAGED_MAX_GROUPS * 8, "the list's arrays");
+  static_assert(T::BLOCKS == 1 || sizeof(PxSmem<KIND, DH, SPLIT>) <= 115712, "two blocks' shared memory");
   // no more than T::BLOCKS to an SM: a third one's TMEM would have to wait
   const int smem = (int)std::max<size_t>(sizeof(PxSmem<KIND, DH, SPLIT>), 80 * 1024);
   const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
@@ -838,7 +971,7 @@ cudaError_t launch(const PrefixArgs &a, int dev, int sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  return launch_after_previous(prefix_kernel<KIND, DH, SPLIT>, sms * T::BLOCKS, PX_THREADS, smem, stream, a);
+  return launch_after_previous(prefix_kernel<KIND, DH, SPLIT>, sms * T::BLOCKS, PX_THREADS, smem, stream, a, maps);
 }
 
 template <int DH>

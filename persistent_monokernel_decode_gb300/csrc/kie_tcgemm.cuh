@@ -52,20 +52,6 @@ __device__ __forceinline__ uint64_t tc_smem_desc(uint32_t saddr) {
 // Instruction descriptor of kind::f16: D fp32, A and B fp16, both K-major, N = TC_N, M = TC_M.
 constexpr uint32_t TC_IDESC = (1u << 4) | ((uint32_t)(TC_N >> 3) << 17) | ((uint32_t)(TC_M >> 4) << 24);
 
-// The warp's 32 TMEM lanes (lane field of taddr = 32 * (warp % 4)), 16 consecutive fp32 columns from taddr.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-      "[%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 struct TcArgs {
   const uint8_t *A;   // weights: [M tiles][KT][16 KB] canonical tiles (rows past M and columns past K are zero)
   const uint8_t *B;   // activations: [KT][32 KB] canonical tiles of the chunk's hi/lo parts

@@ -1,17 +1,37 @@
 // Log probabilities of tokens, entropies and the largest logits (kie_paged.cu holds the C entry).
+//
+// A row is read once, into registers: a block holds up to 64 KB of it, 64 elements of 16 bits (32 of fp32) to a thread, and
+// longer rows, or rows too few to fill the GPU, are split over a cluster of up to eight blocks that meet at the cluster's
+// barrier and pass their results through distributed shared memory. (Rows of more than 512 KB are read again for each
+// pass.) With the maximum of the row as the reference, s = sum exp(x - m) and t = sum exp(x - m) (x - m): ln p = x - m - ln s,
+// and the entropy is ln s - t / s, which stays accurate where x itself is large.
+//
+// The `top` largest: the maxima of groups of 16 threads give a bound that at least `top` elements reach, the `top`-th
+// largest of them; a row of random logits has about 1.6 times as many that do. Those, as keys of value and index, are
+// collected in any order and then put into their places by counting, for each, the keys above it, so results do not depend
+// on the order. Rows with more than LP_KEYS of them (equal logits, fewer tokens left than are asked for) look for one
+// maximum after the other instead.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
 #include "kie_device.cuh"
 #include "kie_paged.cuh"
 
 namespace kie {
 namespace {
 
-constexpr int LP_THREADS = 256, LP_WARPS = LP_THREADS / 32;
+namespace cg = cooperative_groups;
 
-__device__ __forceinline__ float logit(const kie_token_logprobs_args &a, int64_t at) {
-  if (a.dtype == KIE_F32) return static_cast<const float *>(a.logits)[at];
-  if (a.dtype == KIE_F16) return __half2float(static_cast<const __half *>(a.logits)[at]);
-  return __bfloat162float(static_cast<const __nv_bfloat16 *>(a.logits)[at]);
-}
+constexpr int LP_THREADS = 512, LP_WARPS = LP_THREADS / 32;
+constexpr int LP_VECS = 8;       // 16-byte pieces of a row that a thread holds
+constexpr int LP_GROUPS = LP_THREADS / 16;
+constexpr int LP_KEYS = 1024;
+constexpr int LP_CLUSTER = 8;
+constexpr float LP_LEAST = -1e4f;  // a distance from the maximum with a weight of 0 that may be multiplied with it
+constexpr float LOG2E = 1.4426950408889634f;
+
+using Key = unsigned long long;
 
 // A logit as an unsigned integer of the same order, NaN above +inf and -0 as 0.
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -23,63 +43,292 @@ __device__ __forceinline__ float value_of(uint32_t order) {
   return order == 0xffffffffu ? __uint_as_float(0x7fc00000u) : __uint_as_float(order & 0x80000000u ? order ^ 0x80000000u : ~order);
 }
 
-template <class T, class F>
-__device__ __forceinline__ T block_reduce(T v, const F &f) {
-  __shared__ T s_part[LP_WARPS];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = s_part[0];
-#pragma unroll
-  for (int w = 1; w < LP_WARPS; ++w) v = f(v, s_part[w]);
-  return v;
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-__global__ void __launch_bounds__(LP_THREADS) token_logprobs_kernel(const kie_token_logprobs_args a) {
+// 16 bytes of a row: N elements of type X.
+template <int X>
+struct Piece {
+  static constexpr int N = X == KIE_F32 ? 4 : 8, SIZE = 16 / N;
+  uint32_t w[4];
+  __device__ __forceinline__ float get(int e) const {
+    if (X == KIE_F32) return __uint_as_float(w[e & 3]);
+    if (X == KIE_F16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[(e >> 1) & 3]));
+      return e & 1 ? f.y : f.x;
+    }
+    return __uint_as_float(e & 1 ? w[(e >> 1) & 3] & 0xffff0000u : w[(e >> 1) & 3] << 16);
+  }
+  // Elements at .. at + N - 1 of a row of V, those outside as -inf. row + at is 16-byte aligned.
+  __device__ __forceinline__ void load(const uint8_t *row, int at, int V) {
+    const uint8_t *p = row + (int64_t)at * SIZE;
+    if (at >= 0 && at + N <= V) {
+      const uint4 x = __ldcs(reinterpret_cast<const uint4 *>(p));
+      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+      return;
+    }
+    constexpr uint32_t NONE = X == KIE_F32 ? 0xff800000u : X == KIE_F16 ? 0xfc00fc00u : 0xff80ff80u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = NONE;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      if (at + e < 0 || at + e >= V) continue;
+      if (X == KIE_F32)
+        w[e & 3] = *reinterpret_cast<const uint32_t *>(p + e * SIZE);
+      else
+        w[(e >> 1) & 3] = __byte_perm(w[(e >> 1) & 3], *reinterpret_cast<const uint16_t *>(p + e * SIZE), e & 1 ? 0x5410 : 0x3254);
+    }
+  }
+  // The largest element, NaN if there is one.
+  __device__ __forceinline__ float top() const {
+    if (X == KIE_F32) {
+      float m;
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(get(0)), "f"(get(1)));
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(get(2)));
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(get(3)));
+      return m;
+    }
+    if (X == KIE_F16) {
+      const __half2 *h = reinterpret_cast<const __half2 *>(w);
+      const __half2 m = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+      return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+    }
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(w);
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+    return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
+  }
+};
+
+struct LpSmem {
+  uint32_t group[LP_GROUPS];  // maxima
+  float2 sums[LP_WARPS];
+  uint32_t bound;
+  Key warp_best[LP_WARPS];
+  // of the cluster, in its first block:
+  float2 block_sums[LP_CLUSTER];
+  Key block_best[LP_CLUSTER];
+  int n_keys;
+  Key keys[LP_KEYS];
+};
+
+// One row to a cluster (or a block). held: whether every thread's part fits its registers; else `rounds` of them are loaded
+// in each pass.
+template <int X, bool CLUSTER>
+__global__ void __launch_bounds__(LP_THREADS, 2) token_logprobs_kernel(const kie_token_logprobs_args a, int per_block, int rounds) {
+  using P = Piece<X>;
   begin_after_previous();
-  const int64_t row = blockIdx.x, base = row * a.row_stride;
-  const int tid = threadIdx.x;
-  uint32_t top = 0;
-  for (int i = tid; i < a.vocab; i += LP_THREADS) top = max(top, order_of(logit(a, base + i)));
-  top = block_reduce(top, [](uint32_t x, uint32_t y) { return max(x, y); });
-  const float m = value_of(top);
-  const bool none = m == -INFINITY;
+  __shared__ LpSmem sm;
+  const cg::cluster_group cl = cg::this_cluster();
+  const int blocks = CLUSTER ? cl.num_blocks() : 1, block = CLUSTER ? cl.block_rank() : 0;
+  const int64_t row = CLUSTER ? blockIdx.x / blocks : blockIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, V = a.vocab, top = a.top;
+  const auto meet = [&] {
+    if (CLUSTER)
+      cl.sync();
+    else
+      __syncthreads();
+  };
+  LpSmem &first = CLUSTER ? *cl.map_shared_rank(&sm, 0) : sm;
+
+  const uint8_t *base = static_cast<const uint8_t *>(a.logits) + row * a.row_stride * P::SIZE;
+  const int skew = (int)((uintptr_t)base & 15) / P::SIZE;  // elements from the last 16-byte boundary to the row
+  // piece v of the row holds elements v N - skew ..; this block has [v0, v1)
+  const int pieces = (V + skew + P::N - 1) / P::N, v0 = min(block * per_block, pieces), v1 = min(v0 + per_block, pieces);
+  P x[LP_VECS];
+  const auto load = [&](int round) {
+#pragma unroll
+    for (int j = 0; j < LP_VECS; ++j) {
+      const int v = v0 + (round * LP_VECS + j) * LP_THREADS + tid;
+      x[j].load(base, v < v1 ? v * P::N - skew : V, V);
+    }
+  };
+  const auto index_of = [&](int round, int j, int e) { return (v0 + (round * LP_VECS + j) * LP_THREADS + tid) * P::N - skew + e; };
+  load(0);
+  float asked = 0.f;
+  int token = -1;
+  if (tid == 0 && block == 0 && a.logprob) {
+    token = a.tokens[row];
+    if ((unsigned)token < (unsigned)V) {
+      P y;
+      const int at = (token + skew) / P::N * P::N - skew;
+      y.load(base, at, V);
+#pragma unroll
+      for (int e = 0; e < P::N; ++e)
+        if (at + e == token) asked = y.get(e);
+    }
+  }
+  if (tid == 0) sm.n_keys = 0;
+
+  // ---- the maximum, and a bound that the `top` largest reach
+  uint32_t mine = 0;
+  for (int r = 0; r < rounds; ++r) {
+    if (r) load(r);
+#pragma unroll
+    for (int j = 0; j < LP_VECS; ++j) mine = max(mine, order_of(x[j].top()));
+  }
+  uint32_t group = mine;
+#pragma unroll
+  for (int o = 8; o; o >>= 1) group = max(group, __shfl_xor_sync(0xffffffffu, group, o));
+  if ((lane & 15) == 0) sm.group[tid / 16] = group;
+  meet();
+  uint32_t best = 0, all[LP_CLUSTER];  // lane i: group i of each block
+#pragma unroll
+  for (int b = 0; b < (CLUSTER ? LP_CLUSTER : 1); ++b) {
+    all[b] = 0;
+    if (b < blocks) all[b] = CLUSTER ? cl.map_shared_rank(&sm, b)->group[lane] : sm.group[lane];
+    best = max(best, all[b]);
+  }
+  best = __reduce_max_sync(0xffffffffu, best);
+  const float m = value_of(best), ref = m == -INFINITY ? 0.f : m;
+  if (top > 0 && warp == 0) {
+    uint32_t bound = 0;  // its upper 16 bits: of bf16 logits all there is
+    for (uint32_t bit = 0x80000000u; bit > 0x8000u; bit >>= 1) {
+      int n = 0;
+#pragma unroll
+      for (int b = 0; b < (CLUSTER ? LP_CLUSTER : 1); ++b) n += __popc(__ballot_sync(0xffffffffu, all[b] >= (bound | bit)));
+      if (n >= top) bound |= bit;
+    }
+    if (lane == 0) sm.bound = bound;
+  }
+  // ---- the sums
   float s = 0.f, t = 0.f;
-  for (int i = tid; i < a.vocab; i += LP_THREADS) {
-    const float d = logit(a, base + i) - m, w = expf(d);
-    s += w;
-    if (w != 0.f) t += w * d;
+  for (int r = 0; r < rounds; ++r) {
+    if (rounds > 1) load(r);
+#pragma unroll
+    for (int j = 0; j < LP_VECS; ++j)
+#pragma unroll
+      for (int e = 0; e < P::N; ++e) {
+        const float d = fmaxf(x[j].get(e) - ref, LP_LEAST), w = ex2(d * LOG2E);
+        s += w;
+        t = fmaf(w, d, t);
+      }
   }
-  s = block_reduce(s, [](float x, float y) { return x + y; });
-  t = block_reduce(t, [](float x, float y) { return x + y; });
-  const float ls = none ? 0.f : logf(s);
-  if (tid == 0) {
-    if (a.entropy) a.entropy[row] = none ? 0.f : ls - t / s;
-    if (a.logprob) {
-      const int token = a.tokens[row];
-      a.logprob[row] = (unsigned)token >= (unsigned)a.vocab ? 0.f : none ? -INFINITY : logit(a, base + token) - m - ls;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o), t += __shfl_xor_sync(0xffffffffu, t, o);
+  if (lane == 0) sm.sums[warp] = make_float2(s, t);
+  __syncthreads();
+  // ---- the elements that reach the bound
+  if (top > 0 && mine >= sm.bound) {
+    const float least = value_of(sm.bound);
+    bool room = true;
+    for (int r = 0; r < rounds && room; ++r) {
+      if (rounds > 1) load(r);
+#pragma unroll
+      for (int j = 0; j < LP_VECS; ++j)
+#pragma unroll
+        for (int e = 0; e < P::N; ++e) {
+          const float y = x[j].get(e);
+          if (y < least || !room) continue;
+          const int i = index_of(r, j, e);
+          if (i < 0 || i >= V) continue;
+          const int at = atomicAdd(&first.n_keys, 1);
+          room = at < LP_KEYS;
+          if (room) first.keys[at] = (Key)order_of(y) << 32 | (uint32_t)~i;
+        }
     }
   }
-  unsigned long long last = ~0ull;
-  for (int k = 0; k < a.top; ++k) {
-    unsigned long long best = 0;
-    for (int i = tid; i < a.vocab; i += LP_THREADS) {
-      const unsigned long long key = (unsigned long long)order_of(logit(a, base + i)) << 32 | (uint32_t)~i;
-      if (key < last && key > best) best = key;
-    }
-    last = block_reduce(best, [](unsigned long long x, unsigned long long y) { return max(x, y); });
+  if (warp == 0) {
+    float2 y = lane < LP_WARPS ? sm.sums[lane] : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int o = LP_WARPS / 2; o; o >>= 1)
+      y.x += __shfl_xor_sync(0xffffffffu, y.x, o), y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
+    if (lane == 0) first.block_sums[block] = y;
+  }
+  meet();
+  // ---- results, by the first block
+  const int n = first.n_keys;
+  const bool many = n > LP_KEYS;
+  float ls = 0.f;
+  if (block == 0) {
+    float ss = 0.f, tt = 0.f;
+    for (int b = 0; b < blocks; ++b) ss += sm.block_sums[b].x, tt += sm.block_sums[b].y;
+    // nothing left: ln p = -inf, entropy 0; NaN or +inf: NaN
+    const bool none = m == -INFINITY, bad = !(m < INFINITY);
+    ls = none ? INFINITY : bad ? __uint_as_float(0x7fc00000u) : logf(ss);
     if (tid == 0) {
-      a.top_ids[row * a.top + k] = (int)~(uint32_t)last;
-      a.top_logprobs[row * a.top + k] = none ? -INFINITY : value_of((uint32_t)(last >> 32)) - m - ls;
+      if (a.entropy) a.entropy[row] = none ? 0.f : ls - tt / ss;
+      if (a.logprob) a.logprob[row] = (unsigned)token >= (unsigned)V ? 0.f : asked - ref - ls;
+    }
+    if (!many)
+      for (int i = tid; i < n; i += LP_THREADS) {
+        const Key key = sm.keys[i];
+        int above = 0;
+        for (int k = 0; k < n; ++k) above += sm.keys[k] > key;
+        if (above >= top) continue;
+        a.top_ids[row * top + above] = (int)~(uint32_t)key;
+        a.top_logprobs[row * top + above] = value_of((uint32_t)(key >> 32)) - ref - ls;
+      }
+  }
+  if (many) {  // the same in every block
+    Key last = ~0ull;
+    for (int k = 0; k < top; ++k) {
+      Key next = 0;
+      for (int r = 0; r < rounds; ++r) {
+        if (rounds > 1) load(r);
+#pragma unroll
+        for (int j = 0; j < LP_VECS; ++j)
+#pragma unroll
+          for (int e = 0; e < P::N; ++e) {
+            const int i = index_of(r, j, e);
+            const Key key = (Key)order_of(x[j].get(e)) << 32 | (uint32_t)~i;
+            if (key < last && key > next && i >= 0 && i < V) next = key;
+          }
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) next = max(next, __shfl_xor_sync(0xffffffffu, next, o));
+      if (lane == 0) sm.warp_best[warp] = next;
+      __syncthreads();
+      if (tid == 0) {
+        for (int w = 0; w < LP_WARPS; ++w) next = max(next, sm.warp_best[w]);
+        first.block_best[block] = next;
+      }
+      meet();
+      last = 0;
+      for (int b = 0; b < blocks; ++b) last = max(last, first.block_best[b]);
+      if (block == 0 && tid == 0) {
+        a.top_ids[row * top + k] = (int)~(uint32_t)last;
+        a.top_logprobs[row * top + k] = value_of((uint32_t)(last >> 32)) - ref - ls;
+      }
+      meet();  // read before the next round writes
     }
   }
+  if (CLUSTER) cl.sync();  // the first block's memory is read until here
+}
+
+template <int X>
+cudaError_t launch(const kie_token_logprobs_args &a, int sms, cudaStream_t stream) {
+  using P = Piece<X>;
+  const int pieces = a.vocab / P::N + 2, full = LP_VECS * LP_THREADS;  // of a row at most; of a block's registers
+  // A block to a row, or as many as its registers need. Rows that leave SMs idle are split further, as long as every thread of a
+  // block has a piece.
+  int blocks = 1;
+  while (blocks < LP_CLUSTER && (blocks * full < pieces || ((int64_t)a.n_rows * blocks * 2 <= sms && pieces >= 2 * blocks * LP_THREADS)))
+    blocks *= 2;
+  const int per_block = (pieces + blocks - 1) / blocks, rounds = (per_block + full - 1) / full;
+  if ((int64_t)a.n_rows * blocks > INT_MAX) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.n_rows * blocks));
+  cfg.blockDim = dim3(LP_THREADS);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = blocks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = blocks > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, blocks > 1 ? token_logprobs_kernel<X, true> : token_logprobs_kernel<X, false>, a, per_block, rounds);
 }
 
 }  // namespace
 }  // namespace kie
 
-cudaError_t kie_launch_token_logprobs(const kie_token_logprobs_args &a, int, cudaStream_t stream) {
-  return kie::launch_after_previous(kie::token_logprobs_kernel, a.n_rows, kie::LP_THREADS, 0, stream, a);
+cudaError_t kie_launch_token_logprobs(const kie_token_logprobs_args &a, int sms, cudaStream_t stream) {
+  return a.dtype == KIE_F32   ? kie::launch<KIE_F32>(a, sms, stream)
+         : a.dtype == KIE_F16 ? kie::launch<KIE_F16>(a, sms, stream)
+                              : kie::launch<KIE_BF16>(a, sms, stream);
 }

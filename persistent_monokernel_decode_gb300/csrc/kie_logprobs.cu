@@ -1,11 +1,12 @@
 // Log probabilities of tokens, entropies and the largest logits (kie_paged.cu holds the C entry).
 //
-// A row is read once, into shared memory: a block holds up to 64 KB of it, brought by bulk copies, and longer rows, or rows
-// too few to fill the GPU, are split over a cluster of up to eight blocks that meet at the cluster's barrier and pass their
-// results through distributed shared memory. (Rows of more than 512 KB are read again for each pass.) Passes over the row
-// are short loops: held in registers and unrolled, as it was first, the row took 22 instructions an element and most of the
-// time to fetch them. With the maximum of the row as the reference, s = sum exp(x - m) and t = sum exp(x - m) (x - m):
-// ln p = x - m - ln s, and the entropy is ln s - t / s, which stays accurate where x itself is large.
+// A row is streamed once. Each thread keeps a reference r within a few of the maximum of what it has seen, s = sum exp(x - r)
+// and t = sum exp(x - r) (x - r), and the threads' sums are joined at the row's maximum m: ln p = x - m - ln s, and the
+// entropy is ln s - t / s, which stays accurate where x itself is large. Rows too few to fill the GPU are split over a
+// cluster of up to eight blocks, which meet at the cluster's barrier and pass their results through distributed shared
+// memory. Bound by HBM, and nearly by instructions (6 an element of 16 bits, two fp32 operations to an instruction).
+// Holding the row, so that the maximum is known before the sums, took more: in registers, unrolled, 22 instructions an
+// element and 280 us for 8,191 rows of 32,000 bf16 logits; in shared memory 13 and 159 us, three rows to an SM being too few.
 //
 // The `top` largest: the maxima of groups of threads give a bound that at least `top` elements reach, the `top`-th
 // largest of them; a row of random logits has about 1.6 times as many that do. Those, as keys of value and index, are
@@ -14,10 +15,6 @@
 // maximum after the other instead.
 #include <cooperative_groups.h>
 
-#include <limits.h>
-
-#include <algorithm>
-#include <atomic>
 
 #include "kie_device.cuh"
 #include "kie_paged.cuh"
@@ -27,13 +24,13 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-#ifndef LPT
-#define LPT 256
-#endif
-constexpr int LP_THREADS = LPT, LP_WARPS = LP_THREADS / 32;
-constexpr int LP_PIECES = 4096;  // 16-byte pieces of a row that a block holds: three blocks to an SM
-constexpr int LP_GROUPS = 32, LP_GROUP = LP_THREADS / LP_GROUPS;  // of threads
-constexpr int LP_KEYS = 512;
+// Threads of a block: small ones where there are rows enough, so that the waits at the end of a row concern few warps at a
+// time (8,191 rows of 32,000 bf16 logits, 20 largest: ??? us with 128 threads, ??? with 256).
+constexpr int LP_FEW = 256, LP_MANY = 128;
+constexpr int LP_AHEAD = 4;  // 16-byte pieces of a row that a thread has on their way
+constexpr float LP_STEP = 4.f;  // the reference moves when the maximum passes it by more
+constexpr int LP_GROUPS = 64;  // of threads
+constexpr int LP_KEYS = 512, LP_LIST = 1024;
 constexpr int LP_CLUSTER = 8;
 constexpr float LP_LEAST = -1e4f;  // a distance from the maximum with a weight of 0 that may be multiplied with it
 constexpr float LOG2E = 1.4426950408889634f;
@@ -60,6 +57,7 @@ __device__ __forceinline__ float ex2(float x) {
 template <int X>
 struct Piece {
   static constexpr int N = X == KIE_F32 ? 4 : 8, SIZE = 16 / N;
+  static constexpr uint32_t NONE = X == KIE_F32 ? 0xff800000u : X == KIE_F16 ? 0xfc00fc00u : 0xff80ff80u;  // -inf, or two
   uint32_t w[4];
   __device__ __forceinline__ float get(int e) const {
     if (X == KIE_F32) return __uint_as_float(w[e & 3]);
@@ -70,10 +68,8 @@ struct Piece {
     return __uint_as_float(e & 1 ? w[(e >> 1) & 3] & 0xffff0000u : w[(e >> 1) & 3] << 16);
   }
   // Elements at .. at + N - 1 of a row of V one by one, those outside it as -inf.
-  __device__ void gather(const uint8_t *row, int at, int V) {
-    constexpr uint32_t NONE = X == KIE_F32 ? 0xff800000u : X == KIE_F16 ? 0xfc00fc00u : 0xff80ff80u;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = NONE;
+  static __device__ __noinline__ uint4 gather(const uint8_t *row, int at, int V) {
+    uint32_t w[4] = {NONE, NONE, NONE, NONE};
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       if (at + e < 0 || at + e >= V) continue;
@@ -83,6 +79,7 @@ struct Piece {
       else
         w[(e >> 1) & 3] = __byte_perm(w[(e >> 1) & 3], *reinterpret_cast<const uint16_t *>(p), e & 1 ? 0x5410 : 0x3254);
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
   // The elements, two by two, none below a finite value whose weight is 0 (against a maximum above -10^37).
   __device__ __forceinline__ float2 pair(int k) const {
@@ -92,13 +89,30 @@ struct Piece {
     const uint32_t u = *reinterpret_cast<const uint32_t *>(&b);
     return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
   }
+  // This one's elements or y's, whichever is larger at each place, NaN if one is.
+  __device__ __forceinline__ void raise(const Piece &y) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (X == KIE_F32) {
+        float f = __uint_as_float(w[k]);
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(f) : "f"(__uint_as_float(y.w[k])));
+        w[k] = __float_as_uint(f);
+      } else if (X == KIE_F16) {
+        const __half2 h = __hmax2_nan(*reinterpret_cast<const __half2 *>(&w[k]), *reinterpret_cast<const __half2 *>(&y.w[k]));
+        w[k] = *reinterpret_cast<const uint32_t *>(&h);
+      } else {
+        const __nv_bfloat162 h =
+            __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&w[k]), *reinterpret_cast<const __nv_bfloat162 *>(&y.w[k]));
+        w[k] = *reinterpret_cast<const uint32_t *>(&h);
+      }
+    }
+  }
   // The largest element, NaN if there is one.
-  __device__ __forceinline__ float top() const {
+  __device__ __forceinline__ float most() const {
     if (X == KIE_F32) {
-      float m;
-      asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(get(0)), "f"(get(1)));
-      asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(get(2)));
-      asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(get(3)));
+      float m = get(0);
+#pragma unroll
+      for (int e = 1; e < 4; ++e) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(get(e)));
       return m;
     }
     if (X == KIE_F16) {
@@ -140,12 +154,12 @@ __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigne
 }
 
 struct LpSmem {
-  uint64_t full;
-  int failed;
-  uint32_t group[LP_GROUPS];  // maxima
-  float2 sums[LP_WARPS];
+  alignas(16) uint32_t group[LP_GROUPS];  // maxima
+  uint32_t list[LP_LIST];     // rounds of threads that have elements which reach the bound, or may: thread | round << 8
+  int n_list;
+  float2 sums[LP_FEW / 32];
   uint32_t bound;
-  Key warp_best[LP_WARPS];
+  Key warp_best[LP_FEW / 32];
   // of the cluster, in its first block:
   float2 block_sums[LP_CLUSTER];
   Key block_best[LP_CLUSTER];
@@ -153,15 +167,12 @@ struct LpSmem {
   Key keys[LP_KEYS];
 };
 
-constexpr unsigned long long LP_TIMEOUT_NS = 2000000000ull;
-
-// One row to a cluster (or a block), loaded in `rounds` parts of LP_PIECES pieces: one, unless the row is very long.
+// One row to a cluster (or a block), per_block pieces of it to each block.
 template <int X, bool CLUSTER>
-__global__ void __launch_bounds__(LP_THREADS, 3) token_logprobs_kernel(const kie_token_logprobs_args a, int per_block, int rounds) {
+__global__ void __launch_bounds__(CLUSTER ? LP_FEW : LP_MANY, CLUSTER ? 4 : 10) token_logprobs_kernel(const kie_token_logprobs_args a, int per_block) {
   using P = Piece<X>;
-  extern __shared__ __align__(128) uint8_t lp_raw[];
+  constexpr int LP_THREADS = CLUSTER ? LP_FEW : LP_MANY, LP_WARPS = LP_THREADS / 32, LP_GROUP = LP_THREADS / LP_GROUPS;
   __shared__ LpSmem sm;
-  P *const held = reinterpret_cast<P *>(lp_raw);
   const cg::cluster_group cl = cg::this_cluster();
   const int blocks = CLUSTER ? cl.num_blocks() : 1, block = CLUSTER ? cl.block_rank() : 0;
   const int64_t row = CLUSTER ? blockIdx.x / blocks : blockIdx.x;
@@ -179,44 +190,23 @@ __global__ void __launch_bounds__(LP_THREADS, 3) token_logprobs_kernel(const kie
   // piece v of the row holds elements v N - skew ..; this block has [v0, v1); pieces [whole0, whole1) lie inside the row
   const int pieces = (V + skew + P::N - 1) / P::N, v0 = min(block * per_block, pieces), v1 = min(v0 + per_block, pieces);
   const int whole0 = skew ? 1 : 0, whole1 = (V + skew) / P::N;
-  if (tid == 0) {
-    mbar_init(&sm.full, 1);
-    fence_barrier_init();
-    sm.n_keys = 0;
-    sm.failed = 0;
-  }
-  begin_after_previous();
-  __syncthreads();
-  int loads = 0, held0 = 0, n_held = 0;  // pieces held0 .. of the row are there
-  const auto load = [&](int round) {
-    if (loads) {  // everybody is done with the last part
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncthreads();
-    }
-    held0 = v0 + round * LP_PIECES;
-    n_held = max(0, min(v1 - held0, LP_PIECES));
-    const int b = max(held0, whole0), e = min(held0 + n_held, whole1), bytes = max(0, e - b) * 16;
-    if (tid == 0) {
-      mbar_arrive_expect_tx(&sm.full, bytes);
-      for (int at = 0; at < bytes; at += 16384)
-        bulk_g2s(lp_raw + (b - held0) * 16 + at, base + ((int64_t)b * P::N - skew) * P::SIZE + at, min(16384, bytes - at), &sm.full,
-                 l2_evict_first_policy());
-    }
-    if (held0 == 0 && whole0 == 1 && n_held > 0 && tid == 32) held[0].gather(base, -skew, V);
-    if (whole1 < pieces && whole1 >= max(held0, whole0) && whole1 < held0 + n_held && tid == 64)
-      held[whole1 - held0].gather(base, whole1 * P::N - skew, V);
-    if (!mbar_try_wait(&sm.full, loads & 1)) {
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(&sm.full, loads & 1))
-        if (globaltimer() - t0 > LP_TIMEOUT_NS) {
-          sm.failed = 1;
-          break;
-        }
-    }
-    ++loads;
-    if (whole0 == 1 || whole1 < pieces) __syncthreads();  // the pieces put together by hand
+  const uint4 *const from = reinterpret_cast<const uint4 *>(base - skew * P::SIZE);
+  // Thread i takes every LP_THREADS-th of the places [u0 + i, u1): the pieces from the first whole one on, and behind them
+  // the row's first piece where it is none.
+  const int u0 = max(v0, whole0), u1 = v1 + (v0 == 0 && whole0 && v1 > 0 ? 1 : 0);
+  const auto piece_of = [&](int u) { return u == v1 ? 0 : u; };
+  const auto fetch = [&](int u) {
+    uint4 w = make_uint4(P::NONE, P::NONE, P::NONE, P::NONE);
+    if (u < min(v1, whole1))
+      w = __ldcg(from + u);
+    else if (u < u1)
+      w = P::gather(base, piece_of(u) * P::N - skew, V);
+    P x;
+    x.w[0] = w.x, x.w[1] = w.y, x.w[2] = w.z, x.w[3] = w.w;
+    return x;
   };
-  load(0);
+  if (tid == 0) sm.n_keys = sm.n_list = 0;
+  begin_after_previous();
   float asked = 0.f;
   int token = -1;
   if (tid == 0 && block == 0 && a.logprob) {
@@ -229,99 +219,201 @@ __global__ void __launch_bounds__(LP_THREADS, 3) token_logprobs_kernel(const kie
     }
   }
 
-  // ---- the maximum, and a bound that the `top` largest reach
-  uint32_t mine = 0;
-  for (int r = 0; r < rounds; ++r) {
-    if (r) load(r);
-#pragma unroll 4
-    for (int i = tid; i < n_held; i += LP_THREADS) mine = max(mine, order_of(held[i].top()));
+  // ---- the thread's pieces: their maximum and sums
+  float ref = 0.f, most = -INFINITY, next_most = -INFINITY;  // the largest maximum of a round, and the second
+  int most_round = 0;
+  bool any = false, far = false;  // there is a reference; it, or an element, is too large for differences in fp32
+  unsigned long long s2[2] = {0, 0}, t2[2] = {0, 0}, minus = 0;
+  const unsigned long long unit = two(LOG2E, LOG2E);
+  const auto take = [&](const P(&x)[LP_AHEAD], int round) {
+    P up = x[0];
+#pragma unroll
+    for (int k = 1; k < LP_AHEAD; ++k) up.raise(x[k]);
+    const float high = up.most();
+    if (!(high <= most)) {
+      next_most = most;
+      most = high;  // a NaN stays: whatever follows counts as more
+      most_round = round;
+    } else if (high > next_most) {
+      next_most = high;
+    }
+    if (!(high <= ref + LP_STEP) || !any) {  // seldom but for the first time
+      far = far || (!(fabsf(high) < 1e37f) && high != -INFINITY);
+      if (high != -INFINITY && !far) {
+        const float by = any ? ref - high : 0.f, f = ex2(by * LOG2E);  // t + s (old - new reference), s, both times f
+        const unsigned long long f2 = two(f, f), by2 = two(by, by);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          t2[k] = mul2(fma2(s2[k], by2, t2[k]), f2);
+          s2[k] = mul2(s2[k], f2);
+        }
+        ref = high;
+        minus = two(-ref, -ref);
+        any = true;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < LP_AHEAD; ++k)
+#pragma unroll
+      for (int e = 0; e < P::N / 2; ++e) {
+        const float2 f = x[k].pair(e);
+        const unsigned long long d = add2(two(f.x, f.y), minus);
+        const float2 g = both(mul2(d, unit));
+        const unsigned long long w = two(ex2(g.x), ex2(g.y));
+        s2[e & 1] = add2(s2[e & 1], w);
+        t2[e & 1] = fma2(w, d, t2[e & 1]);
+      }
+  };
+  const int rounds = max(0, min(v1, whole1) - u0) / (LP_AHEAD * LP_THREADS);  // without an end in them
+  {
+    const uint4 *at = from + u0 + tid;
+#pragma unroll 1
+    for (int r = 0; r < rounds; ++r, at += LP_AHEAD * LP_THREADS) {
+      P x[LP_AHEAD];
+#pragma unroll
+      for (int k = 0; k < LP_AHEAD; ++k) {
+        const uint4 w = __ldcg(at + k * LP_THREADS);
+        x[k].w[0] = w.x, x[k].w[1] = w.y, x[k].w[2] = w.z, x[k].w[3] = w.w;
+      }
+      take(x, r);
+    }
   }
+  const int all_rounds = (max(0, u1 - u0) + LP_AHEAD * LP_THREADS - 1) / (LP_AHEAD * LP_THREADS);
+#pragma unroll 1
+  for (int r = rounds; r < all_rounds; ++r) {
+    P x[LP_AHEAD];
+#pragma unroll
+    for (int k = 0; k < LP_AHEAD; ++k) x[k] = fetch(u0 + tid + (r * LP_AHEAD + k) * LP_THREADS);
+    take(x, r);
+  }
+  const uint32_t mine = order_of(most);
+  // ---- the row's maximum, and a bound that the `top` largest reach
   uint32_t group = mine;
 #pragma unroll
   for (int o = LP_GROUP / 2; o; o >>= 1) group = max(group, __shfl_xor_sync(0xffffffffu, group, o));
   if (tid % LP_GROUP == 0) sm.group[tid / LP_GROUP] = group;
   meet();
-  uint32_t best = 0, all[CLUSTER ? LP_CLUSTER : 1];  // lane i: group i of each block
+  uint32_t best = 0;
+  if constexpr (CLUSTER) {
+    uint32_t all[LP_CLUSTER], y[LP_CLUSTER];  // lane i: groups i and i + 32 of each block
 #pragma unroll
-  for (int b = 0; b < (CLUSTER ? LP_CLUSTER : 1); ++b) {
-    all[b] = 0;
-    if (b < blocks) all[b] = CLUSTER ? cl.map_shared_rank(&sm, b)->group[lane] : sm.group[lane];
-    best = max(best, all[b]);
+    for (int b = 0; b < LP_CLUSTER; ++b) {  // no condition: the loads are on their way together
+      const uint32_t *g = cl.map_shared_rank(&sm, min(b, blocks - 1))->group;
+      all[b] = g[lane], y[b] = g[lane + 32];
+    }
+#pragma unroll
+    for (int b = 0; b < LP_CLUSTER; ++b) {
+      all[b] = b < blocks ? max(all[b], y[b]) : 0u;
+      best = max(best, all[b]);
+    }
+    if (top > 0 && warp == 0) {
+      uint32_t bound = 0;  // its upper 16 bits: of bf16 logits all there is
+#pragma unroll 1
+      for (uint32_t bit = 0x80000000u; bit > 0x8000u; bit >>= 1) {
+        int n = 0;
+#pragma unroll
+        for (int b = 0; b < LP_CLUSTER; ++b) n += __popc(__ballot_sync(0xffffffffu, all[b] >= (bound | bit)));
+        if (n >= top) bound |= bit;
+      }
+      if (lane == 0) sm.bound = bound;
+    }
+  } else {
+    best = max(sm.group[lane], sm.group[lane + 32]);
+    if (top > 0) {  // the group with top - 1 others above it
+      constexpr int PARTS = LP_THREADS / LP_GROUPS;
+      const int g = tid / PARTS, part = tid % PARTS;
+      const uint32_t own = sm.group[g];
+      int above = 0;
+#pragma unroll 4
+      for (int k = 0; k < LP_GROUPS / PARTS; k += 4) {
+        const int at = part * (LP_GROUPS / PARTS) + k;
+        const uint4 y = *reinterpret_cast<const uint4 *>(&sm.group[at]);
+        above += (y.x > own || (y.x == own && at < g)) + (y.y > own || (y.y == own && at + 1 < g)) +
+                 (y.z > own || (y.z == own && at + 2 < g)) + (y.w > own || (y.w == own && at + 3 < g));
+      }
+#pragma unroll
+      for (int o = 1; o < PARTS; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+      if (above == top - 1) sm.bound = own;
+    }
   }
   best = __reduce_max_sync(0xffffffffu, best);
-  const float m = value_of(best), ref = m == -INFINITY ? 0.f : m;
-  if (top > 0 && warp == 0) {
-    uint32_t bound = 0;  // its upper 16 bits: of bf16 logits all there is
+  const float m = value_of(best), base_m = m == -INFINITY ? 0.f : m;
+  // ---- the sums at the row's maximum
+  float s = 0.f, t = 0.f;
+  if (!(fabsf(base_m) < 1e37f) || far) {  // differences may leave the range, or there is an infinity or NaN: once more
 #pragma unroll 1
-    for (uint32_t bit = 0x80000000u; bit > 0x8000u; bit >>= 1) {
-      int n = 0;
+    for (int u = u0 + tid; u < u1; u += LP_THREADS) {
+      const P x = fetch(u);
 #pragma unroll
-      for (int b = 0; b < (CLUSTER ? LP_CLUSTER : 1); ++b) n += __popc(__ballot_sync(0xffffffffu, all[b] >= (bound | bit)));
-      if (n >= top) bound |= bit;
-    }
-    if (lane == 0) sm.bound = bound;
-  }
-  // ---- the sums
-  float s, t;
-  if (fabsf(ref) < 1e37f) {
-    unsigned long long s2[2] = {0, 0}, t2[2] = {0, 0};
-    const unsigned long long minus = two(-ref, -ref), unit = two(LOG2E, LOG2E);
-    for (int r = 0; r < rounds; ++r) {
-      if (rounds > 1) load(r);
-#pragma unroll 2
-      for (int i = tid; i < n_held; i += LP_THREADS) {
-        const P x = held[i];
-#pragma unroll
-        for (int k = 0; k < P::N / 2; ++k) {
-          const float2 f = x.pair(k);
-          const unsigned long long d = add2(two(f.x, f.y), minus);
-          const float2 g = both(mul2(d, unit));
-          const unsigned long long w = two(ex2(g.x), ex2(g.y));
-          s2[k & 1] = add2(s2[k & 1], w);
-          t2[k & 1] = fma2(w, d, t2[k & 1]);
-        }
+      for (int e = 0; e < P::N; ++e) {
+        const float d = fmaxf(x.get(e) - base_m, LP_LEAST), w = ex2(d * LOG2E);
+        s += w;
+        t = fmaf(w, d, t);
       }
     }
+  } else if (any) {
     const float2 f = both(add2(s2[0], s2[1])), g = both(add2(t2[0], t2[1]));
-    s = f.x + f.y, t = g.x + g.y;
-  } else {  // differences may leave the range, or there is an infinity or NaN
-    s = t = 0.f;
-    for (int r = 0; r < rounds; ++r) {
-      if (rounds > 1) load(r);
-#pragma unroll 1
-      for (int i = tid; i < n_held; i += LP_THREADS) {
-        const P x = held[i];
-#pragma unroll
-        for (int e = 0; e < P::N; ++e) {
-          const float d = fmaxf(x.get(e) - ref, LP_LEAST), w = ex2(d * LOG2E);
-          s += w;
-          t = fmaf(w, d, t);
-        }
-      }
-    }
+    const float by = ref - base_m, factor = ex2(by * LOG2E);
+    s = f.x + f.y;
+    t = fmaf(s, fmaxf(by, LP_LEAST), g.x + g.y) * factor;
+    s *= factor;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o), t += __shfl_xor_sync(0xffffffffu, t, o);
   if (lane == 0) sm.sums[warp] = make_float2(s, t);
   __syncthreads();
-  // ---- the elements that reach the bound
-  const uint32_t bound = sm.bound;
-  const float least = value_of(bound);
-  for (int r = 0; top > 0 && r < rounds; ++r) {
-    if (rounds > 1) load(r);
-    bool room = mine >= bound;
+  // ---- the elements that reach the bound: the rounds that have some are read again, half a piece to a lane, four rounds of
+  // a thread to a warp
+  if (top > 0) {
+    const uint32_t bound = sm.bound;
+    const float least = value_of(bound);
+    if (mine >= bound) {
+      const bool more = !(next_most < least);  // which rounds is not known
+      for (int r = more ? 0 : most_round; r < (more ? all_rounds : most_round + 1); ++r) {
+        const int at = atomicAdd(&sm.n_list, 1);
+        if (at >= LP_LIST) break;
+        sm.list[at] = tid | r << 8;
+      }
+    }
+    __syncthreads();
+    const int n_list = sm.n_list;
+    static_assert(LP_AHEAD * 2 * 4 == 32 && LP_THREADS <= 256, "a round is eight lanes' work; a thread's number takes 8 bits");
+    if (n_list > LP_LIST) {
+      if (tid == 0) atomicAdd(&first.n_keys, LP_KEYS + 1);
+    } else {
 #pragma unroll 1
-    for (int i = tid; i < n_held && room; i += LP_THREADS) {
-      const P x = held[i];
-      if (x.top() < least) continue;
+      for (int e = warp * 4 + (lane >> 3); e < n_list; e += 8 * LP_WARPS) {
+        P x[2];
+        int u[2];
 #pragma unroll
-      for (int e = 0; e < P::N; ++e) {
-        const float y = x.get(e);
-        const int id = (held0 + i) * P::N - skew + e;
-        if (y < least || id < 0 || id >= V || !room) continue;
-        const int at = atomicAdd(&first.n_keys, 1);
-        room = at < LP_KEYS;
-        if (room) first.keys[at] = (Key)order_of(y) << 32 | (uint32_t)~id;
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t who = sm.list[min(e + i * 4 * LP_WARPS, n_list - 1)];
+          u[i] = e + i * 4 * LP_WARPS < n_list ? u0 + ((who >> 8) * LP_AHEAD + (lane >> 1 & 3)) * LP_THREADS + (who & 255u) : u1;
+          x[i] = fetch(u[i]);
+        }
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          P h = x[0];
+          const int v = u[0];
+          x[0] = x[1], u[0] = u[1];
+          if (lane & 1) h.w[0] = h.w[2], h.w[1] = h.w[3];
+          h.w[2] = h.w[0], h.w[3] = h.w[1];
+          if (h.most() < least || v >= u1) continue;
+          const int id0 = piece_of(v) * P::N - skew + (lane & 1) * (P::N / 2);
+#pragma unroll 1
+          for (int k = 0; k < P::N / 2; ++k) {
+            const float y = h.get(0);
+            const int id = id0 + k;
+            if (P::SIZE == 4)  // the next one
+              h.w[0] = h.w[1];
+            else
+              h.w[0] = h.w[0] >> 16 | h.w[1] << 16, h.w[1] >>= 16;
+            if (y < least || id < 0 || id >= V) continue;
+            const int at = atomicAdd(&first.n_keys, 1);
+            if (at >= LP_KEYS) break;
+            first.keys[at] = (Key)order_of(y) << 32 | (uint32_t)~id;
+          }
+        }
       }
     }
   }
@@ -330,8 +422,7 @@ __global__ void __launch_bounds__(LP_THREADS, 3) token_logprobs_kernel(const kie
 #pragma unroll
     for (int o = LP_WARPS / 2; o; o >>= 1)
       y.x += __shfl_xor_sync(0xffffffffu, y.x, o), y.y += __shfl_xor_sync(0xffffffffu, y.y, o);
-    // a copy that did not come shows as NaN
-    if (lane == 0) first.block_sums[block] = sm.failed ? make_float2(__uint_as_float(0x7fc00000u), 0.f) : y;
+    if (lane == 0) first.block_sums[block] = y;
   }
   meet();
   // ---- results, by the first block
@@ -346,34 +437,30 @@ __global__ void __launch_bounds__(LP_THREADS, 3) token_logprobs_kernel(const kie
     ls = none ? INFINITY : bad ? __uint_as_float(0x7fc00000u) : logf(ss);
     if (tid == 0) {
       if (a.entropy) a.entropy[row] = none ? 0.f : ls - tt / ss;
-      if (a.logprob) a.logprob[row] = (unsigned)token >= (unsigned)V ? 0.f : asked - ref - ls;
+      if (a.logprob) a.logprob[row] = (unsigned)token >= (unsigned)V ? 0.f : asked - base_m - ls;
     }
     if (!many)
-      for (int i = tid; i < n; i += LP_THREADS) {
+      for (int i = warp; i < n; i += LP_WARPS) {  // the place of a key: as many are above it
         const Key key = sm.keys[i];
         int above = 0;
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) above += sm.keys[k] > key;
-        if (above >= top) continue;
+        for (int k = 0; k < n; k += 32) above += __popc(__ballot_sync(0xffffffffu, k + lane < n && sm.keys[k + lane] > key));
+        if (above >= top || lane) continue;
         a.top_ids[row * top + above] = (int)~(uint32_t)key;
-        a.top_logprobs[row * top + above] = value_of((uint32_t)(key >> 32)) - ref - ls;
+        a.top_logprobs[row * top + above] = value_of((uint32_t)(key >> 32)) - base_m - ls;
       }
   }
   if (many) {  // the same in every block
     Key last = ~0ull;
     for (int k = 0; k < top; ++k) {
       Key next = 0;
-      for (int r = 0; r < rounds; ++r) {
-        if (rounds > 1) load(r);
 #pragma unroll 1
-        for (int i = tid; i < n_held; i += LP_THREADS) {
-          const P x = held[i];
+      for (int u = u0 + tid; u < u1; u += LP_THREADS) {
+        const P x = fetch(u);
 #pragma unroll
-          for (int e = 0; e < P::N; ++e) {
-            const int id = (held0 + i) * P::N - skew + e;
-            const Key key = (Key)order_of(x.get(e)) << 32 | (uint32_t)~id;
-            if (key < last && key > next && id >= 0 && id < V) next = key;
-          }
+        for (int e = 0; e < P::N; ++e) {
+          const int id = piece_of(u) * P::N - skew + e;
+          const Key key = (Key)order_of(x.get(e)) << 32 | (uint32_t)~id;
+          if (key < last && key > next && id >= 0 && id < V) next = key;
         }
       }
 #pragma unroll
@@ -389,7 +476,7 @@ __global__ void __launch_bounds__(LP_THREADS, 3) token_logprobs_kernel(const kie
       for (int b = 0; b < blocks; ++b) last = max(last, first.block_best[b]);
       if (block == 0 && tid == 0) {
         a.top_ids[row * top + k] = (int)~(uint32_t)last;
-        a.top_logprobs[row * top + k] = value_of((uint32_t)(last >> 32)) - ref - ls;
+        a.top_logprobs[row * top + k] = value_of((uint32_t)(last >> 32)) - base_m - ls;
       }
       meet();  // read before the next round writes
     }
@@ -398,29 +485,17 @@ __global__ void __launch_bounds__(LP_THREADS, 3) token_logprobs_kernel(const kie
 }
 
 template <int X>
-cudaError_t launch(const kie_token_logprobs_args &a, int dev, int sms, cudaStream_t stream) {
+cudaError_t launch(const kie_token_logprobs_args &a, int sms, cudaStream_t stream) {
   using P = Piece<X>;
   const int pieces = a.vocab / P::N + 2;  // of a row at most
-  // A block to a row, or as many as it takes to hold it. Rows that leave SMs idle are split further, as long as every thread
-  // of a block has a piece.
+  // Rows that leave SMs idle are split, as long as every thread of a block has a piece.
   int blocks = 1;
-  while (blocks < LP_CLUSTER &&
-         (blocks * LP_PIECES < pieces || ((int64_t)a.n_rows * blocks * 2 <= sms && pieces >= 2 * blocks * LP_THREADS)))
-    blocks *= 2;
-  const int per_block = (pieces + blocks - 1) / blocks, rounds = (per_block + LP_PIECES - 1) / LP_PIECES;
-  if ((int64_t)a.n_rows * blocks > INT_MAX) return cudaErrorInvalidValue;
+  while (blocks < LP_CLUSTER && (int64_t)a.n_rows * blocks * 2 <= sms && pieces >= 2 * blocks * LP_FEW) blocks *= 2;
+  const int per_block = (pieces + blocks - 1) / blocks;
   auto *const kernel = blocks > 1 ? token_logprobs_kernel<X, true> : token_logprobs_kernel<X, false>;
-  static std::atomic<uint64_t> ready[2];  // devices whose limit of dynamic shared memory is raised
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
-  if (!bit || !(ready[blocks > 1].load(std::memory_order_relaxed) & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LP_PIECES * 16);
-    if (e != cudaSuccess) return e;
-    ready[blocks > 1].fetch_or(bit, std::memory_order_relaxed);
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(a.n_rows * blocks));
-  cfg.blockDim = dim3(LP_THREADS);
-  cfg.dynamicSmemBytes = std::min(per_block, LP_PIECES) * 16;
+  cfg.blockDim = dim3(blocks > 1 ? LP_FEW : LP_MANY);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -430,14 +505,14 @@ cudaError_t launch(const kie_token_logprobs_args &a, int dev, int sms, cudaStrea
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = blocks > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a, per_block, rounds);
+  return cudaLaunchKernelEx(&cfg, kernel, a, per_block);
 }
 
 }  // namespace
 }  // namespace kie
 
-cudaError_t kie_launch_token_logprobs(const kie_token_logprobs_args &a, int dev, int sms, cudaStream_t stream) {
-  return a.dtype == KIE_F32   ? kie::launch<KIE_F32>(a, dev, sms, stream)
-         : a.dtype == KIE_F16 ? kie::launch<KIE_F16>(a, dev, sms, stream)
-                              : kie::launch<KIE_BF16>(a, dev, sms, stream);
+cudaError_t kie_launch_token_logprobs(const kie_token_logprobs_args &a, int sms, cudaStream_t stream) {
+  return a.dtype == KIE_F32   ? kie::launch<KIE_F32>(a, sms, stream)
+         : a.dtype == KIE_F16 ? kie::launch<KIE_F16>(a, sms, stream)
+                              : kie::launch<KIE_BF16>(a, sms, stream);
 }

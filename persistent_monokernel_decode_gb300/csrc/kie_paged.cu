@@ -760,5 +760,5 @@ int kie_token_logprobs(const kie_token_logprobs_args *p, void *stream) {
   if (!ints_aligned({a.tokens, a.logprob, a.entropy, a.top_ids, a.top_logprobs})) return refuse("an array is not 4-byte aligned");
   int dev, sms;
   if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
-  return finish(kie_launch_token_logprobs(a, dev, sms, (cudaStream_t)stream), "token_logprobs");
+  return finish(kie_launch_token_logprobs(a, sms, (cudaStream_t)stream), "token_logprobs");
 }

@@ -391,7 +391,8 @@ int kie_paged_copy(const kie_paged_copy_args *a, void *stream);
  * page_map [n_blocks] holds the new id of each page in use, -1 for the free ones, for whoever else knows pages by id. In
  * place: block_table (the entries of the rows' positions), shares [n_blocks] (0 for free pages) and free_blocks, which is
  * n_blocks - 1, ..., n_live from the bottom, so that n_live is given next; n_free_out [1] (free_capacity at most) must not
- * be n_free. The copies have to come before the next append or attention. */
+ * be n_free. The copies have to come before the next append or attention. n_blocks <= KIE_PAGED_MAX_COMPACT. */
+#define KIE_PAGED_MAX_COMPACT (1 << 22)
 typedef struct {
   const int32_t *lens, *n_free;
   int32_t *block_table;

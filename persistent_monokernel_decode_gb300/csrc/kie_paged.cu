@@ -732,6 +732,7 @@ int kie_paged_compact(const kie_paged_compact_args *p, void *stream) {
   const kie_paged_compact_args &a = *p;
   if (a.n_seqs < 0 || a.max_blocks < 1 || a.free_capacity < 0 || a.n_blocks < 1)
     return refuse("n_seqs and free_capacity must be >= 0, max_blocks and n_blocks >= 1");
+  if (a.n_blocks > KIE_PAGED_MAX_COMPACT) return refuse("n_blocks must not pass KIE_PAGED_MAX_COMPACT");
   if (a.block_size < PAGED_ROWS || a.block_size % PAGED_ROWS) return refuse("block_size must be a positive multiple of 16");
   if ((int64_t)a.max_blocks * a.block_size > INT_MAX) return refuse("max_blocks * block_size must be below 2^31");
   if (!a.n_free || !a.n_free_out || !a.shares || !a.page_map) return refuse("n_free, n_free_out, shares or page_map is NULL");
@@ -742,7 +743,9 @@ int kie_paged_compact(const kie_paged_compact_args *p, void *stream) {
   if (!ints_aligned({a.lens, a.n_free, a.block_table, a.shares, a.free_blocks, a.n_free_out, a.src, a.dst, a.page_map}))
     return refuse("an int32 array is not 4-byte aligned");
   if (a.n_free_out == a.n_free) return refuse("n_free_out must not be n_free");
-  return finish(kie_launch_paged_compact(a, (cudaStream_t)stream), "paged_compact");
+  int dev, sms;
+  if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
+  return finish(kie_launch_paged_compact(a, dev, (cudaStream_t)stream), "paged_compact");
 }
 
 int kie_token_logprobs(const kie_token_logprobs_args *p, void *stream) {

@@ -40,20 +40,38 @@ __device__ __forceinline__ int rank_of(bool flag, int *all) {
   return __shfl_sync(0xffffffffu, up - n, warp) + __popc(m & ((1u << lane) - 1u));
 }
 
-// The sum of every block's value (*all), and of those before this one. Every thread calls, in every block.
-__device__ __forceinline__ int before_in_cluster(const cg::cluster_group &cl, int mine, int *all) {
-  __shared__ int s_value;
-  if (threadIdx.x == 0) s_value = mine;
+// The sum of v over the block. Every thread calls.
+__device__ __forceinline__ int block_sum(int v) {
+  __shared__ int s_sum[PS_WARPS];
+  v = __reduce_add_sync(0xffffffffu, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return __reduce_add_sync(0xffffffffu, s_sum[threadIdx.x & 31]);
+}
+
+// The sum of every block's value (*all), and of those before this one. *place, in shared memory, is not used again. Every
+// thread calls, in every block, and the cluster meets once more before a block ends.
+__device__ __forceinline__ int before_in_cluster(const cg::cluster_group &cl, int *place, int mine, int *all) {
+  if (threadIdx.x == 0) *place = mine;
   cl.sync();
-  int before = 0, sum = 0;
-  for (unsigned i = 0; i < cl.num_blocks(); ++i) {
-    const int v = *cl.map_shared_rank(&s_value, i);
-    if (i < cl.block_rank()) before += v;
-    sum += v;
+  const int lane = threadIdx.x & 31, blocks = cl.num_blocks();
+  const int v = *cl.map_shared_rank(place, min(lane, blocks - 1));
+  *all = __reduce_add_sync(0xffffffffu, lane < blocks ? v : 0);
+  return __reduce_add_sync(0xffffffffu, lane < (int)cl.block_rank() ? v : 0);
+}
+
+// f(j, from[j]) for j < n, the loads of four at a time on their way together: a warp.
+template <class F>
+__device__ __forceinline__ void for_each(const int *from, int n, const F &f) {
+  for (int j0 = threadIdx.x & 31; j0 < n; j0 += 128) {
+    int v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = __ldcg(from + min(j0 + 32 * k, n - 1));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (j0 + 32 * k < n) f(j0 + 32 * k, v[k]);
   }
-  cl.sync();  // the values are read before they change, or their block ends
-  *all = sum;
-  return before;
 }
 
 // The i-th of `parts` equal ranges of n, its bounds multiples of 32.
@@ -132,104 +150,150 @@ __global__ void __launch_bounds__(PS_THREADS) paged_fork_kernel(const ForkArgs a
     const int p = parent_of(a, r);
     bool part;
     if (p >= 0 && p != r) {
-      const int *from = a.block_table + p * a.table_stride;
       const int n = pages_of(a, a.lens[p], &part);
-      for (int j = lane; j < n; j += 32)
-        staged[(int64_t)r * a.max_blocks + j] = rank[r] >= 0 && j == n - 1 ? a.free_blocks[n_free - 1 - rank[r]] : from[j];
+      int *to = staged + (int64_t)r * a.max_blocks;
+      for_each(a.block_table + p * a.table_stride, n, [&](int j, int x) { to[j] = x; });
+      if (rank[r] >= 0 && lane == ((n - 1) & 31)) to[n - 1] = a.free_blocks[n_free - 1 - rank[r]];  // the lane that wrote it
     }
     if (kids[r] == 1) continue;  // its pages have as many holders as before
     const int n = pages_of(a, a.lens[r], &part);
-    for (int j = lane; j < n; j += 32) {
-      const int x = a.block_table[r * a.table_stride + j];
+    for_each(a.block_table + r * a.table_stride, n, [&](int j, int x) {
       const int change = (part && j == n - 1 ? min(kids[r], 1) : kids[r]) - 1;
       if (change && (unsigned)x < (unsigned)a.n_blocks) atomicAdd(&a.shares[x], change);
-    }
+    });
   }
   cl.sync();
   for (int r = block * PS_WARPS + warp; r < R; r += blocks * PS_WARPS) {
     const int p = parent_of(a, r);
     if (p < 0 || p == r) continue;
     bool part;
-    const int n = pages_of(a, a.lens[p], &part);
-    for (int j = lane; j < n; j += 32) a.block_table[r * a.table_stride + j] = __ldcg(staged + (int64_t)r * a.max_blocks + j);
+    int *to = a.block_table + r * a.table_stride;
+    for_each(staged + (int64_t)r * a.max_blocks, pages_of(a, a.lens[p], &part), [&](int j, int x) { to[j] = x; });
   }
   // pages that nobody holds any more, in the order of their ids
+  __shared__ int s_freed;
   const int x0 = range_begin(a.n_blocks, block, blocks), x1 = range_begin(a.n_blocks, block + 1, blocks);
   int mine = 0, freed;
-  for (int x = x0 + tid; x - tid < x1; x += PS_THREADS) mine += __syncthreads_count(x < x1 && __ldcg(&a.shares[x]) < 0);
-  long long to = (long long)n_free - total + before_in_cluster(cl, mine, &freed);
+#pragma unroll 8
+  for (int x = x0 + tid; x < x1; x += PS_THREADS) mine += __ldcg(&a.shares[x]) < 0;
+  mine = block_sum(mine);
+  long long to = (long long)n_free - total + before_in_cluster(cl, &s_freed, mine, &freed);
   if (mine)
-    for (int x = x0 + tid; x - tid < x1; x += PS_THREADS) {
-      const bool free = x < x1 && __ldcg(&a.shares[x]) < 0;
-      int all;
-      const int k = rank_of(free, &all);
-      if (free) {
-        a.shares[x] = 0;
-        if (to + k < a.free_capacity) a.free_blocks[to + k] = x;
+    for (int c0 = x0; c0 < x1; c0 += 4 * PS_THREADS) {
+      bool free[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int x = c0 + k * PS_THREADS + tid;
+        free[k] = x < x1 && __ldcg(&a.shares[x]) < 0;
       }
-      to += all;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int x = c0 + k * PS_THREADS + tid;
+        int all;
+        const int place = rank_of(free[k], &all);
+        if (free[k]) {
+          a.shares[x] = 0;
+          if (to + place < a.free_capacity) a.free_blocks[to + place] = x;
+        }
+        to += all;
+      }
     }
   if (block == 0 && tid == 0) *a.n_free_out = (int)min((long long)n_free - total + freed, (long long)a.free_capacity);
+  cl.sync();  // the others have read this block's count
 }
 
 // ---- compaction ----------------------------------------------------------------------------------------------
 
-// Live pages at and behind the number of live pages move into the free ones before it, both in the order of their ids.
-__global__ void __launch_bounds__(PS_THREADS) paged_compact_kernel(const kie_paged_compact_args a) {
+// Live pages at and behind the number of live pages move into the free ones before it, both in the order of their ids. Each
+// block keeps, for its range of pages, a bit to each in shared memory (set: free) and how many free ones lie before every 32:
+// the list of free pages is read once, and everything else follows from the bits.
+__global__ void __launch_bounds__(PS_THREADS) paged_compact_kernel(const kie_paged_compact_args a, int per) {
   begin_after_previous();
+  extern __shared__ int ps_raw[];
+  __shared__ int s_values[2];
   const cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, n = a.n_blocks, most = n / 2;
   const int blocks = cl.num_blocks(), block = cl.block_rank(), all_tid = block * PS_THREADS + tid, all = blocks * PS_THREADS;
-  const int x0 = range_begin(n, block, blocks), x1 = range_begin(n, block + 1, blocks);
-  for (int x = x0 + tid; x < x1; x += PS_THREADS) a.page_map[x] = 0;
+  const int x0 = (int)min((long long)block * per, (long long)n), x1 = (int)min((long long)x0 + per, (long long)n);
+  const int words = per / 32;
+  unsigned *bits = reinterpret_cast<unsigned *>(ps_raw);
+  int *before = ps_raw + words;
+  for (int w = tid; w < words; w += PS_THREADS) bits[w] = 0u;
   cl.sync();
   const int n_free = min(max(*a.n_free, 0), a.free_capacity);
-  for (int i = all_tid; i < n_free; i += all) {
-    const int x = a.free_blocks[i];
-    if ((unsigned)x < (unsigned)n) a.page_map[x] = -1;
+  for (int i0 = all_tid; i0 < n_free; i0 += 4 * all) {
+    int x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = i0 + k * all < n_free ? a.free_blocks[i0 + k * all] : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if ((unsigned)x[k] < (unsigned)n)
+        atomicOr(cl.map_shared_rank(bits, x[k] / per) + x[k] % per / 32, 1u << (x[k] % 32));
   }
   cl.sync();
-  int mine = 0, live;
-  for (int x = x0 + tid; x - tid < x1; x += PS_THREADS) mine += __syncthreads_count(x < x1 && __ldcg(&a.page_map[x]) == 0);
-  int first = before_in_cluster(cl, mine, &live);  // live pages before this block's
-  mine = 0;
-  for (int x = x0 + tid; x - tid < x1; x += PS_THREADS)
-    mine += __syncthreads_count(x < x1 && x < live && __ldcg(&a.page_map[x]) == 0);
-  int low;
-  before_in_cluster(cl, mine, &low);  // live pages that stay
-  const int moves = live - low;
-  for (int x = x0 + tid; x - tid < x1; x += PS_THREADS) {
-    const bool used = x < x1 && __ldcg(&a.page_map[x]) == 0;
-    int in_chunk;
-    const int k = first + rank_of(used, &in_chunk);
-    if (x < x1 && !used && x < live) a.dst[x - k] = x;
-    if (used && x >= live) a.src[k - low] = x;
-    first += in_chunk;
+  // free pages before each word of this block, and in it
+  int in_block = 0;
+  for (int w0 = 0; w0 < words; w0 += PS_THREADS) {
+    const int w = w0 + tid, c = w < words ? __popc(bits[w]) : 0;
+    int up = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane >= o) up += y;
+    }
+    __shared__ int s_warp[PS_WARPS];
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = up;
+    __syncthreads();
+    const int part = s_warp[lane];
+    const int earlier = __reduce_add_sync(0xffffffffu, lane < warp ? part : 0), sum = __reduce_add_sync(0xffffffffu, part);
+    if (w < words) before[w] = in_block + earlier + up - c;
+    in_block += sum;
+  }
+  int free;
+  const int first = before_in_cluster(cl, &s_values[0], in_block, &free);  // of the blocks before
+  const int live = n - free;
+  __syncthreads();
+  const auto free_before = [&](int x) {  // of a page of this block
+    const int w = (x - x0) >> 5;
+    return first + before[w] + __popc(bits[w] & ((1u << (x & 31)) - 1u));
+  };
+  // free pages below `live`: as many pages move
+  int moves;
+  before_in_cluster(cl, &s_values[1], live > x0 && live <= x1 ? (live < x1 ? free_before(live) : first + in_block) : 0, &moves);
+  for (int x = x0 + tid; x < x1; x += PS_THREADS) {
+    const bool unused = bits[(x - x0) >> 5] >> (x & 31) & 1u;
+    const int k = free_before(x);
+    if (unused && x < live) a.dst[k] = x;
+    if (!unused && x >= live) a.src[x - k - (live - moves)] = x;  // x - k live pages lie before it, live - moves of them stay
+    if (unused || x < live) a.page_map[x] = unused ? -1 : x;
   }
   for (int i = moves + all_tid; i < most; i += all) a.src[i] = a.dst[i] = -1;
+  for (int i = all_tid; i < min(free, a.free_capacity); i += all) a.free_blocks[i] = n - 1 - i;
   cl.sync();
   for (int i = all_tid; i < moves; i += all) {
     const int from = __ldcg(&a.src[i]), to = __ldcg(&a.dst[i]);
-    a.shares[to] = a.shares[from];
     a.page_map[from] = to;
+    a.shares[to] = a.shares[from];
   }
-  for (int x = all_tid; x < live; x += all)
-    if (__ldcg(&a.page_map[x]) == 0) a.page_map[x] = x;  // the holes, at -1, stay so
   cl.sync();
   for (int x = live + all_tid; x < n; x += all) a.shares[x] = 0;
-  for (int i = all_tid; i < min(n - live, a.free_capacity); i += all) a.free_blocks[i] = n - 1 - i;
   for (int r = block * PS_WARPS + warp; r < a.n_seqs; r += blocks * PS_WARPS) {
     const int len = a.lens[r];
     const int pages = len > 0 ? min((int)(((unsigned)len + a.block_size - 1) / (unsigned)a.block_size), a.max_blocks) : 0;
-    for (int j = lane; j < pages; j += 32) {
-      int *at = a.block_table + r * a.table_stride + j;
-      const int x = *at;
-      if ((unsigned)x >= (unsigned)n) continue;
-      const int to = __ldcg(&a.page_map[x]);
-      if (to >= 0 && to != x) *at = to;
+    int *row = a.block_table + r * a.table_stride;
+    for (int j0 = lane; j0 < pages; j0 += 128) {
+      int x[4], to[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = j0 + 32 * k < pages ? row[j0 + 32 * k] : -1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) to[k] = (unsigned)x[k] < (unsigned)n ? __ldcg(&a.page_map[x[k]]) : -1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (to[k] >= 0 && to[k] != x[k]) row[j0 + 32 * k] = to[k];
     }
   }
-  if (all_tid == 0) *a.n_free_out = min(n - live, a.free_capacity);
+  if (all_tid == 0) *a.n_free_out = min(free, a.free_capacity);
 }
 
 // ---- copies --------------------------------------------------------------------------------------------------
@@ -265,8 +329,18 @@ __global__ void __launch_bounds__(PC_THREADS) paged_copy_kernel(const kie_paged_
   }
 }
 
-template <class K, class A>
-cudaError_t launch_cluster(K kernel, size_t smem, cudaStream_t stream, const A &args) {
+// Raises a kernel's limit of dynamic shared memory, once on each device.
+template <class K>
+cudaError_t allow_smem(K kernel, std::atomic<uint64_t> *ready, int dev, size_t most) {
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit && (ready->load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (e == cudaSuccess) ready->fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+template <class K, class... A>
+cudaError_t launch_cluster(K kernel, size_t smem, cudaStream_t stream, const A &...args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(PS_CLUSTER);
   cfg.blockDim = dim3(PS_THREADS);
@@ -280,26 +354,25 @@ cudaError_t launch_cluster(K kernel, size_t smem, cudaStream_t stream, const A &
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, args);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace
 }  // namespace kie
 
 cudaError_t kie_launch_paged_fork(const kie::ForkArgs &a, int dev, cudaStream_t stream) {
-  static std::atomic<uint64_t> ready{0};  // devices whose limit of dynamic shared memory is raised
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
-  if (!bit || !(ready.load(std::memory_order_relaxed) & bit)) {
-    const cudaError_t e = cudaFuncSetAttribute(kie::paged_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               3 * KIE_PAGED_MAX_FORK * 4);
-    if (e != cudaSuccess) return e;
-    ready.fetch_or(bit, std::memory_order_relaxed);
-  }
-  return kie::launch_cluster(kie::paged_fork_kernel, (size_t)3 * a.n_seqs * 4, stream, a);
+  static std::atomic<uint64_t> ready{0};
+  const cudaError_t e = kie::allow_smem(kie::paged_fork_kernel, &ready, dev, 3 * KIE_PAGED_MAX_FORK * 4);
+  return e != cudaSuccess ? e : kie::launch_cluster(kie::paged_fork_kernel, (size_t)3 * a.n_seqs * 4, stream, a);
 }
 
-cudaError_t kie_launch_paged_compact(const kie_paged_compact_args &a, cudaStream_t stream) {
-  return kie::launch_cluster(kie::paged_compact_kernel, 0, stream, a);
+cudaError_t kie_launch_paged_compact(const kie_paged_compact_args &a, int dev, cudaStream_t stream) {
+  static std::atomic<uint64_t> ready{0};
+  const auto pages = [](int n) { return ((n + kie::PS_CLUSTER - 1) / kie::PS_CLUSTER + 31) / 32 * 32; };  // of a block
+  const cudaError_t e = kie::allow_smem(kie::paged_compact_kernel, &ready, dev, (size_t)pages(KIE_PAGED_MAX_COMPACT) / 32 * 8);
+  return e != cudaSuccess ? e
+                          : kie::launch_cluster(kie::paged_compact_kernel, (size_t)pages(a.n_blocks) / 32 * 8, stream, a,
+                                                pages(a.n_blocks));
 }
 
 cudaError_t kie_launch_paged_copy(const kie_paged_copy_args &a, cudaStream_t stream) {

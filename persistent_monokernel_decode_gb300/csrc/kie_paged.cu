@@ -588,7 +588,7 @@ int kie_paged_release(const kie_paged_release_args *p, void *stream) {
     f.block_size = a.block_size;
     f.n_blocks = a.n_blocks;
     f.free_capacity = a.free_capacity;
-    return finish(kie_launch_paged_fork(f, dev, (cudaStream_t)stream), "paged_release");
+    return finish(kie_launch_paged_fork(f, dev, sms, (cudaStream_t)stream), "paged_release");
   }
   const int teams = PX_THREADS / px_team(a.n_seqs <= PX_THREADS ? 1 : 4);
   const int grid = std::min(sms, std::max(1, (a.n_seqs + teams - 1) / teams));
@@ -702,7 +702,7 @@ int kie_paged_fork(const kie_paged_fork_args *p, void *stream) {
   if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
   ForkArgs f = {};
   static_cast<kie_paged_fork_args &>(f) = a;
-  return finish(kie_launch_paged_fork(f, dev, (cudaStream_t)stream), "paged_fork");
+  return finish(kie_launch_paged_fork(f, dev, sms, (cudaStream_t)stream), "paged_fork");
 }
 
 int kie_paged_copy(const kie_paged_copy_args *p, void *stream) {
@@ -745,7 +745,7 @@ int kie_paged_compact(const kie_paged_compact_args *p, void *stream) {
   if (a.n_free_out == a.n_free) return refuse("n_free_out must not be n_free");
   int dev, sms;
   if (!sm_count(&dev, &sms)) return finish(cudaErrorInvalidDevice, "device query");
-  return finish(kie_launch_paged_compact(a, dev, (cudaStream_t)stream), "paged_compact");
+  return finish(kie_launch_paged_compact(a, dev, sms, (cudaStream_t)stream), "paged_compact");
 }
 
 int kie_token_logprobs(const kie_token_logprobs_args *p, void *stream) {

@@ -135,8 +135,8 @@ __device__ __forceinline__ int row_len(const kie_paged_attention_args &a, int b)
 
 }  // namespace kie
 
-cudaError_t kie_launch_paged_fork(const kie::ForkArgs &a, int dev, cudaStream_t stream);
-cudaError_t kie_launch_paged_compact(const kie_paged_compact_args &a, int dev, cudaStream_t stream);
+cudaError_t kie_launch_paged_fork(const kie::ForkArgs &a, int dev, int sms, cudaStream_t stream);
+cudaError_t kie_launch_paged_compact(const kie_paged_compact_args &a, int dev, int sms, cudaStream_t stream);
 cudaError_t kie_launch_paged_copy(const kie_paged_copy_args &a, cudaStream_t stream);
 cudaError_t kie_launch_token_logprobs(const kie_token_logprobs_args &a, int sms, cudaStream_t stream);
 cudaError_t kie_launch_paged_suffix(const kie::PrefixArgs &a, int dev, int sms, cudaStream_t stream);

@@ -92,30 +92,32 @@ struct ForkArgs : kie_paged_fork_args {
   const uint8_t *done;
 };
 
-// Attention of groups with a common prefix (kie_prefix_attn.cu): the prefixes' kernel works on a list of items (group, tile
-// of its rows, KV head) of PX_ITEM_COST places and one for each unit of positions. Block i takes the places from i *
-// per_block on and leaves a piece of each item whose units it had: the weighted sum of V, unnormalised, for `rows` rows, at
-// prefix[slot * DH], dimensions in groups of eight [DH / 8][rows][8], and at prefix_ml[slot + row] the reference (log2
-// units) and the sum of weights; slot = row.slot + head * row.rows + 128 i.
-constexpr int PX_ITEM_COST = 2, PX_MIN_RUN = 4;
+// Attention of groups with a common prefix is four launches (kie_prefix_attn.cu): a plan; the prefixes; the rows' own
+// positions (kie_paged_attn.cu), beside them; and the join. The prefixes are a list of items (group, tile of its rows, KV head)
+// of PX_ITEM_COST places and one for each unit of positions. Block i takes the places from i * per_block on and leaves a piece
+// of each item whose units it had: the weighted sum of V, unnormalised, for `rows` rows, at prefix[slot * DH], dimensions in
+// groups of eight [DH / 8][rows][8], and at prefix_ml[slot + row] the reference (log2 units) and the sum of weights; slot =
+// row.slot + head * row.rows + 128 i. The rows' own positions are a piece [DH] for each query head, at own and own_ml.
+constexpr int PX_ITEM_COST = 2, PX_MIN_RUN = 2;
 struct PrefixRow {
   long long place;  // of the first head's item in the list
-  int lo, units;    // positions that the group has read for the row; units of an item
+  int lo, units;    // positions that the group reads for the row; units of an item
   int slot, rows, local, unused;  // the row's query heads are rows local .. of the tile
 };
-// Where the pieces of a row's query heads of one KV head are: n of them, 128 slots apart.
-struct PrefixPieces {
-  long long slot;
-  int n, rows, local;
+// Where a block begins: its first item, of the group's `item`-th, at `place`, and the group's rows. place < 0: nothing to do.
+struct PrefixBlock {
+  long long place;
+  int g, item, start, end;
 };
 struct PrefixArgs : kie_paged_attention_args {
   const int32_t *group_start, *prefix_lens;
   int n_groups;
-  int32_t *row_lo;  // lo of each row
-  PrefixRow *rows;
   long long *per_block;
-  float *prefix;
-  float2 *prefix_ml;
+  PrefixBlock *blocks;
+  PrefixRow *rows;
+  int32_t *row_lo;  // lo of each row
+  float *prefix, *own;
+  float2 *prefix_ml, *own_ml;
 };
 
 // The kernels find the rows' ends in lens, be they lengths or a step's positions, and the number of table rows in n_table.
@@ -139,7 +141,7 @@ cudaError_t kie_launch_paged_fork(const kie::ForkArgs &a, int dev, int sms, cuda
 cudaError_t kie_launch_paged_compact(const kie_paged_compact_args &a, int dev, int sms, cudaStream_t stream);
 cudaError_t kie_launch_paged_copy(const kie_paged_copy_args &a, cudaStream_t stream);
 cudaError_t kie_launch_token_logprobs(const kie_token_logprobs_args &a, int sms, cudaStream_t stream);
-cudaError_t kie_launch_paged_suffix(const kie::PrefixArgs &a, int dev, int sms, cudaStream_t stream);
+cudaError_t kie_launch_paged_own(const kie::PrefixArgs &a, int dev, int sms, cudaStream_t stream);
 cudaError_t kie_launch_paged_prefix(const kie_paged_prefix_attention_args &a, int dev, int sms, cudaStream_t stream);
 size_t kie_paged_prefix_workspace_bytes(int n_seqs, int n_heads, int n_kv_heads, int head_dim, int sms);
 cudaError_t kie_launch_paged_attention(const kie_paged_attention_args &a, int dev, int sms, cudaStream_t stream);

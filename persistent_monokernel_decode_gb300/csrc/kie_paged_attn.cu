@@ -75,7 +75,6 @@ struct PaSmem {
   float scale[PA_WARPS][KIND == PG_E4M3 ? T::NS : 1][32];
   float4 m[PA_ROWS], l[PA_ROWS];  // of a row: the four warps'
   uint32_t live[PA_WARPS][T::NS];
-  PrefixPieces prefix;  // of the item at work
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
@@ -179,7 +178,7 @@ __device__ __forceinline__ Span span_of(const Args &a, int b) {
   Span s;
   s.len = row_len(a, b);
   if constexpr (std::is_same<Args, PrefixArgs>::value)
-    s.lo = a.row_lo[b];  // the positions before are the group's
+    s.lo = __ldcg(a.row_lo + b);  // the positions before are the group's
   else
     s.lo = a.window > 0 ? max(0, s.len - a.window) : 0;
   s.from = s.lo & ~15;
@@ -406,47 +405,16 @@ __device__ __forceinline__ void join_pieces(const Pieces &piece, int n, int grou
     if (me.r0 + q * S::STEP < group) put(me.r0 + q * S::STEP, me.d, acc[q], top[q], sum[q]);
 }
 
-// The pieces that the row's group has for its query heads join the row's own sums, in their order.
-template <int DH>
-__device__ __forceinline__ void add_prefix(const PrefixArgs &a, const PrefixPieces &p, int r, int d, float4 &acc, float &M, float &L) {
-  const int n = p.n;
-  const float *o = a.prefix + p.slot * DH + (int64_t)(d >> 3) * p.rows * 8 + (p.local + r) * 8 + (d & 7);
-  const float2 *ml = a.prefix_ml + p.slot + p.local + r;
-  constexpr int BATCH = 12;
-  for (int i0 = 0; i0 < n; i0 += BATCH) {
-    float2 w[BATCH];
-    float4 y[BATCH];
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      const int64_t i = min(i0 + k, n - 1);
-      w[k] = __ldcg(ml + 128 * i);
-      y[k] = __ldcg(reinterpret_cast<const float4 *>(o + 128 * DH * i));
-    }
-    float mn = M;
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k)
-      if (i0 + k < n) mn = fmaxf(mn, w[k].x);
-    const float ref = mn == -INFINITY ? 0.f : mn, f0 = ex2(M - ref);
-    L *= f0, acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k)
-      if (i0 + k < n) {
-        const float f = ex2(w[k].x - ref);
-        L = fmaf(w[k].y, f, L);
-        acc.x = fmaf(y[k].x, f, acc.x), acc.y = fmaf(y[k].y, f, acc.y);
-        acc.z = fmaf(y[k].z, f, acc.z), acc.w = fmaf(y[k].w, f, acc.w);
-      }
-    M = mn;
-  }
-}
-
 // Four dimensions of a query head's output from its weighted sum, and its lse from the reference M (log2 units) and the
 // sum of weights L: zeros and -inf where nothing was attended. vec: the output is aligned for one store of four.
 template <int DH, class Args>
-__device__ __forceinline__ void finish4(const Args &a, const PrefixPieces &prefix, bool vec, int b, int h, int r, int d, float4 acc,
-                                        float M, float L) {
-  if constexpr (std::is_same<Args, PrefixArgs>::value) add_prefix<DH>(a, prefix, r, d, acc, M, L);
-  const int64_t head = (int64_t)h * (a.n_heads / a.pages.n_kv_heads) + r;
+__device__ __forceinline__ void finish4(const Args &a, bool vec, int b, int64_t head, int d, float4 acc, float M, float L) {
+  if constexpr (std::is_same<Args, PrefixArgs>::value) {  // the piece that the join takes
+    const int64_t at = b * (int64_t)a.n_heads + head;
+    *reinterpret_cast<float4 *>(a.own + at * DH + d) = acc;
+    if (d == 0) a.own_ml[at] = make_float2(M, L);
+    return;
+  }
   const float inv = L == 0.f ? 0.f : rcp(L);
   const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
   const int64_t to = b * a.out_stride[0] + head * a.out_stride[1] + d;
@@ -475,14 +443,14 @@ __device__ __forceinline__ void put_piece(float *p, int group, int r, int d, flo
 // After this block has written its piece of item (b, h), whose `units` units begin at place v of the list: whoever of
 // the blocks that share it comes last joins the pieces.
 template <int DH, class Args>
-__device__ __forceinline__ void publish(const Args &a, const PrefixPieces &prefix, unsigned long long call, int b, int h, long long v,
+__device__ __forceinline__ void publish(const Args &a, unsigned long long call, int b, int h, long long v,
                                         int units, long long per_block) {
   const Workspace ws(a, DH);
   const int first = (int)divide(v, per_block), last = (int)divide(v + units - 1, per_block);
   const int group = a.n_heads / a.pages.n_kv_heads, n = last - first + 1;
   const bool vec = out_vec(a);
   const auto finish = [&](int r, int d, float4 acc, float M, float L) {
-    finish4<DH>(a, prefix, vec, b, h, r, d, acc, M, L);
+    finish4<DH>(a, vec, b, (int64_t)h * group + r, d, acc, M, L);
   };
   const size_t step = PA_PIECES * ws.piece;
   if (n <= PA_ONE_LEVEL) {
@@ -557,12 +525,21 @@ paged_attn_kernel(const Args a, unsigned long long call) {
   const unsigned bs = a.pages.block_size;
   const int bs_shift = (bs & (bs - 1)) ? -1 : __ffs(bs) - 1;
 
-  wait_for_previous();
+  // Beside a prefix the kernel before this one is at work on it, and what came before that is complete: its blocks let this
+  // one begin when they have seen to that. The join has to find both complete, so the last block waits, in the end.
+  constexpr bool BESIDE = std::is_same<Args, PrefixArgs>::value;
+  if (BESIDE)
+    __threadfence();  // nothing that older kernels left in this SM's L1 is read
+  else
+    wait_for_previous();
   Cursor<T::UNIT> c;
   int end;
   long long per_block;
   locate(a, &c, &end, &per_block);
-  if (c.v >= end) return;
+  if (c.v >= end) {
+    if (BESIDE && blockIdx.x == gridDim.x - 1) wait_for_previous();
+    return;
+  }
 
   // Chunk ch of row r of a half lies at chunk ch ^ swz(r): the eight rows of an 8 x 8 matrix fall in different banks.
   const auto swz = [](int row) { return CH >= 8 ? row & 7 : (row >> 1) & 3; };
@@ -661,9 +638,6 @@ paged_attn_kernel(const Args a, unsigned long long call) {
         [&](int i) { return 16 * (i >> 1) + (KIND == PG_E4M3 ? 4 * t + 2 * (i & 1) : 2 * t + 8 * (i & 1)); }, raw);
   };
   request_q(c.b, c.h);
-  PrefixRow row;
-  long long prefix_per = 1;
-  if constexpr (std::is_same<Args, PrefixArgs>::value) row = a.rows[c.b], prefix_per = *a.per_block;
   set_head();
   fetch_pages();
 #pragma unroll 1
@@ -681,16 +655,6 @@ paged_attn_kernel(const Args a, unsigned long long call) {
 
   for (;;) {  // an item, or this block's part of it
     const int units = min(c.s.n - c.unit, end - c.v);
-    if constexpr (std::is_same<Args, PrefixArgs>::value) {
-      if (threadIdx.x == 0) {  // seen by the others behind the join's barrier
-        const long long place = row.place + (long long)c.h * (row.units + PX_ITEM_COST) + PX_ITEM_COST;
-        const long long first = divide(place, prefix_per);
-        sm.prefix.slot = row.slot + (long long)c.h * row.rows + 128 * first;
-        sm.prefix.n = row.lo > 0 ? (int)(divide(place + row.units - 1, prefix_per) - first) + 1 : 0;
-        sm.prefix.rows = row.rows;
-        sm.prefix.local = row.local;
-      }
-    }
     {  // its query heads as B fragments
       float down = 1.f;
       if (!SPLIT) {
@@ -886,10 +850,7 @@ paged_attn_kernel(const Args a, unsigned long long call) {
     c.v += units - 1;
     c.next(a);
     const bool done = c.v >= end;
-    if (!done) {  // the next item's queries arrive while this one is finished
-      request_q(c.b, c.h);
-      if constexpr (std::is_same<Args, PrefixArgs>::value) row = a.rows[c.b];
-    }
+    if (!done) request_q(c.b, c.h);  // the next item's queries arrive while this one is finished
     {
       __syncwarp();  // every lane is done with the slot
       float *join = reinterpret_cast<float *>(sm.ring[warp][used]);
@@ -934,18 +895,19 @@ paged_attn_kernel(const Args a, unsigned long long call) {
           acc.z = fmaf(y.z, f[w], acc.z), acc.w = fmaf(y.w, f[w], acc.w);
         }
         if (whole)
-          finish4<DH>(a, sm.prefix, vec, b, h, r, me.d, acc, M, L);
+          finish4<DH>(a, vec, b, (int64_t)h * group + r, me.d, acc, M, L);
         else
           put_piece<DH>(piece, group, r, me.d, acc, M, L);
       }
       if (!whole)
-        publish<DH>(a, sm.prefix, call, b, h, v, n, per_block);
+        publish<DH>(a, call, b, h, v, n, per_block);
       __syncthreads();  // the next half may land in the slot, and the next item's sums in theirs
       if (done) break;
     }
   }
-  let_next_begin();
+  if (!BESIDE) let_next_begin();
   cp_wait<0>();
+  if (BESIDE && blockIdx.x == gridDim.x - 1) wait_for_previous();
 }
 
 // 56 bits, never 0, that no other call of the process has (steps through the odd numbers) and other data hardly holds.
@@ -989,6 +951,6 @@ cudaError_t kie_launch_paged_attention(const kie_paged_attention_args &args, int
   return a.pages.head_dim == 64 ? kie::launch_dh<64>(a, dev, sms, stream) : kie::launch_dh<128>(a, dev, sms, stream);
 }
 
-cudaError_t kie_launch_paged_suffix(const kie::PrefixArgs &a, int dev, int sms, cudaStream_t stream) {
+cudaError_t kie_launch_paged_own(const kie::PrefixArgs &a, int dev, int sms, cudaStream_t stream) {
   return a.pages.head_dim == 64 ? kie::launch_dh<64>(a, dev, sms, stream) : kie::launch_dh<128>(a, dev, sms, stream);
 }

@@ -64,8 +64,6 @@ struct PxSmem {
   uint32_t live[PX_TILES];       // bit i: positions 16 i .. 16 i + 15 lie on a page
   float rs[PX_M];                // score scale of a row, in log2 units
   uint64_t full[T::NS], empty[T::NS], unit[PX_TILES], s_full[2], p_full[2], pv_done[2], fix, raw_full[T::RAW], raw_empty[T::RAW];
-  long long place, sums[PX_THREADS / 32];  // the first item's place in the list; scratch of the sums over the block
-  int g, edge[2];                // its group, and that one's rows
   int reach;                     // positions of the prefix that the longest row of the group has
   uint32_t tmem;
   int failed;
@@ -225,8 +223,10 @@ __device__ __forceinline__ long long divide_up(long long a, unsigned b) {  // a 
   return (a >> 32) == 0 ? (long long)((unsigned)a / b) : a / b;
 }
 
+constexpr int PL_THREADS = 1024;
 // Sums over the block in thread order: v becomes the sum of the threads' before this one, *all of all.
-__device__ __forceinline__ long long sum_before(long long v, long long *s_warp, long long *all) {
+__device__ __forceinline__ long long sum_before(long long v, long long *all) {
+  __shared__ long long s_warp[PL_THREADS / 32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long up = v;
 #pragma unroll
@@ -236,14 +236,94 @@ __device__ __forceinline__ long long sum_before(long long v, long long *s_warp, 
   }
   if (lane == 31) s_warp[warp] = up;
   __syncthreads();
-  long long before = up - v, sum = 0;
-  for (int w = 0; w < PX_THREADS / 32; ++w) {
-    if (w < warp) before += s_warp[w];
-    sum += s_warp[w];
+  long long w = s_warp[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += x;
   }
+  *all = __shfl_sync(0xffffffffu, w, 31);
+  const long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  return up - v + (warp > 0 ? before : 0);
+}
+
+// The list: what each row and each block of the prefixes' kernel has to know. Every block of the plan goes over all groups and
+// then sees to its share of the rows and blocks.
+__global__ void __launch_bounds__(PL_THREADS) plan_kernel(const PrefixArgs a, int prefix_blocks) {
+  begin_after_previous();
+  extern __shared__ long long base[];  // places before each group, and before the end
+  int *const starts = reinterpret_cast<int *>(base + a.n_groups + 1);
+  const int tid = threadIdx.x, G = a.n_groups, heads = a.pages.n_kv_heads, group = a.n_heads / heads, members = PX_M / group;
+  const int each = (G + PL_THREADS - 1) / PL_THREADS, g0 = min(tid * each, G), g1 = min(g0 + each, G);
+  bool falls = false;
+  long long mine = 0, total;
+  for (int g = g0; g < g1; ++g) {
+    const int start = clamp_start(a, g), end = clamp_start(a, g + 1);
+    falls |= end < start;
+    mine += places_of(a, group_of(a, g, start, end), members);
+    starts[g] = start;
+  }
+  if (tid == 0) starts[G] = clamp_start(a, G);
+  if (__syncthreads_or(falls)) {  // a start below an earlier one counts as that one
+    if (tid == 0)
+      for (int g = 0; g < G; ++g) starts[g + 1] = max(starts[g + 1], starts[g]);
+    __syncthreads();
+    mine = 0;
+    for (int g = g0; g < g1; ++g) mine += places_of(a, group_of(a, g, starts[g], starts[g + 1]), members);
+  }
+  long long at = sum_before(mine, &total);
+  for (int g = g0; g < g1; ++g) {
+    base[g] = at;
+    at += places_of(a, group_of(a, g, starts[g], starts[g + 1]), members);
+  }
+  if (tid == 0) base[G] = total;
   __syncthreads();
-  *all = sum;
-  return before;
+  const long long per = max(divide_up(total, prefix_blocks), (long long)PX_MIN_RUN);
+  if (blockIdx.x == 0 && tid == 0) *a.per_block = per;
+  for (int k = blockIdx.x * PL_THREADS + tid; k < prefix_blocks; k += gridDim.x * PL_THREADS) {
+    const long long v0 = k * per;
+    PrefixBlock b = {-1, 0, 0, 0, 0};
+    if (v0 < total) {
+      int lo = 0, hi = G;  // the last group that begins at v0 or before it and is not empty
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (base[mid] <= v0)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      const Group x = group_of(a, lo, starts[lo], starts[lo + 1]);
+      const unsigned span = x.units + PX_ITEM_COST;
+      b.g = lo, b.start = x.start, b.end = x.end;
+      b.item = (int)(divide_up(v0 - base[lo] + 1, span) - 1);
+      b.place = base[lo] + (long long)b.item * span;
+    }
+    a.blocks[k] = b;
+  }
+  for (int b = blockIdx.x * PL_THREADS + tid; b < a.n_seqs; b += gridDim.x * PL_THREADS) {
+    int lo = 0, hi = G + 1;  // the number of starts that are not behind the row
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (starts[mid] <= b)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    const int g = lo - 1;
+    PrefixRow row = {};
+    if (g >= 0 && g < G) {
+      const Group x = group_of(a, g, starts[g], starts[g + 1]);
+      const int t = (b - x.start) / members, first = x.start + t * members;
+      row.lo = min(x.prefix, length_of(a, b));
+      row.units = x.units;
+      row.place = base[g] + (long long)t * heads * (x.units + PX_ITEM_COST);
+      row.slot = first * a.n_heads;
+      row.rows = min(members, x.end - first) * group;
+      row.local = (b - first) * group;
+    }
+    a.row_lo[b] = row.lo;
+    a.rows[b] = row;
+  }
 }
 
 // The E neighbouring elements of a query that start at `at`, as they are: fp32 (WIDE) or two to a word; zeros if not live.
@@ -740,82 +820,11 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ PrefixMaps maps) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.v) : "memory");
   }
   wait_for_previous();
-
-  // ---- where this block's run begins
-  const int G = a.n_groups, each = (G + PX_THREADS - 1) / PX_THREADS, g0 = min(tid * each, G), g1 = min(g0 + each, G);
-  int *starts = reinterpret_cast<int *>(px_raw);  // [n_groups + 1]; the ring and queries are not in use yet
-  bool falls = false;
-  long long mine = 0, total;
-  for (int g = g0; g < g1; ++g) {
-    const int start = clamp_start(a, g), end = clamp_start(a, g + 1);
-    falls |= end < start;
-    mine += places_of(a, group_of(a, g, start, end), members);
-  }
-  falls = __syncthreads_or(falls);
-  const auto start_of = [&](int g) { return falls ? starts[g] : clamp_start(a, g); };
-  if (falls) {  // a start below an earlier one counts as that one
-    for (int g = tid; g <= G; g += PX_THREADS) starts[g] = clamp_start(a, g);
-    __syncthreads();
-    if (tid == 0)
-      for (int g = 0; g < G; ++g) starts[g + 1] = max(starts[g + 1], starts[g]);
-    __syncthreads();
-    mine = 0;
-    for (int g = g0; g < g1; ++g) mine += places_of(a, group_of(a, g, start_of(g), start_of(g + 1)), members);
-  }
-  const long long before = sum_before(mine, sm.sums, &total);
-  const long long per = max(divide_up(total, gridDim.x), (long long)PX_MIN_RUN), v0 = blockIdx.x * per, v1 = min(v0 + per, total);
-  if (v0 >= before && v0 < before + mine) {
-    long long at = before;
-    int g = g0;
-    for (;; ++g) {
-      const long long n = places_of(a, group_of(a, g, start_of(g), start_of(g + 1)), members);
-      if (v0 < at + n) break;
-      at += n;
-    }
-    sm.g = g, sm.place = at, sm.edge[0] = start_of(g), sm.edge[1] = start_of(g + 1);
-  }
-  // What the join has to know of a row: by the last blocks, which have the least to do
-  const int rows0 = (int)(gridDim.x - 1 - blockIdx.x) * PX_THREADS;
-  for (int b0 = rows0; b0 < a.n_seqs; b0 += gridDim.x * PX_THREADS) {
-    long long *base = reinterpret_cast<long long *>(px_raw + (KIE_PAGED_MAX_GROUPS + 4) * 4);
-    if (b0 == rows0) {
-      long long at = before;
-      for (int g = g0; g < g1; ++g) {
-        if (!falls) starts[g] = clamp_start(a, g);
-        base[g] = at;
-        at += places_of(a, group_of(a, g, start_of(g), start_of(g + 1)), members);
-      }
-      if (tid == 0 && !falls) starts[G] = clamp_start(a, G);
-      __syncthreads();
-    }
-    const int b = b0 + tid;
-    if (b >= a.n_seqs) continue;
-    int lo = 0, hi = G + 1;  // the number of starts that are not behind the row
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (starts[mid] <= b)
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    const int g = lo - 1;
-    PrefixRow row = {};
-    if (g >= 0 && g < G) {
-      const Group x = group_of(a, g, starts[g], starts[g + 1]);
-      const int t = (b - x.start) / members, first = x.start + t * members;
-      row.lo = min(x.prefix, length_of(a, b));
-      row.units = x.units;
-      row.place = base[g] + (long long)t * heads * (x.units + PX_ITEM_COST);
-      row.slot = first * a.n_heads;
-      row.rows = min(members, x.end - first) * group;
-      row.local = (b - first) * group;
-    }
-    a.row_lo[b] = row.lo;
-    a.rows[b] = row;
-  }
-  if (blockIdx.x == 0 && tid == 0) *a.per_block = per;
-  if (v0 >= total) return;
-
+  let_next_begin();  // the rows' own positions need nothing of this kernel
+  const PrefixBlock begin = a.blocks[blockIdx.x];
+  const long long per = *a.per_block;
+  if (begin.place < 0) return;
+  const long long v0 = blockIdx.x * per, v1 = v0 + per;  // places behind the list's end are behind its last item
   if (warp == PX_ISSUER) {
     tmem_alloc(&sm.tmem, PX_TMEM);
     tmem_relinquish();
@@ -827,15 +836,9 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ PrefixMaps maps) {
   const uint32_t my_lanes = (uint32_t)((warp & 3) * 32) << 16;
 
   uint32_t tiles = 0, halves = 0, fixes = 0;  // units of all items so far; halves of them (K or V) in the ring; mended halves
-  int g = sm.g;
-  Group x = group_of(a, g, sm.edge[0], sm.edge[1]);
-  long long place = sm.place;
-  int item;  // of the group: tile * heads + head
-  {
-    const unsigned span = x.units + PX_ITEM_COST;
-    item = (int)(divide_up(v0 - place + 1, span) - 1);
-    place += (long long)item * span;
-  }
+  int g = begin.g, item = begin.item;  // the item is the group's item-th: tile * heads + head
+  Group x = group_of(a, g, begin.start, begin.end);
+  long long place = begin.place;
   for (;;) {
     // ---- an item, or this block's part of it: units [u0, u1)
     const int t = item / heads, h = item % heads, first = x.start + t * members;
@@ -897,14 +900,14 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ PrefixMaps maps) {
       item = 0;
       int end = x.end;
       do {
-        ++g;  // the list has places left, so another group with units follows
+        if (++g >= a.n_groups) break;
         const int start = end;
         end = max(start, clamp_start(a, g + 1));
         x = group_of(a, g, start, end);
       } while (x.units == 0);
+      if (g >= a.n_groups) break;
     }
   }
-  let_next_begin();
   if (warp == PX_ISSUER) tmem_dealloc(tmem, PX_TMEM);
 }
 
@@ -959,8 +962,6 @@ cudaError_t launch(const PrefixArgs &a, int dev, int sms, cudaStream_t stream) {
     return cudaErrorInvalidPitchValue;
   static std::atomic<uint64_t> ready{0};  // devices whose limit of dynamic shared memory is raised
   using T = PxShape<KIND, DH, SPLIT>;
-  using Sm = PxSmem<KIND, DH, SPLIT>;
-  static_assert(offsetof(Sm, live) >= (KIE_PAGED_MAX_GROUPS + 4) * 4 + KIE_PAGED_MAX_GROUPS * 8, "the list's arrays");
   static_assert(T::BLOCKS == 1 || sizeof(PxSmem<KIND, DH, SPLIT>) <= 115712, "two blocks' shared memory");
   // no more than T::BLOCKS to an SM: a third one's TMEM would have to wait
   const int smem = (int)std::max<size_t>(sizeof(PxSmem<KIND, DH, SPLIT>), 80 * 1024);
@@ -971,7 +972,7 @@ cudaError_t launch(const PrefixArgs &a, int dev, int sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  return launch_after_previous(prefix_kernel<KIND, DH, SPLIT>, sms * T::BLOCKS, PX_THREADS, smem, stream, a, maps);
+  return launch_after_previous(prefix_kernel<KIND, DH, SPLIT>, sms, PX_THREADS, smem, stream, a, maps);
 }
 
 template <int DH>
@@ -983,21 +984,113 @@ cudaError_t launch_dh(const PrefixArgs &a, int dev, int sms, cudaStream_t stream
   return wide ? launch<PG_F16, DH, true>(a, dev, sms, stream) : launch<PG_F16, DH, false>(a, dev, sms, stream);
 }
 
+// ---- the join ------------------------------------------------------------------------------------------------
+
+// The pieces of a query head, its own positions' first, then the prefix's in their order: a thread has four dimensions.
+constexpr int PJ_THREADS = 128;
+template <int DH>
+__global__ void __launch_bounds__(PJ_THREADS) join_kernel(const PrefixArgs a) {
+  begin_after_previous();
+  constexpr int LANES = DH / 4;
+  const int64_t at = ((int64_t)blockIdx.x * PJ_THREADS + threadIdx.x) / LANES;  // row * heads + head
+  if (at >= (int64_t)a.n_seqs * a.n_heads) return;
+  const int d = threadIdx.x % LANES * 4, b = (int)(at / a.n_heads), head = (int)(at % a.n_heads);
+  const int group = a.n_heads / a.pages.n_kv_heads, h = head / group;
+  const PrefixRow row = a.rows[b];
+  const long long per = *a.per_block;
+  float4 acc = __ldcg(reinterpret_cast<const float4 *>(a.own + at * DH + d));
+  const float2 own = __ldcg(a.own_ml + at);
+  float M = own.x, L = own.y;
+  if (row.lo > 0) {
+    const long long place = row.place + (long long)h * (row.units + PX_ITEM_COST) + PX_ITEM_COST;
+    const auto block_of = [&](long long v) { return (int)((v | per) >> 32 ? v / per : (unsigned)v / (unsigned)per); };
+    const int first = block_of(place), n = block_of(place + row.units - 1) - first + 1;
+    const int64_t slot = row.slot + (int64_t)h * row.rows + (int64_t)PX_M * first;
+    const int r = row.local + head - h * group;
+    const float *o = a.prefix + slot * DH + (int64_t)(d >> 3) * row.rows * 8 + r * 8 + (d & 7);
+    const float2 *ml = a.prefix_ml + slot + r;
+    constexpr int BATCH = 8;
+    for (int i0 = 0; i0 < n; i0 += BATCH) {
+      float2 w[BATCH];
+      float4 y[BATCH];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const int64_t i = min(i0 + k, n - 1);
+        w[k] = __ldcg(ml + PX_M * i);
+        y[k] = __ldcg(reinterpret_cast<const float4 *>(o + PX_M * DH * i));
+      }
+      float mn = M;
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k)
+        if (i0 + k < n) mn = fmaxf(mn, w[k].x);
+      const float ref = mn == -INFINITY ? 0.f : mn, f0 = ex2(M - ref);
+      L *= f0, acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k)
+        if (i0 + k < n) {
+          const float f = ex2(w[k].x - ref);
+          L = fmaf(w[k].y, f, L);
+          acc.x = fmaf(y[k].x, f, acc.x), acc.y = fmaf(y[k].y, f, acc.y);
+          acc.z = fmaf(y[k].z, f, acc.z), acc.w = fmaf(y[k].w, f, acc.w);
+        }
+      M = mn;
+    }
+  }
+  const float inv = L == 0.f ? 0.f : __fdividef(1.f, L);
+  const float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+  const int64_t to = b * a.out_stride[0] + head * a.out_stride[1] + d;
+  const int size = paged_dtype_bytes(a.q_dtype);
+  const bool vec = ((uintptr_t)a.out | (uintptr_t)(a.out_stride[0] * size) | (uintptr_t)(a.out_stride[1] * size)) % (4 * size) == 0;
+  if (!vec) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) paged_store(a.out, to + e, a.q_dtype, v[e]);
+  } else if (a.q_dtype == KIE_F32) {
+    *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + to) = make_float4(v[0], v[1], v[2], v[3]);
+  } else {
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + to) =
+        make_uint2(pack2(v[0], v[1], a.q_dtype), pack2(v[2], v[3], a.q_dtype));
+  }
+  if (d == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + lg2(L)) * 0.6931471805599453f;
+}
+
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-// The workspace: that of the rows' own positions, then what the two kernels pass on.
+// The workspace: that of the rows' own positions, then what the launches pass on.
 struct Parts {
-  size_t per_block, row_lo, rows, ml, o, all;
+  size_t per_block, blocks, row_lo, rows, prefix_ml, own_ml, own, prefix, all;
   Parts(int n_seqs, int n_heads, int n_kv_heads, int head_dim, int sms) {
-    const size_t slots = (size_t)n_seqs * n_heads + (size_t)PX_M * 2 * sms;
+    const size_t heads = (size_t)n_seqs * n_heads, slots = heads + (size_t)PX_M * sms;
     per_block = up256(kie_paged_attention_workspace_bytes(n_heads, n_kv_heads, head_dim, sms));
-    row_lo = per_block + 256;
+    blocks = per_block + 256;
+    row_lo = up256(blocks + sms * sizeof(PrefixBlock));
     rows = up256(row_lo + (size_t)n_seqs * 4);
-    ml = up256(rows + (size_t)n_seqs * sizeof(PrefixRow));
-    o = up256(ml + slots * 8);
-    all = o + slots * head_dim * 4;
+    prefix_ml = up256(rows + (size_t)n_seqs * sizeof(PrefixRow));
+    own_ml = up256(prefix_ml + slots * 8);
+    own = up256(own_ml + heads * 8);
+    prefix = up256(own + heads * head_dim * 4);
+    all = prefix + slots * head_dim * 4;
   }
 };
+
+template <int DH>
+cudaError_t launch_all(const PrefixArgs &a, int dev, int sms, cudaStream_t stream) {
+  const int plan_blocks = std::max(1, std::min(sms / 8, (a.n_seqs + PL_THREADS - 1) / PL_THREADS));
+  static std::atomic<uint64_t> ready{0};  // devices whose limit of dynamic shared memory is raised
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  cudaError_t e = cudaSuccess;
+  if (!bit || !(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (KIE_PAGED_MAX_GROUPS + 1) * 12);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  if (e == cudaSuccess)
+    e = launch_after_previous(plan_kernel, plan_blocks, PL_THREADS, (size_t)(a.n_groups + 1) * 12, stream, a, sms);
+  if (e == cudaSuccess) e = launch_dh<DH>(a, dev, sms, stream);
+  if (e == cudaSuccess) e = kie_launch_paged_own(a, dev, sms, stream);
+  const int64_t threads = (int64_t)a.n_seqs * a.n_heads * (DH / 4);
+  return e != cudaSuccess ? e
+                          : launch_after_previous(join_kernel<DH>, (unsigned)((threads + PJ_THREADS - 1) / PJ_THREADS), PJ_THREADS, 0,
+                                                  stream, a);
+}
 
 }  // namespace
 }  // namespace kie
@@ -1015,10 +1108,12 @@ cudaError_t kie_launch_paged_prefix(const kie_paged_prefix_attention_args &args,
   const kie::Parts p(a.n_seqs, a.n_heads, a.pages.n_kv_heads, a.pages.head_dim, sms);
   uint8_t *at = static_cast<uint8_t *>(a.workspace);
   a.per_block = reinterpret_cast<long long *>(at + p.per_block);
+  a.blocks = reinterpret_cast<kie::PrefixBlock *>(at + p.blocks);
   a.row_lo = reinterpret_cast<int32_t *>(at + p.row_lo);
   a.rows = reinterpret_cast<kie::PrefixRow *>(at + p.rows);
-  a.prefix_ml = reinterpret_cast<float2 *>(at + p.ml);
-  a.prefix = reinterpret_cast<float *>(at + p.o);
-  const cudaError_t e = a.pages.head_dim == 64 ? kie::launch_dh<64>(a, dev, sms, stream) : kie::launch_dh<128>(a, dev, sms, stream);
-  return e != cudaSuccess ? e : kie_launch_paged_suffix(a, dev, sms, stream);
+  a.prefix_ml = reinterpret_cast<float2 *>(at + p.prefix_ml);
+  a.own_ml = reinterpret_cast<float2 *>(at + p.own_ml);
+  a.own = reinterpret_cast<float *>(at + p.own);
+  a.prefix = reinterpret_cast<float *>(at + p.prefix);
+  return a.pages.head_dim == 64 ? kie::launch_all<64>(a, dev, sms, stream) : kie::launch_all<128>(a, dev, sms, stream);
 }

@@ -97,8 +97,8 @@ struct ForkArgs : kie_paged_fork_args {
 // of PX_ITEM_COST places and one for each unit of positions. Block i takes the places from i * per_block on and leaves a piece
 // of each item whose units it had: the weighted sum of V, unnormalised, for `rows` rows, at prefix[slot * DH], dimensions in
 // groups of eight [DH / 8][rows][8], and at prefix_ml[slot + row] the reference (log2 units) and the sum of weights; slot =
-// row.slot + head * row.rows + 128 i. The rows' own positions are a piece [DH] for each query head, at own and own_ml.
-constexpr int PX_ITEM_COST = 2, PX_MIN_RUN = 2;
+// row.slot + head * row.rows + PX_TILE * i. The rows' own positions are a piece [DH] for each query head, at own and own_ml.
+constexpr int PX_ITEM_COST = 2, PX_MIN_RUN = 2, PX_TILE = 256;
 struct PrefixRow {
   long long place;  // of the first head's item in the list
   int lo, units;    // positions that the group reads for the row; units of an item

@@ -28,15 +28,16 @@
 namespace kie {
 namespace {
 
-constexpr int PX_M = 128, PX_N = 64;       // rows of a tile, positions of a unit
-// Warps: the softmax's four, the loader, two that convert codes, the one that issues the MMAs. Eight, so that two blocks get
-// 128 registers a thread.
-constexpr int PX_SOFT = 4, PX_LOADER = 4, PX_CONVERT = 5, PX_CONVERTERS = 2, PX_ISSUER = 7;
-constexpr int PX_THREADS = 256;
+constexpr int PX_M = 128, PX_N = 64;       // rows of a half of a tile (an MMA's), positions of a unit
+// Warps: four of the softmax for each half of a tile, the loader, two that convert codes, the one that issues the MMAs.
+constexpr int PX_SOFT = 4, PX_LOADER = 8, PX_CONVERT = 9, PX_CONVERTERS = 2, PX_ISSUER = 11;
+constexpr int PX_THREADS = 384;
+// Registers of a thread: what the rows' own attention leaves of an SM with a block of its own there.
+constexpr int PX_REGISTERS = 112;
 // Depth of what is kept per unit besides K and V. The loader is at most NS + RAW <= 6 halves ahead of the oldest one in use,
 // so at most four units ahead of the one whose weights are formed.
 constexpr int PX_TILES = 8;
-constexpr uint32_t PX_TMEM = 256;          // columns: S twice, O
+constexpr uint32_t PX_TMEM = 512;          // columns: for each half, S twice and O
 constexpr unsigned long long PX_TIMEOUT_NS = 2000000000ull;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float P_BIAS = 7.f, P_STEP = 8.f;  // weights are 2^7 2^(v - reference), below 2^15
@@ -46,24 +47,22 @@ enum { PG_F16 = 0, PG_BF16 = 1, PG_E4M3 = 2 };
 
 template <int KIND, int DH, bool SPLIT>
 struct PxShape {
-  static constexpr int Q_BYTES = PX_M * DH * 2 * (SPLIT ? 2 : 1), SLOT = PX_N * DH * 2, CODES = PX_N * DH;
-  // Two blocks fit an SM but where fp32 queries meet E4M3 pages of 128
-  static constexpr int BLOCKS = SPLIT && KIND == PG_E4M3 && DH == 128 ? 1 : 2;
-  static constexpr int NS = KIND == PG_E4M3 ? 3 : SPLIT && DH == 128 ? 3 : 5;  // ring slots
-  static constexpr int RAW = KIND == PG_E4M3 ? 3 : 1;                          // of codes as they come
+  static constexpr int Q_HALF = PX_M * DH * 2 * (SPLIT ? 2 : 1), SLOT = PX_N * DH * 2, CODES = PX_N * DH;
+  static constexpr int NS = KIND == PG_E4M3 ? 3 : 5;     // ring slots
+  static constexpr int RAW = KIND == PG_E4M3 ? 3 : 1;  // of codes as they come
 };
 
 template <int KIND, int DH, bool SPLIT>
 struct PxSmem {
   using T = PxShape<KIND, DH, SPLIT>;
   static constexpr bool E4M3 = KIND == PG_E4M3;
-  uint8_t q[T::Q_BYTES];         // [part][64-dim block][row][128 B], 16-byte chunks swizzled by the row
+  uint8_t q[2][T::Q_HALF];       // of each half: [part][64-dim block][row][128 B], 16-byte chunks swizzled by the row
   uint8_t ring[T::NS][T::SLOT];  // [64-dim block][position][128 B], the same
   uint8_t raw[E4M3 ? T::RAW : 1][E4M3 ? T::CODES : 16];  // [position][DH]
   float scale[E4M3 ? PX_TILES : 1][3][E4M3 ? PX_N : 1];  // of K, of V, log2 of V's
   uint32_t live[PX_TILES];       // bit i: positions 16 i .. 16 i + 15 lie on a page
-  float rs[PX_M];                // score scale of a row, in log2 units
-  uint64_t full[T::NS], empty[T::NS], unit[PX_TILES], s_full[2], p_full[2], pv_done[2], fix, raw_full[T::RAW], raw_empty[T::RAW];
+  float rs[2][PX_M];             // score scale of a row, in log2 units
+  uint64_t full[T::NS], empty[T::NS], unit[PX_TILES], s_full[2][2], p_full[2][2], pv_done[2][2], fix, raw_full[T::RAW], raw_empty[T::RAW];
   int reach;                     // positions of the prefix that the longest row of the group has
   uint32_t tmem;
   int failed;
@@ -253,7 +252,7 @@ __global__ void __launch_bounds__(PL_THREADS) plan_kernel(const PrefixArgs a, in
   begin_after_previous();
   extern __shared__ long long base[];  // places before each group, and before the end
   int *const starts = reinterpret_cast<int *>(base + a.n_groups + 1);
-  const int tid = threadIdx.x, G = a.n_groups, heads = a.pages.n_kv_heads, group = a.n_heads / heads, members = PX_M / group;
+  const int tid = threadIdx.x, G = a.n_groups, heads = a.pages.n_kv_heads, group = a.n_heads / heads, members = 2 * (PX_M / group);
   const int each = (G + PL_THREADS - 1) / PL_THREADS, g0 = min(tid * each, G), g1 = min(g0 + each, G);
   bool falls = false;
   long long mine = 0, total;
@@ -395,7 +394,7 @@ __device__ __forceinline__ int load_item(const PrefixArgs &a, const PrefixMaps &
   reach = __reduce_max_sync(0xffffffffu, reach);
   source = __reduce_min_sync(0xffffffffu, mine == reach ? source : INT_MAX);
   if (lane == 0) sm.reach = reach;
-  asm volatile("bar.arrive 1, 256;" ::: "memory");  // the others, once the queries are there
+  asm volatile("bar.arrive 1, 384;" ::: "memory");  // the others, once the queries are there
   const int n = max(0, min(u1, (reach + PX_N - 1) / PX_N) - u0);
   const int *pages = a.block_table + (n > 0 ? sequence_of(a, source) : 0) * a.table_stride;
   const unsigned bs = a.pages.block_size;
@@ -545,154 +544,199 @@ __device__ __forceinline__ void convert_item(PxSmem<KIND, DH, SPLIT> &sm, int ct
   }
 }
 
-// One warp, an elected lane of which issues.
+// One warp, an elected lane of which issues. parts: halves of the tile that have rows.
 template <int KIND, int DH, bool SPLIT>
-__device__ __forceinline__ void multiply_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_t tmem, int n, uint32_t tiles, uint32_t halves) {
-  constexpr int NS = PxShape<KIND, DH, SPLIT>::NS, KB = DH / 64;
+__device__ __forceinline__ void multiply_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_t tmem, int parts, int n,
+                                              const uint32_t (&units)[2], uint32_t halves) {
+  using T = PxShape<KIND, DH, SPLIT>;
+  constexpr int NS = T::NS, KB = DH / 64;
   constexpr uint32_t S_DESC = px_idesc(PX_N, KIND == PG_BF16, false), O_DESC = px_idesc(DH, KIND == PG_BF16, true);
   // descriptors of the first step; those of the others are 16-byte units further (addresses stay below 2^18)
   const uint64_t q0 = px_desc(smem_u32(sm.q), 16), k0 = px_desc(smem_u32(sm.ring), 16), v0 = px_desc(smem_u32(sm.ring), PX_N * 128);
-  constexpr uint32_t SLOT = PxShape<KIND, DH, SPLIT>::SLOT / 16;
+  constexpr uint32_t SLOT = T::SLOT / 16, Q_HALF = T::Q_HALF / 16;
   uint32_t half = halves;
 #pragma unroll 1
   for (int j = 0; j <= n; ++j) {
     if (j < n) {  // S = Q K^T
-      const uint32_t tile = tiles + j, to = tmem + (tile & 1u) * PX_N;
       const Half<NS> x(half);
       if (!warp_wait(&sm.full[x.slot], x.round, &sm.failed)) return;
-      if (j >= 2 && !warp_wait(&sm.pv_done[tile & 1u], (tile - 2) >> 1 & 1u, &sm.failed)) return;  // unit j - 2 is done with it
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t k = k0 + x.slot * SLOT;
+#pragma unroll 1
+      for (int w = 0; w < parts; ++w) {
+        const uint32_t tile = (w ? units[1] : units[0]) + j, buf = tile & 1u;
+        if (j >= 2 && !warp_wait(&sm.pv_done[w][buf], (tile - 2) >> 1 & 1u, &sm.failed)) return;  // unit j - 2 is done with it
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t k = k0 + x.slot * SLOT, q = q0 + w * Q_HALF;
+          const uint32_t to = tmem + w * (PX_TMEM / 2) + buf * PX_N;
 #pragma unroll
-        for (int p = 0; p < (SPLIT ? 2 : 1); ++p)
+          for (int p = 0; p < (SPLIT ? 2 : 1); ++p)
 #pragma unroll
-          for (int s = 0; s < DH / 16; ++s)
-            tc_mma(to, q0 + (p * KB + s / 4) * (PX_M * 8) + s % 4 * 2, k + s / 4 * (PX_N * 8) + s % 4 * 2, S_DESC, p || s ? 1u : 0u);
-        tc_commit(&sm.empty[x.slot]);
-        tc_commit(&sm.s_full[tile & 1u]);
+            for (int s = 0; s < DH / 16; ++s)
+              tc_mma(to, q + (p * KB + s / 4) * (PX_M * 8) + s % 4 * 2, k + s / 4 * (PX_N * 8) + s % 4 * 2, S_DESC, p || s ? 1u : 0u);
+          if (w == parts - 1) tc_commit(&sm.empty[x.slot]);
+          tc_commit(&sm.s_full[w][buf]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       ++half;
     }
     if (j > 0) {  // O += P V
-      const uint32_t tile = tiles + j - 1, p = tmem + (tile & 1u) * PX_N;
       const Half<NS> x(half);
-      if (!warp_wait(&sm.p_full[tile & 1u], tile >> 1 & 1u, &sm.failed)) return;
       if (!warp_wait(&sm.full[x.slot], x.round, &sm.failed)) return;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t v = v0 + x.slot * SLOT;
+#pragma unroll 1
+      for (int w = 0; w < parts; ++w) {
+        const uint32_t tile = (w ? units[1] : units[0]) + j - 1, buf = tile & 1u;
+        if (!warp_wait(&sm.p_full[w][buf], tile >> 1 & 1u, &sm.failed)) return;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t v = v0 + x.slot * SLOT;
+          const uint32_t to = tmem + w * (PX_TMEM / 2), p = to + buf * PX_N;
 #pragma unroll
-        for (int s = 0; s < PX_N / 16; ++s)
+          for (int s = 0; s < PX_N / 16; ++s)
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
-            tc_mma_ts(tmem + 2 * PX_N, p + s * 16 + part * 8, v + s * 128, O_DESC, j > 1 || s || part ? 1u : 0u);
-        tc_commit(&sm.empty[x.slot]);
-        tc_commit(&sm.pv_done[tile & 1u]);
+            for (int part = 0; part < 2; ++part)
+              tc_mma_ts(to + 2 * PX_N, p + s * 16 + part * 8, v + s * 128, O_DESC, j > 1 || s || part ? 1u : 0u);
+          if (w == parts - 1) tc_commit(&sm.empty[x.slot]);
+          tc_commit(&sm.pv_done[w][buf]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       ++half;
     }
   }
 }
 
-// A thread is the row `row`, which attends to positions below lim; `rows`: whether the warp has any row at all. m, l: the
-// reference (log2 units) and the sum of weights. O is complete on return; false if a wait ran out.
+// Two fp32 operations at a time.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 both(Two r) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(r));
+  return f;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A thread is the row `row` of half `w`, which attends to positions below lim; `rows`: whether the warp has any row at all. m,
+// l: the reference (log2 units) and the sum of weights. units: of the half, in the items before. O is complete on return; false if a wait ran out.
 template <int KIND, int DH, bool SPLIT>
-__device__ __forceinline__ bool soften_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_t tmem, int row, bool rows, int lim, int u0, int n,
-                                            uint32_t tiles, float *m_out, float *l_out) {
-  const float rs = lim > 0 ? sm.rs[row] : 1.f;
+__device__ __forceinline__ bool soften_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_t tmem, int w, int row, bool rows, int lim, int u0,
+                                            int n, uint32_t tiles, uint32_t units, float *m_out, float *l_out) {
+  constexpr bool E4M3 = KIND == PG_E4M3;
+  const float rs = lim > 0 ? sm.rs[w][row] : 1.f;
   const uint32_t t_o = tmem + 2 * PX_N;
   const int lane = row & 31;
   float m = -INFINITY, l = 0.f;
+#pragma unroll 1
   for (int j = 0; j < n; ++j) {
-    const uint32_t tile = tiles + j, t_s = tmem + (tile & 1u) * PX_N;
+    const uint32_t place = (tiles + j) % PX_TILES, tile = units + j, t_s = tmem + (tile & 1u) * PX_N;
     const int left = lim - (u0 + j) * PX_N;  // positions of the unit that the row attends to
-    if (!warp_wait(&sm.unit[tile % PX_TILES], tile / PX_TILES & 1u, &sm.failed)) return false;
-    if (!warp_wait(&sm.s_full[tile & 1u], tile >> 1 & 1u, &sm.failed)) return false;
+    if (!warp_wait(&sm.unit[place], (tiles + j) / PX_TILES & 1u, &sm.failed)) return false;
+    if (!warp_wait(&sm.s_full[w][tile & 1u], tile >> 1 & 1u, &sm.failed)) return false;
     tc_fence_after();
     if (rows) {
-      const uint32_t live = sm.live[tile % PX_TILES];
-      const bool whole = __all_sync(0xffffffffu, left >= PX_N && live == 15u);
-      const float *scale = &sm.scale[KIND == PG_E4M3 ? tile % PX_TILES : 0][0][0];  // E4M3: of K, V, log2 of V's
-      // 32 positions at a time, twice over, in loops: most blocks come here a few times only, and code that is not there yet
-      // costs more than reading the scores again
-      const auto scores = [&](int c, float(&s)[32]) {
-        tmem_ld32(t_s + c, s);
-        tmem_wait_ld();
-        if (KIND == PG_E4M3) {
+      const uint32_t live = sm.live[place];
+      const float *scale = &sm.scale[E4M3 ? place : 0][0][0];  // E4M3: of K, V, log2 of V's
+      float s[2][32];
+      tmem_ld32(t_s, s[0]);
+      tmem_ld32(t_s + 32, s[1]);
+      tmem_wait_ld();
+      if (E4M3) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] *= scale[c + e];
+        for (int e = 0; e < PX_N; e += 2) {
+          const float2 k = *reinterpret_cast<const float2 *>(scale + (E4M3 ? e : 0));
+          const float2 f = both(mul2(two(s[e / 32][e % 32], s[e / 32][e % 32 + 1]), two(k.x, k.y)));
+          s[e / 32][e % 32] = f.x, s[e / 32][e % 32 + 1] = f.y;
         }
-        if (!whole) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c + e >= left || !(live >> ((c + e) >> 4) & 1u)) s[e] = -INFINITY;
-        }
-      };
-      float top = -INFINITY;
-#pragma unroll 1
-      for (int c = 0; c < PX_N; c += 32) {
-        float s[32];
-        scores(c, s);
-#pragma unroll
-        for (int e = 0; e < 32; ++e) top = fmaxf(top, KIND == PG_E4M3 ? fmaf(s[e], rs, scale[2 * PX_N + c + e]) : s[e]);
       }
-      if (KIND != PG_E4M3) top *= rs;
+      if (!__all_sync(0xffffffffu, left >= PX_N && live == 15u)) {
+#pragma unroll
+        for (int e = 0; e < PX_N; ++e)
+          if (e >= left || !(live >> (e / 16) & 1u)) s[e / 32][e % 32] = -INFINITY;
+      }
+      const Two rs2 = two(rs, rs);
+      float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < PX_N; e += 2) {
+        float2 f = make_float2(s[e / 32][e % 32], s[e / 32][e % 32 + 1]);
+        if (E4M3) {
+          const float2 ls = *reinterpret_cast<const float2 *>(scale + (E4M3 ? 2 * PX_N + e : 0));
+          f = both(fma2(two(f.x, f.y), rs2, two(ls.x, ls.y)));
+        }
+        tops[e / 2 & 3] = fmaxf(tops[e / 2 & 3], fmaxf(f.x, f.y));
+      }
+      float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+      if (!E4M3) top *= rs;
       const bool far = top > m + P_STEP;
       if (__any_sync(0xffffffffu, far)) {
         const float mn = far ? top : m, f = far && m != -INFINITY ? ex2(m - mn) : 1.f;
         m = mn;
         l *= f;
         if (j > 0) {
-          if (!warp_wait(&sm.pv_done[(tile - 1) & 1u], (tile - 1) >> 1 & 1u, &sm.failed)) return false;
+          if (!warp_wait(&sm.pv_done[w][(tile - 1) & 1u], (tile - 1) >> 1 & 1u, &sm.failed)) return false;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < DH; c += 16) {
             float o[16];
             tmem_ld16(t_o + c, o);
-            uint32_t w[16];
+            uint32_t y[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[e] * f);
-            tmem_st16(t_o + c, w);
+            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(o[e] * f);
+            tmem_st16(t_o + c, y);
           }
         }
       }
       const float bias = P_BIAS - (m == -INFINITY ? 0.f : m);
-      float part[2] = {0.f, 0.f};
-#pragma unroll 1
-      for (int c = 0; c < PX_N; c += 32) {
-        float s[32];
-        scores(c, s);
+      const Two bias2 = two(bias, bias), minus2 = two(-1.f, -1.f);
+      Two part[2] = {0, 0};
 #pragma unroll
-        for (int k = 0; k < 32; k += 16) {  // the weights of 16 positions: eight columns of first parts, eight of second ones
-          uint32_t w[16];
+      for (int c = 0; c < PX_N; c += 16) {  // the weights of 16 positions: eight columns of first parts, eight of second ones
+        uint32_t y[16];
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float y[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              y[i] = ex2(fmaf(s[k + e + i], rs, bias));
-              part[i] += y[i];
-              if (KIND == PG_E4M3) y[i] *= scale[PX_N + c + k + e + i];
-            }
-            const uint32_t hi = pack16<KIND>(y[0], y[1]);
-            const float2 b = unpack16<KIND>(hi);
-            w[e / 2] = hi;
-            w[8 + e / 2] = pack16<KIND>(y[0] - b.x, y[1] - b.y);
+        for (int e = 0; e < 16; e += 2) {
+          const int at = c + e;
+          const float2 x = both(fma2(two(s[at / 32][at % 32], s[at / 32][at % 32 + 1]), rs2, bias2));
+          Two p = two(ex2(x.x), ex2(x.y));
+          part[e / 2 & 1] = add2(part[e / 2 & 1], p);
+          if (E4M3) {
+            const float2 vs = *reinterpret_cast<const float2 *>(scale + (E4M3 ? PX_N + at : 0));
+            p = mul2(p, two(vs.x, vs.y));
           }
-          tmem_st16(t_s + c + k, w);
+          const float2 f = both(p);
+          const uint32_t hi = pack16<KIND>(f.x, f.y);
+          const float2 b = unpack16<KIND>(hi);
+          const float2 lo = both(fma2(two(b.x, b.y), minus2, p));
+          y[e / 2] = hi;
+          y[8 + e / 2] = pack16<KIND>(lo.x, lo.y);
         }
+        tmem_st16(t_s + c, y);
       }
-      l += part[0] + part[1];
+      const float2 f = both(add2(part[0], part[1]));
+      l += f.x + f.y;
       tmem_wait_st();
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.p_full[tile & 1u]);
+    if (lane == 0) mbar_arrive(&sm.p_full[w][tile & 1u]);
   }
-  if (n > 0 && !warp_wait(&sm.pv_done[(tiles + n - 1) & 1u], (tiles + n - 1) >> 1 & 1u, &sm.failed)) return false;
+  if (n > 0 && !warp_wait(&sm.pv_done[w][(units + n - 1) & 1u], (units + n - 1) >> 1 & 1u, &sm.failed)) return false;
   *m_out = m;
   *l_out = l;
   return true;
@@ -702,7 +746,8 @@ __device__ __forceinline__ bool soften_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_
 
 // The rows of queries of an item, in the layout of an MMA operand, by every warp but the loader.
 template <int KIND, int DH, bool SPLIT>
-__device__ __forceinline__ void stage_queries(const PrefixArgs &a, PxSmem<KIND, DH, SPLIT> &sm, int first, int h, int group, int rows) {
+__device__ __forceinline__ void stage_queries(const PrefixArgs &a, PxSmem<KIND, DH, SPLIT> &sm, int first, int h, int group, int rows0,
+                                              int rows) {
   constexpr int KB = DH / 64, E = DH / 32, AHEAD = 4, WARPS = PX_THREADS / 32 - 1, CH = DH / 8;
   const int w = threadIdx.x >> 5, warp = w < PX_LOADER ? w : w - 1, lane = threadIdx.x & 31;
   const bool bf16_q = a.q_dtype == KIE_BF16;
@@ -710,13 +755,13 @@ __device__ __forceinline__ void stage_queries(const PrefixArgs &a, PxSmem<KIND, 
   const uintptr_t odd = (uintptr_t)a.q | (uintptr_t)(a.q_stride[0] * size) | (uintptr_t)(a.q_stride[1] * size);
   if (!SPLIT && !(KIND == PG_E4M3 && bf16_q) && a.scale > 0.f && odd % 16 == 0) {  // as they are, 16 bytes at a time
     if (lane == 0)
-      for (int r = warp; r < rows; r += WARPS) sm.rs[r] = fmaxf(a.scale, FLT_MIN) * LOG2E;
+      for (int r = warp; r < rows; r += WARPS) sm.rs[r >= rows0][r >= rows0 ? r - rows0 : r] = fmaxf(a.scale, FLT_MIN) * LOG2E;
     const uint16_t *q = static_cast<const uint16_t *>(a.q) + (int64_t)first * a.q_stride[0] + (int64_t)h * group * a.q_stride[1];
 #pragma unroll 4
     for (int i = warp * 32 + lane; i < rows * CH; i += 32 * WARPS) {
-      const int r = i / CH, c = i % CH;
+      const int r = i / CH, c = i % CH, w = r >= rows0, at = w ? r - rows0 : r;  // rows from rows0 on are the second half's
       const uint4 x = *reinterpret_cast<const uint4 *>(q + r / group * a.q_stride[0] + r % group * a.q_stride[1] + c * 8);
-      *reinterpret_cast<uint4 *>(sm.q + (c >> 3) * (PX_M * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
+      *reinterpret_cast<uint4 *>(sm.q[w] + (c >> 3) * (PX_M * 128) + at * 128 + (((c & 7) ^ (at & 7)) << 4)) = x;
     }
     return;
   }
@@ -758,7 +803,8 @@ __device__ __forceinline__ void stage_queries(const PrefixArgs &a, PxSmem<KIND, 
         up *= __int_as_float((127 + e2) << 23);
         rs *= __int_as_float((127 - e2) << 23);
       }
-      if (lane == 0) sm.rs[r] = rs;
+      const int half = r >= rows0, place = half ? r - rows0 : r;
+      if (lane == 0) sm.rs[half][place] = rs;
       uint32_t hi[E / 2], lo[E / 2];
 #pragma unroll
       for (int e = 0; e < E / 2; ++e) {
@@ -785,7 +831,7 @@ __device__ __forceinline__ void stage_queries(const PrefixArgs &a, PxSmem<KIND, 
         }
       }
       const int byte = lane * E * 2;  // of the row; 128 bytes to a block
-      uint8_t *to = sm.q + (byte >> 7) * (PX_M * 128) + r * 128 + ((((byte >> 4) & 7) ^ (r & 7)) << 4) + (byte & 15);
+      uint8_t *to = sm.q[half] + (byte >> 7) * (PX_M * 128) + place * 128 + ((((byte >> 4) & 7) ^ (place & 7)) << 4) + (byte & 15);
 #pragma unroll
       for (int p = 0; p < (SPLIT ? 2 : 1); ++p) {
         const uint32_t(&y)[E / 2] = p ? lo : hi;
@@ -799,7 +845,7 @@ __device__ __forceinline__ void stage_queries(const PrefixArgs &a, PxSmem<KIND, 
 }
 
 template <int KIND, int DH, bool SPLIT>
-__global__ void __launch_bounds__(PX_THREADS, PxShape<KIND, DH, SPLIT>::BLOCKS)
+__global__ void __maxnreg__(PX_REGISTERS)
 prefix_kernel(const PrefixArgs a, const __grid_constant__ PrefixMaps maps) {
   using T = PxShape<KIND, DH, SPLIT>;
   using Sm = PxSmem<KIND, DH, SPLIT>;
@@ -807,12 +853,13 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ PrefixMaps maps) {
   extern __shared__ __align__(1024) uint8_t px_raw[];
   Sm &sm = *reinterpret_cast<Sm *>(px_raw);
   const int tid = threadIdx.x, warp = tid >> 5;
-  const int heads = a.pages.n_kv_heads, group = a.n_heads / heads, members = PX_M / group;
+  const int heads = a.pages.n_kv_heads, group = a.n_heads / heads, members = 2 * (PX_M / group);
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) mbar_init(&sm.full[i], KIND == PG_E4M3 ? PX_CONVERTERS : 1), mbar_init(&sm.empty[i], 1);
     for (int i = 0; i < T::RAW; ++i) mbar_init(&sm.raw_full[i], 1), mbar_init(&sm.raw_empty[i], PX_CONVERTERS);
     for (int i = 0; i < PX_TILES; ++i) mbar_init(&sm.unit[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&sm.s_full[i], 1), mbar_init(&sm.p_full[i], PX_SOFT), mbar_init(&sm.pv_done[i], 1);
+    for (int i = 0; i < 4; ++i)
+      mbar_init(&sm.s_full[i / 2][i % 2], 1), mbar_init(&sm.p_full[i / 2][i % 2], PX_SOFT), mbar_init(&sm.pv_done[i / 2][i % 2], 1);
     mbar_init(&sm.fix, 1);
     fence_barrier_init();
     sm.failed = 0;
@@ -832,63 +879,69 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ PrefixMaps maps) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem, t_o = tmem + 2 * PX_N;
-  const uint32_t my_lanes = (uint32_t)((warp & 3) * 32) << 16;
+  const uint32_t tmem = sm.tmem;
+  const int part = warp / PX_SOFT, in_part = tid % PX_M;  // of the softmax's threads: the half of the tile, and the row there
+  const uint32_t my_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16) + part * (PX_TMEM / 2), t_o = my_tmem + 2 * PX_N;
 
-  uint32_t tiles = 0, halves = 0, fixes = 0;  // units of all items so far; halves of them (K or V) in the ring; mended halves
+  // units of all items so far; of those that had rows in each half of the tile; halves (K or V) in the ring; mended halves
+  uint32_t tiles = 0, units[2] = {0, 0}, halves = 0, fixes = 0;
   int g = begin.g, item = begin.item;  // the item is the group's item-th: tile * heads + head
   Group x = group_of(a, g, begin.start, begin.end);
   long long place = begin.place;
   for (;;) {
     // ---- an item, or this block's part of it: units [u0, u1)
     const int t = item / heads, h = item % heads, first = x.start + t * members;
-    const int rows = min(members, x.end - first) * group;
+    const int rows = min(members, x.end - first) * group, rows0 = min(rows, members / 2 * group);
     const int u0 = (int)max(0ll, v0 - place - PX_ITEM_COST), u1 = (int)min((long long)x.units, v1 - place - PX_ITEM_COST);
     if (u1 > u0) {
       int n;
       if (warp == PX_LOADER) {
         n = load_item<KIND, DH, SPLIT>(a, maps, sm, x, h, u0, u1, tiles, halves, fixes);
       } else {
-        const int lim = tid < rows ? min(x.prefix, length_of(a, first + tid / group)) : 0;
-        stage_queries<KIND, DH, SPLIT>(a, sm, first, h, group, rows);
+        const int mine = part < 2 && in_part < (part ? rows - rows0 : rows0) ? in_part + part * rows0 : -1;  // the row, of the tile
+        const int lim = mine >= 0 ? min(x.prefix, length_of(a, first + mine / group)) : 0;
+        stage_queries<KIND, DH, SPLIT>(a, sm, first, h, group, rows0, rows);
         fence_async_proxy();
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("bar.sync 1, 384;" ::: "memory");
         const int reach = sm.reach;
         n = max(0, min(u1, (reach + PX_N - 1) / PX_N) - u0);
         if (warp == PX_ISSUER) {
-          multiply_item<KIND, DH, SPLIT>(sm, tmem, n, tiles, halves);
-        } else if (warp >= PX_SOFT) {
+          multiply_item<KIND, DH, SPLIT>(sm, tmem, rows > rows0 ? 2 : 1, n, units, halves);
+        } else if (part >= 2) {
           if constexpr (KIND == PG_E4M3) convert_item<KIND, DH, SPLIT>(sm, tid - 32 * PX_CONVERT, reach, u0, n, halves);
-        } else {
+        } else if (part == 0 || rows > rows0) {
           float m = -INFINITY, l = 0.f;
-          const bool ok = soften_item<KIND, DH, SPLIT>(sm, tmem + my_lanes, tid, warp * 32 < rows, lim, u0, n, tiles, &m, &l);
+          const bool some = __any_sync(0xffffffffu, mine >= 0);
+          const bool ok = soften_item<KIND, DH, SPLIT>(sm, my_tmem, part, in_part, some, lim, u0, n, tiles, part ? units[1] : units[0], &m, &l);
           // the piece: eight dimensions of a row at a time, rows side by side
-          const int64_t slot = (int64_t)first * a.n_heads + h * rows + (int64_t)PX_M * blockIdx.x;
-          float *to = a.prefix + slot * DH + 8 * tid;
+          const int64_t slot = (int64_t)first * a.n_heads + h * rows + (int64_t)PX_TILE * blockIdx.x;
+          float *to = a.prefix + slot * DH + 8 * mine;
           tc_fence_after();
-          if (warp * 32 < rows) {
+          if (some) {
 #pragma unroll 1
             for (int c = 0; c < DH; c += 32) {
               float o[32];
               if (ok && n > 0) {
-                tmem_ld32(t_o + my_lanes + c, o);
+                tmem_ld32(t_o + c, o);
                 tmem_wait_ld();
               } else {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = 0.f;
               }
-              if (tid < rows) {
+              if (mine >= 0) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) store8(to + (int64_t)(c + e) * rows, &o[e]);
               }
             }
           }
           // a wait that ran out shows as NaN in every result that it concerns
-          if (tid < rows) a.prefix_ml[slot + tid] = make_float2(ok ? m - P_BIAS : 0.f, ok ? l : __int_as_float(0x7fc00000));
+          if (mine >= 0) a.prefix_ml[slot + mine] = make_float2(ok ? m - P_BIAS : 0.f, ok ? l : __int_as_float(0x7fc00000));
           tc_fence_before();
         }
       }
       tiles += n;
+      units[0] += n;
+      if (rows > rows0) units[1] += n;
       halves += 2 * n;
       __syncthreads();
       tc_fence_after();
@@ -961,10 +1014,7 @@ cudaError_t launch(const PrefixArgs &a, int dev, int sms, cudaStream_t stream) {
   if (!make_map(&maps.k, &maps.order[0], a.pages, false, maps.rows) || !make_map(&maps.v, &maps.order[1], a.pages, true, maps.rows))
     return cudaErrorInvalidPitchValue;
   static std::atomic<uint64_t> ready{0};  // devices whose limit of dynamic shared memory is raised
-  using T = PxShape<KIND, DH, SPLIT>;
-  static_assert(T::BLOCKS == 1 || sizeof(PxSmem<KIND, DH, SPLIT>) <= 115712, "two blocks' shared memory");
-  // no more than T::BLOCKS to an SM: a third one's TMEM would have to wait
-  const int smem = (int)std::max<size_t>(sizeof(PxSmem<KIND, DH, SPLIT>), 80 * 1024);
+  const int smem = (int)sizeof(PxSmem<KIND, DH, SPLIT>);
   const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
   if (!bit || !(ready.load(std::memory_order_relaxed) & bit)) {
     const cudaError_t e =
@@ -1005,7 +1055,7 @@ __global__ void __launch_bounds__(PJ_THREADS) join_kernel(const PrefixArgs a) {
     const long long place = row.place + (long long)h * (row.units + PX_ITEM_COST) + PX_ITEM_COST;
     const auto block_of = [&](long long v) { return (int)((v | per) >> 32 ? v / per : (unsigned)v / (unsigned)per); };
     const int first = block_of(place), n = block_of(place + row.units - 1) - first + 1;
-    const int64_t slot = row.slot + (int64_t)h * row.rows + (int64_t)PX_M * first;
+    const int64_t slot = row.slot + (int64_t)h * row.rows + (int64_t)PX_TILE * first;
     const int r = row.local + head - h * group;
     const float *o = a.prefix + slot * DH + (int64_t)(d >> 3) * row.rows * 8 + r * 8 + (d & 7);
     const float2 *ml = a.prefix_ml + slot + r;
@@ -1016,8 +1066,8 @@ __global__ void __launch_bounds__(PJ_THREADS) join_kernel(const PrefixArgs a) {
 #pragma unroll
       for (int k = 0; k < BATCH; ++k) {
         const int64_t i = min(i0 + k, n - 1);
-        w[k] = __ldcg(ml + PX_M * i);
-        y[k] = __ldcg(reinterpret_cast<const float4 *>(o + PX_M * DH * i));
+        w[k] = __ldcg(ml + PX_TILE * i);
+        y[k] = __ldcg(reinterpret_cast<const float4 *>(o + PX_TILE * DH * i));
       }
       float mn = M;
 #pragma unroll
@@ -1059,7 +1109,7 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 struct Parts {
   size_t per_block, blocks, row_lo, rows, prefix_ml, own_ml, own, prefix, all;
   Parts(int n_seqs, int n_heads, int n_kv_heads, int head_dim, int sms) {
-    const size_t heads = (size_t)n_seqs * n_heads, slots = heads + (size_t)PX_M * sms;
+    const size_t heads = (size_t)n_seqs * n_heads, slots = heads + (size_t)PX_TILE * sms;
     per_block = up256(kie_paged_attention_workspace_bytes(n_heads, n_kv_heads, head_dim, sms));
     blocks = per_block + 256;
     row_lo = up256(blocks + sms * sizeof(PrefixBlock));

@@ -29,9 +29,9 @@ namespace kie {
 namespace {
 
 constexpr int PX_M = 128, PX_N = 64;       // rows of a half of a tile (an MMA's), positions of a unit
-// Warps: four of the softmax for each half of a tile, the loader, two that convert codes, the one that issues the MMAs.
-constexpr int PX_SOFT = 4, PX_LOADER = 8, PX_CONVERT = 9, PX_CONVERTERS = 2, PX_ISSUER = 11;
-constexpr int PX_THREADS = 384;
+// Warps: four of the softmax for each half of a tile, the loaders of K and of V, one that issues the MMAs of each half, and
+// where the cache holds codes those that convert them.
+constexpr int PX_SOFT = 4, PX_LOADER = 8, PX_ISSUER = 10, PX_CONVERT = 12, PX_CONVERTERS = 4;
 // Registers of a thread: what the rows' own attention leaves of an SM with a block of its own there.
 constexpr int PX_REGISTERS = 112;
 // Depth of what is kept per unit besides K and V. The loader is at most NS + RAW <= 6 halves ahead of the oldest one in use,
@@ -50,6 +50,7 @@ struct PxShape {
   static constexpr int Q_HALF = PX_M * DH * 2 * (SPLIT ? 2 : 1), SLOT = PX_N * DH * 2, CODES = PX_N * DH;
   static constexpr int NS = KIND == PG_E4M3 ? 3 : 5;     // ring slots
   static constexpr int RAW = KIND == PG_E4M3 ? 3 : 1;  // of codes as they come
+  static constexpr int THREADS = 32 * (PX_CONVERT + (KIND == PG_E4M3 ? PX_CONVERTERS : 0));
 };
 
 template <int KIND, int DH, bool SPLIT>
@@ -366,7 +367,11 @@ struct Half {
   __device__ __forceinline__ explicit Half(uint32_t i) : slot(i % NS), round(i / NS & 1u) {}
 };
 
-// Half i of n units: its unit, and whether it is V.
+// The halves of n units come as K0 K1 V0 K2 V1 ...: where K or V of unit u comes,
+__device__ __forceinline__ int half_of(int u, int n, bool is_v) {
+  return is_v ? min(2 * u + 2, 2 * n - 1) : max(2 * u - 1, 0);
+}
+// and of half i its unit, and whether it is V.
 __device__ __forceinline__ int unit_of(int i, int n, bool *is_v) {
   if (i == 0) return *is_v = false, 0;
   if (i == 2 * n - 1) return *is_v = true, n - 1;
@@ -374,11 +379,11 @@ __device__ __forceinline__ int unit_of(int i, int n, bool *is_v) {
   return (i & 1) ? (i + 1) / 2 : i / 2 - 1;
 }
 
-// One warp. Finds the group's longest row (the first of them), through whose table row the prefix is read, and loads, without
+// The warp that loads K, or V. Finds the group's longest row (the first of them), through whose table row the prefix is read, and loads, without
 // waiting for the queries. Returns the number of units, all of them with positions.
 template <int KIND, int DH, bool SPLIT>
 __device__ __forceinline__ int load_item(const PrefixArgs &a, const PrefixMaps &maps, PxSmem<KIND, DH, SPLIT> &sm, const Group &x,
-                                         int h, int u0, int u1, uint32_t tiles, uint32_t halves, uint32_t &fixes) {
+                                         bool is_v, int h, int u0, int u1, uint32_t tiles, uint32_t halves, uint32_t &fixes) {
   using T = PxShape<KIND, DH, SPLIT>;
   constexpr bool CODES = KIND == PG_E4M3;
   constexpr int NS = CODES ? T::RAW : T::NS, KB = CODES ? 1 : DH / 64;
@@ -393,8 +398,8 @@ __device__ __forceinline__ int load_item(const PrefixArgs &a, const PrefixMaps &
   const int mine = reach;
   reach = __reduce_max_sync(0xffffffffu, reach);
   source = __reduce_min_sync(0xffffffffu, mine == reach ? source : INT_MAX);
-  if (lane == 0) sm.reach = reach;
-  asm volatile("bar.arrive 1, 384;" ::: "memory");  // the others, once the queries are there
+  if (lane == 0 && !is_v) sm.reach = reach;
+  asm volatile("bar.arrive 1, %0;" ::"n"(T::THREADS) : "memory");  // the others, once the queries are there
   const int n = max(0, min(u1, (reach + PX_N - 1) / PX_N) - u0);
   const int *pages = a.block_table + (n > 0 ? sequence_of(a, source) : 0) * a.table_stride;
   const unsigned bs = a.pages.block_size;
@@ -413,7 +418,6 @@ __device__ __forceinline__ int load_item(const PrefixArgs &a, const PrefixMaps &
   const int runs = PX_N / maps.rows;  // boxes of maps.rows positions by 128 bytes
   uint64_t *const full = CODES ? sm.raw_full : sm.full, *const empty = CODES ? sm.raw_empty : sm.empty;
   const uint32_t ring = smem_u32(CODES ? &sm.raw[0][0] : &sm.ring[0][0]);
-  int page0 = -1, at0 = 0, page1 = -1, at1 = 0;  // lane i: run i of the last even and the last odd unit, for their V
   float ks[2], vs[2];         // E4M3: the next unit's scales, positions lane and lane + 32
   const auto request_scales = [&](int unit) {
 #pragma unroll
@@ -433,37 +437,26 @@ __device__ __forceinline__ int load_item(const PrefixArgs &a, const PrefixMaps &
     page_a = page_b, at_a = at_b;
     fetch(batch + 8, &page_b, &at_b);
   };
-  if (CODES && n > 0) request_scales(u0);
-  const auto load = [&](int i) {
-    bool is_v;
-    const int u = unit_of(i, n, &is_v), unit = u0 + u;
-    const uint32_t half = halves + i, slot = half % NS;
+  if (CODES && !is_v && n > 0) request_scales(u0);
+  const CUtensorMap *const map = is_v ? &maps.v : &maps.k;
+  const int order = maps.order[is_v];
+  const auto load = [&](int u) {
+    const int unit = u0 + u;
+    const uint32_t half = halves + half_of(u, n, is_v), slot = half % NS;
+    turn_to(unit);
+    const uint32_t live = __ballot_sync(0xffffffffu, page_a >= 0) >> ((unit - batch) * 4) & 15u;
     if (!warp_wait(&empty[slot], (half / NS & 1u) ^ 1u, &sm.failed)) return false;
-    int page = u & 1 ? page1 : page0, at = u & 1 ? at1 : at0;
-    uint32_t live = 0;
-    if (!is_v) {
-      turn_to(unit);
-      live = __ballot_sync(0xffffffffu, page_a >= 0) >> ((unit - batch) * 4) & 15u;
-      const int from = (unit - batch) * 4 + lane * (maps.rows >> 4);
-      page = __shfl_sync(0xffffffffu, page_a, from & 31);
-      at = __shfl_sync(0xffffffffu, at_a, from & 31);
-      if (u & 1)
-        page1 = page, at1 = at;
-      else
-        page0 = page, at0 = at;
-    }
     // rows of V behind the end would meet weights of 0 as whatever they hold: they become zeros before the MMA may begin
     const int tail = reach - unit * PX_N;
     const bool mend = !CODES && is_v && tail < PX_N;
     uint64_t *const bar = mend ? &sm.fix : &full[slot];
-    const CUtensorMap *const map = is_v ? &maps.v : &maps.k;
-    const int order = maps.order[is_v];
     const bool one = elect_one();
     if (one) mbar_arrive_expect_tx(bar, BYTES);
     uint32_t to = ring + slot * BYTES;
 #pragma unroll 1
     for (int run = 0; run < runs; ++run, to += maps.rows * (CODES ? DH : 128)) {
-      const int p = __shfl_sync(0xffffffffu, page, run), y = __shfl_sync(0xffffffffu, at, run);
+      const int from = (unit - batch) * 4 + run * (maps.rows >> 4);
+      const int p = __shfl_sync(0xffffffffu, page_a, from), y = __shfl_sync(0xffffffffu, at_a, from);
       const int z = p >= 0 ? p : a.pages.n_blocks;
       const auto coordinate = [&](int what) { return (what & 3) == 0 ? y : (what & 3) == 1 ? h : z; };
       if (one) {
@@ -506,8 +499,8 @@ __device__ __forceinline__ int load_item(const PrefixArgs &a, const PrefixMaps &
     return true;
   };
 #pragma unroll 1
-  for (int i = 0; i < 2 * n; ++i)
-    if (!load(i)) break;
+  for (int u = 0; u < n; ++u)
+    if (!load(u)) break;
   return n;
 }
 
@@ -544,64 +537,58 @@ __device__ __forceinline__ void convert_item(PxSmem<KIND, DH, SPLIT> &sm, int ct
   }
 }
 
-// One warp, an elected lane of which issues. parts: halves of the tile that have rows.
+// The warp that issues for half w of a tile, an elected lane of which does. parts: halves of the tile that have rows.
 template <int KIND, int DH, bool SPLIT>
-__device__ __forceinline__ void multiply_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_t tmem, int parts, int n,
-                                              const uint32_t (&units)[2], uint32_t halves) {
+__device__ __forceinline__ void multiply_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_t tmem, int w, int parts, int n,
+                                              uint32_t units, uint32_t halves) {
   using T = PxShape<KIND, DH, SPLIT>;
   constexpr int NS = T::NS, KB = DH / 64;
   constexpr uint32_t S_DESC = px_idesc(PX_N, KIND == PG_BF16, false), O_DESC = px_idesc(DH, KIND == PG_BF16, true);
   // descriptors of the first step; those of the others are 16-byte units further (addresses stay below 2^18)
-  const uint64_t q0 = px_desc(smem_u32(sm.q), 16), k0 = px_desc(smem_u32(sm.ring), 16), v0 = px_desc(smem_u32(sm.ring), PX_N * 128);
-  constexpr uint32_t SLOT = T::SLOT / 16, Q_HALF = T::Q_HALF / 16;
+  const uint64_t q0 = px_desc(smem_u32(sm.q[w]), 16), k0 = px_desc(smem_u32(sm.ring), 16), v0 = px_desc(smem_u32(sm.ring), PX_N * 128);
+  constexpr uint32_t SLOT = T::SLOT / 16;
   uint32_t half = halves;
 #pragma unroll 1
   for (int j = 0; j <= n; ++j) {
     if (j < n) {  // S = Q K^T
-      const Half<NS> x(half);
+      const Half<NS> x(half++);
+      const uint32_t tile = units + j, buf = tile & 1u;
       if (!warp_wait(&sm.full[x.slot], x.round, &sm.failed)) return;
-#pragma unroll 1
-      for (int w = 0; w < parts; ++w) {
-        const uint32_t tile = (w ? units[1] : units[0]) + j, buf = tile & 1u;
-        if (j >= 2 && !warp_wait(&sm.pv_done[w][buf], (tile - 2) >> 1 & 1u, &sm.failed)) return;  // unit j - 2 is done with it
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t k = k0 + x.slot * SLOT, q = q0 + w * Q_HALF;
-          const uint32_t to = tmem + w * (PX_TMEM / 2) + buf * PX_N;
+      if (j >= 2 && !warp_wait(&sm.pv_done[w][buf], (tile - 2) >> 1 & 1u, &sm.failed)) return;  // unit j - 2 is done with it
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t k = k0 + x.slot * SLOT;
+        const uint32_t to = tmem + buf * PX_N;
 #pragma unroll
-          for (int p = 0; p < (SPLIT ? 2 : 1); ++p)
+        for (int p = 0; p < (SPLIT ? 2 : 1); ++p)
 #pragma unroll
-            for (int s = 0; s < DH / 16; ++s)
-              tc_mma(to, q + (p * KB + s / 4) * (PX_M * 8) + s % 4 * 2, k + s / 4 * (PX_N * 8) + s % 4 * 2, S_DESC, p || s ? 1u : 0u);
-          if (w == parts - 1) tc_commit(&sm.empty[x.slot]);
-          tc_commit(&sm.s_full[w][buf]);
-        }
-        __syncwarp();
+          for (int s = 0; s < DH / 16; ++s)
+            tc_mma(to, q0 + (p * KB + s / 4) * (PX_M * 8) + s % 4 * 2, k + s / 4 * (PX_N * 8) + s % 4 * 2, S_DESC, p || s ? 1u : 0u);
+        tc_commit(&sm.s_full[w][buf]);
+        tc_commit(&sm.empty[x.slot]);
+        if (parts == 1) tc_commit(&sm.empty[x.slot]);
       }
-      ++half;
+      __syncwarp();
     }
     if (j > 0) {  // O += P V
-      const Half<NS> x(half);
+      const Half<NS> x(half++);
+      const uint32_t tile = units + j - 1, buf = tile & 1u;
       if (!warp_wait(&sm.full[x.slot], x.round, &sm.failed)) return;
-#pragma unroll 1
-      for (int w = 0; w < parts; ++w) {
-        const uint32_t tile = (w ? units[1] : units[0]) + j - 1, buf = tile & 1u;
-        if (!warp_wait(&sm.p_full[w][buf], tile >> 1 & 1u, &sm.failed)) return;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t v = v0 + x.slot * SLOT;
-          const uint32_t to = tmem + w * (PX_TMEM / 2), p = to + buf * PX_N;
+      if (!warp_wait(&sm.p_full[w][buf], tile >> 1 & 1u, &sm.failed)) return;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t v = v0 + x.slot * SLOT;
+        const uint32_t to = tmem + 2 * PX_N, p = tmem + buf * PX_N;
 #pragma unroll
-          for (int s = 0; s < PX_N / 16; ++s)
+        for (int s = 0; s < PX_N / 16; ++s)
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
-              tc_mma_ts(to + 2 * PX_N, p + s * 16 + part * 8, v + s * 128, O_DESC, j > 1 || s || part ? 1u : 0u);
-          if (w == parts - 1) tc_commit(&sm.empty[x.slot]);
-          tc_commit(&sm.pv_done[w][buf]);
-        }
-        __syncwarp();
+          for (int part = 0; part < 2; ++part)
+            tc_mma_ts(to, p + s * 16 + part * 8, v + s * 128, O_DESC, j > 1 || s || part ? 1u : 0u);
+        tc_commit(&sm.pv_done[w][buf]);
+        tc_commit(&sm.empty[x.slot]);
+        if (parts == 1) tc_commit(&sm.empty[x.slot]);
       }
-      ++half;
+      __syncwarp();
     }
   }
 }
@@ -744,12 +731,12 @@ __device__ __forceinline__ bool soften_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_
 
 // ---- the kernel ----------------------------------------------------------------------------------------------
 
-// The rows of queries of an item, in the layout of an MMA operand, by every warp but the loader.
+// The rows of queries of an item, in the layout of an MMA operand, by every warp but the loaders.
 template <int KIND, int DH, bool SPLIT>
 __device__ __forceinline__ void stage_queries(const PrefixArgs &a, PxSmem<KIND, DH, SPLIT> &sm, int first, int h, int group, int rows0,
                                               int rows) {
-  constexpr int KB = DH / 64, E = DH / 32, AHEAD = 4, WARPS = PX_THREADS / 32 - 1, CH = DH / 8;
-  const int w = threadIdx.x >> 5, warp = w < PX_LOADER ? w : w - 1, lane = threadIdx.x & 31;
+  constexpr int KB = DH / 64, E = DH / 32, AHEAD = 4, WARPS = PxShape<KIND, DH, SPLIT>::THREADS / 32 - 2, CH = DH / 8;
+  const int w = threadIdx.x >> 5, warp = w < PX_LOADER ? w : w - 2, lane = threadIdx.x & 31;
   const bool bf16_q = a.q_dtype == KIE_BF16;
   const int size = paged_dtype_bytes(a.q_dtype);
   const uintptr_t odd = (uintptr_t)a.q | (uintptr_t)(a.q_stride[0] * size) | (uintptr_t)(a.q_stride[1] * size);
@@ -855,7 +842,7 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ PrefixMaps maps) {
   const int tid = threadIdx.x, warp = tid >> 5;
   const int heads = a.pages.n_kv_heads, group = a.n_heads / heads, members = 2 * (PX_M / group);
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) mbar_init(&sm.full[i], KIND == PG_E4M3 ? PX_CONVERTERS : 1), mbar_init(&sm.empty[i], 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&sm.full[i], KIND == PG_E4M3 ? PX_CONVERTERS : 1), mbar_init(&sm.empty[i], 2);
     for (int i = 0; i < T::RAW; ++i) mbar_init(&sm.raw_full[i], 1), mbar_init(&sm.raw_empty[i], PX_CONVERTERS);
     for (int i = 0; i < PX_TILES; ++i) mbar_init(&sm.unit[i], 1);
     for (int i = 0; i < 4; ++i)
@@ -895,18 +882,20 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ PrefixMaps maps) {
     const int u0 = (int)max(0ll, v0 - place - PX_ITEM_COST), u1 = (int)min((long long)x.units, v1 - place - PX_ITEM_COST);
     if (u1 > u0) {
       int n;
-      if (warp == PX_LOADER) {
-        n = load_item<KIND, DH, SPLIT>(a, maps, sm, x, h, u0, u1, tiles, halves, fixes);
+      if (warp == PX_LOADER || warp == PX_LOADER + 1) {
+        n = load_item<KIND, DH, SPLIT>(a, maps, sm, x, warp != PX_LOADER, h, u0, u1, tiles, halves, fixes);
       } else {
         const int mine = part < 2 && in_part < (part ? rows - rows0 : rows0) ? in_part + part * rows0 : -1;  // the row, of the tile
         const int lim = mine >= 0 ? min(x.prefix, length_of(a, first + mine / group)) : 0;
         stage_queries<KIND, DH, SPLIT>(a, sm, first, h, group, rows0, rows);
         fence_async_proxy();
-        asm volatile("bar.sync 1, 384;" ::: "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(T::THREADS) : "memory");
         const int reach = sm.reach;
         n = max(0, min(u1, (reach + PX_N - 1) / PX_N) - u0);
-        if (warp == PX_ISSUER) {
-          multiply_item<KIND, DH, SPLIT>(sm, tmem, rows > rows0 ? 2 : 1, n, units, halves);
+        if (warp == PX_ISSUER || warp == PX_ISSUER + 1) {
+          const int w = warp - PX_ISSUER;
+          if (w == 0 || rows > rows0)
+            multiply_item<KIND, DH, SPLIT>(sm, tmem + w * (PX_TMEM / 2), w, rows > rows0 ? 2 : 1, n, w ? units[1] : units[0], halves);
         } else if (part >= 2) {
           if constexpr (KIND == PG_E4M3) convert_item<KIND, DH, SPLIT>(sm, tid - 32 * PX_CONVERT, reach, u0, n, halves);
         } else if (part == 0 || rows > rows0) {
@@ -1022,7 +1011,7 @@ cudaError_t launch(const PrefixArgs &a, int dev, int sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready.fetch_or(bit, std::memory_order_relaxed);
   }
-  return launch_after_previous(prefix_kernel<KIND, DH, SPLIT>, sms, PX_THREADS, smem, stream, a, maps);
+  return launch_after_previous(prefix_kernel<KIND, DH, SPLIT>, sms, PxShape<KIND, DH, SPLIT>::THREADS, smem, stream, a, maps);
 }
 
 template <int DH>

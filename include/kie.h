@@ -124,6 +124,13 @@ int kie_sync(kie_ctx *ctx);
  * Requires a prior prefill. */
 int kie_decode_forced(kie_ctx *ctx, int n, const int32_t *forced, int32_t *out_tokens, float *out_logits);
 
+/* Scores a given continuation: for each of the n host tokens, what kie_token_logprobs (below) reads off the logits before
+ * it, those after all tokens ahead of it; then the sequence has taken all n in, as if kie_decode had emitted them.
+ * logprob [n] and, if not NULL, entropy [n]; top_ids, top_logprobs [n][top], 0 <= top <= min(vocab, KIE_MAX_TOP), NULL if
+ * top is 0. The logits stay on the device. Host arrays, synchronous; requires a prior prefill. */
+int kie_decode_score(kie_ctx *ctx, int n, const int32_t *tokens, int top, float *logprob, float *entropy, int32_t *top_ids,
+                     float *top_logprobs);
+
 /* No counterpart on the pages: a testing aid for sparse-MoE models (below). The expert selection is itself a
  * floating-point decision (a top_k over router logits) that a CPU reference and the GPU take from logits rounded
  * differently; to compare every step, the reference's own selections can be imposed on the GPU.

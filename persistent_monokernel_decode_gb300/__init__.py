@@ -259,6 +259,7 @@ SIGNATURES = {
     "kie_decode_async": ([P, ctypes.c_int, P], ctypes.c_int),
     "kie_sync": ([P], ctypes.c_int),
     "kie_decode_forced": ([P, ctypes.c_int, P, P, P], ctypes.c_int),
+    "kie_decode_score": ([P, ctypes.c_int, P, ctypes.c_int, P, P, P, P], ctypes.c_int),
     "kie_decode_forced_routed": ([P, ctypes.c_int, P, P, P, P, P], ctypes.c_int),
     "kie_get_logits": ([P, P], ctypes.c_int),
     "kie_position": ([P], ctypes.c_int),
@@ -498,6 +499,19 @@ class Decoder:
                                               toks.ctypes.data, None if logits is None else logits.ctypes.data,
                                               None if own is None else own.ctypes.data), self.ctx)
         return toks, logits, own
+
+    def score(self, tokens, *, top: int = 0):
+        """The log probability of each of the given tokens after the sequence and the tokens ahead of it, the entropy of
+        the distribution that it is of, and its `top` most probable tokens: a TokenLogprobs of numpy arrays
+        (kie_decode_score). The sequence then goes on behind them."""
+        t = np.ascontiguousarray(tokens, dtype=np.int32).reshape(-1)
+        n, k = t.size, max(0, int(top))
+        out = TokenLogprobs(np.empty(n, np.float32), np.empty(n, np.float32), np.empty((n, k), np.int32),
+                            np.empty((n, k), np.float32))
+        _check(lib().kie_decode_score(self.ctx, n, t.ctypes.data, top, out.logprob.ctypes.data, out.entropy.ctypes.data,
+                                      out.top_ids.ctypes.data if k else None,
+                                      out.top_logprobs.ctypes.data if k else None), self.ctx)
+        return out
 
     def logits(self) -> np.ndarray:
         out = np.empty(self.model.vocab, dtype=np.float32)

@@ -56,7 +56,7 @@ struct ScratchLayout {
 
 struct WsLayout {
   ScratchLayout scr;  // at offset 0
-  size_t logits, rope, persist, trace, trace_arrive, stats, tok_in, tok_out, chunk, route_in, route_out, pf_x, pf_h,
+  size_t logits, rope, persist, trace, trace_arrive, stats, tok_in, tok_out, chunk, score, route_in, route_out, pf_x, pf_h,
       pf_q, pf_o, pf_a,
       pf_scale, pf_part, pf_tcb, pf_att_o, pf_att_ml, total;
   int smax;
@@ -212,6 +212,7 @@ const char *make_plan(const kie_config *c, const kie_moe_config *moe, int n_cta,
   s.tok_in = take((size_t)c->max_seq * 4);
   s.tok_out = take((size_t)c->max_seq * 4);
   s.chunk = take((size_t)LOGIT_CHUNK * c->vocab * 4);
+  s.score = take((size_t)LOGIT_CHUNK * (2 + 2 * KIE_MAX_TOP) * 4);  // what a chunk's logits say of its tokens
   // forced and returned expert selections of one forced-decode launch (sparse MoE)
   s.route_in = take((size_t)LOGIT_CHUNK * L * topk * 4);
   s.route_out = take((size_t)LOGIT_CHUNK * L * topk * 4);
@@ -845,6 +846,65 @@ int kie_decode_forced(kie_ctx *ctx, int n, const int32_t *forced, int32_t *out_t
 int kie_decode_forced_routed(kie_ctx *ctx, int n, const int32_t *forced, const int32_t *forced_experts,
                              int32_t *out_tokens, float *out_logits, int32_t *out_experts) {
   return decode_forced_impl(ctx, n, forced, forced_experts, out_tokens, out_logits, out_experts, true);
+}
+
+int kie_decode_score(kie_ctx *ctx, int n, const int32_t *tokens, int top, float *logprob, float *entropy, int32_t *top_ids,
+                     float *top_logprobs) {
+  if (!ctx) return KIE_ERR_INVALID;
+  if (n < 1 || !tokens || !logprob) return fail(ctx, KIE_ERR_INVALID, "scoring needs n >= 1, tokens and logprob");
+  const int V = ctx->cfg.vocab;
+  if (top < 0 || top > KIE_MAX_TOP || top > V) return fail(ctx, KIE_ERR_INVALID, "top must be from 0 to KIE_MAX_TOP and at most vocab");
+  if (top > 0 && (!top_ids || !top_logprobs)) return fail(ctx, KIE_ERR_INVALID, "top_ids or top_logprobs is NULL");
+  if (!ctx->has_logits) return fail(ctx, KIE_ERR_INVALID, "decode before prefill: there are no current logits");
+  if ((long long)ctx->pos + n > ctx->cfg.max_seq) return fail(ctx, KIE_ERR_CAPACITY, "decode exceeds max_seq");
+  for (int i = 0; i < n; ++i)
+    if (tokens[i] < 0 || tokens[i] >= V) return fail(ctx, KIE_ERR_INVALID, "token id out of range");
+  const WsLayout &ws = ctx->plan.ws;
+  int *tin = (int *)(ctx->wsbuf + ws.tok_in);
+  float *chunk = (float *)(ctx->wsbuf + ws.chunk);
+  float *lp = (float *)(ctx->wsbuf + ws.score), *ent = lp + LOGIT_CHUNK, *tlp = ent + LOGIT_CHUNK;
+  int *tid = (int *)(tlp + (size_t)LOGIT_CHUNK * KIE_MAX_TOP);
+  // rows of logits and the tokens that they are of: the first token's are the current ones, the others the chunk's
+  const auto read_off = [&](const float *logits, int at, int rows) {
+    kie_token_logprobs_args a{};
+    a.logits = logits;
+    a.row_stride = V;
+    a.tokens = tin + at;
+    a.logprob = lp + at;
+    a.entropy = entropy ? ent + at : nullptr;
+    a.top_ids = top ? tid + at * top : nullptr;
+    a.top_logprobs = top ? tlp + at * top : nullptr;
+    a.n_rows = rows;
+    a.vocab = V;
+    a.top = top;
+    a.dtype = KIE_F32;
+    const int rc = kie_token_logprobs(&a, ctx->stream);
+    return rc == KIE_OK ? rc : fail(ctx, rc, kie_paged_last_error());
+  };
+  for (int done = 0; done < n;) {
+    const int m = std::min(LOGIT_CHUNK, n - done);
+    std::memcpy(ctx->pinned, tokens + done, (size_t)m * 4);
+    KIE_CUDA(ctx, cudaMemcpyAsync(tin, ctx->pinned, (size_t)m * 4, cudaMemcpyHostToDevice, ctx->stream));
+    int rc = read_off((const float *)(ctx->wsbuf + ws.logits), 0, 1);
+    if (rc == KIE_OK) rc = launch(ctx, m, kie::MODE_FORCED, 0, tin, nullptr, chunk);
+    if (rc == KIE_OK && m > 1) rc = read_off(chunk, 1, m - 1);
+    if (rc != KIE_OK) return rc;
+    const auto fetch = [&](void *out, const void *from, int each) {
+      return out ? cudaMemcpyAsync((char *)out + (size_t)done * each * 4, from, (size_t)m * each * 4, cudaMemcpyDeviceToHost,
+                                   ctx->stream)
+                 : cudaSuccess;
+    };
+    KIE_CUDA(ctx, fetch(logprob, lp, 1));
+    KIE_CUDA(ctx, fetch(entropy, ent, 1));
+    if (top) {
+      KIE_CUDA(ctx, fetch(top_ids, tid, top));
+      KIE_CUDA(ctx, fetch(top_logprobs, tlp, top));
+    }
+    rc = finish(ctx);
+    if (rc != KIE_OK) return rc;
+    done += m;
+  }
+  return KIE_OK;
 }
 
 int kie_get_logits(kie_ctx *ctx, float *out) {

@@ -171,21 +171,20 @@ __device__ __forceinline__ int plan_fork(const ForkArgs &a, int block, int block
   return total;
 }
 
-// After every block's plan_fork: the rows change, by all blocks of the grid, and pages that nobody holds any more go on the
-// list, by the first cluster.
+// After every block's plan_fork: pages that nobody holds any more go on the list, by the first cluster, and the rows change,
+// by the others where there are any.
 __device__ __forceinline__ void finish_fork(const ForkArgs &a, int left) {
   const cg::cluster_group cl = cg::this_cluster();
   const int R = a.n_seqs, tid = threadIdx.x, warp = tid >> 5;
-  const int block = blockIdx.x, blocks = gridDim.x;
+  const int block = blockIdx.x, parts = cl.num_blocks(), first = gridDim.x > parts ? parts : 0, blocks = gridDim.x - first;
   int *staged = static_cast<int *>(a.workspace);
-  for (int r = block * PS_WARPS + warp; r < R; r += blocks * PS_WARPS) {
+  for (int r = block < first ? R : (block - first) * PS_WARPS + warp; r < R; r += blocks * PS_WARPS) {
     const int p = parent_of(a, r);
     if (p < 0 || p == r) continue;
     bool part;
     int *to = a.block_table + r * a.table_stride;
     for_each(staged + (int64_t)r * a.max_blocks, pages_of(a, a.lens[p], &part), [&](int j, int x) { to[j] = x; });
   }
-  const int parts = cl.num_blocks();
   if (block >= parts) return;
   __shared__ int s_freed[PS_CLUSTER];
   const int x0 = range_begin(a.n_blocks, block, parts), x1 = range_begin(a.n_blocks, block + 1, parts);
@@ -231,11 +230,10 @@ __global__ void __launch_bounds__(PS_THREADS) paged_fork_plan_kernel(const ForkA
   plan_fork(a, blockIdx.x, gridDim.x);
 }
 __global__ void __launch_bounds__(PS_THREADS) paged_fork_finish_kernel(const ForkArgs a) {
+  cg::this_cluster().sync();  // every block has begun, and others may write to its shared memory
   begin_after_previous();
   if (a.ok && !*a.ok) return;
-  const int left = __ldcg(a.n_free_out);
-  cg::this_cluster().sync();  // read by all before it changes
-  finish_fork(a, left);
+  finish_fork(a, __ldcg(a.n_free_out));  // the cluster's barriers lie between this and its change
 }
 
 

@@ -479,10 +479,11 @@ int kie_paged_attention(const kie_paged_attention_args *a, void *stream);
  * [0, n_seqs], a start below an earlier one as that one), and its positions below prefix_lens[g] (any length; what is
  * behind a row's own end is left out for that row) are read through the block table row of the longest of its query rows
  * (the first of those that reach the prefix's end); the positions behind, and those of rows in no group, through each
- * row's own. Rows of one sequence, a part of a prompt, are
- * such a group too: its prefix is what was cached before. n_groups <= KIE_PAGED_MAX_GROUPS; n_groups = 0 is
- * kie_paged_attention. The limits and the treatment of infinities are those of kie_paged_attention; a NaN or an infinity
- * in a prefix concerns the rows of its group alone.
+ * row's own. Rows of one sequence, a part of a prompt, are such a group too: its prefix is what was cached before. A prefix is
+ * read 64 positions at a time: what its last page holds behind its end may be read and is of no consequence. n_groups <=
+ * KIE_PAGED_MAX_GROUPS; n_groups = 0 is kie_paged_attention. The limits and the treatment of infinities are those of
+ * kie_paged_attention; a NaN or an infinity in a prefix concerns the rows of its group alone. K and V have to fit a tensor
+ * map; INVALID where CUDA refuses to make one of their strides.
  * a.workspace: kie_paged_prefix_attention_workspace bytes, 256-byte aligned, contents arbitrary before and after; calls
  * that may overlap need one each. */
 #define KIE_PAGED_MAX_GROUPS 4096

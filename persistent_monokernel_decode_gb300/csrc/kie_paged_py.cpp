@@ -1,5 +1,6 @@
-// Marshalling of the paged-cache operators and the log probabilities from tensors to the C ABI (include/kie.h): types, shapes and devices are
-// checked, outputs and the workspace allocated, and the call made on the current stream of the tensors' device. A call of
+// Marshalling of the paged-cache operators and the log probabilities from tensors to the C ABI (include/kie.h): types,
+// shapes and devices are checked, outputs and the workspace allocated, and the call made on the current stream of the
+// tensors' device. A call of
 // the attention takes 6.5 us of the host's time, of the append 3.4, of the release 5, of extend 8; marshalled in Python
 // they took 22, 12, 24 and 31 us, several times what the kernels of a small step do.
 //

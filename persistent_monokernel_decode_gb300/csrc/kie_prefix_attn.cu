@@ -1,19 +1,26 @@
-// The shared part of kie_paged_prefix_attention: attention of the rows of each group over the positions of their prefix.
-// The rows' own positions, and the sum of both, are kie_paged_attn.cu's.
+// kie_paged_prefix_attention: a plan, attention of the rows of each group over the positions of their prefix, the rows' own
+// positions beside it (kie_paged_attn.cu), and the join of the pieces of both.
 //
 // For one KV head, the query heads of a group's rows are the rows of a matrix: with 5 query heads a KV head, 25 sequences
 // fill the 128 rows of a tensor-core tile, so that what kie_paged_attn.cu has to do as matrix-vector products becomes
-// S = Q K^T and O += P V on tcgen05. Work is a list of items (group, tile of its rows, KV head), each a row of units of 64
-// positions; every block takes an equal run of the list and writes a piece (O, reference, sum of weights) for each item
-// that it has part in. The kernel of the rows' own positions joins the pieces where it finishes a row: hundreds of blocks
-// there read them side by side.
+// S = Q K^T and O += P V on tcgen05. A tile is two such halves, which share what is loaded of K and V. Work is a list of items
+// (group, tile of its rows, KV head), each a row of units of 64 positions; every block, one to an SM, takes an equal run of the
+// list and writes a piece (O, reference, sum of weights) for each item that it has part in.
 //
-// In a block one warp brings K and V tiles into a ring by TMA (two more turn E4M3 codes into fp16 on the way), one thread
-// issues the MMAs, and four warps hold the softmax: thread = row = TMEM lane, so its maxima and sums need no shuffles. S is
-// double-buffered in TMEM, so that the scores of the next tile are formed while this one's weights are; the weights go back
+// In a block a warp brings K and another V into a ring by TMA (one for both took 1,300 cycles for each 64 positions in pages
+// of 16), a warp issues the MMAs of each half (one for both, which waits for one half while the other could go on: 3,800
+// instead of 2,200 cycles a unit, 256 rows 70 instead of 64 us), four turn E4M3 codes into fp16 on the way where there are
+// codes, and four for each half hold the softmax: thread = row = TMEM lane, so its maxima and sums need no shuffles. S is
+// double-buffered in TMEM, so that the scores of the next unit are formed while this one's weights are; the weights go back
 // over the scores, as the TMEM operand of the second product. As in kie_paged_attn.cu, the softmax's reference stays within
 // 2^8 of the running maximum and O is only rescaled when a weight would pass 2^15, weights and fp32 queries are two 16-bit
 // parts, and the sum of weights is of the weights before they are rounded.
+//
+// Measured: 64 rows of 20 / 4 heads over 8,192 positions and up to 512 of their own, fp16, 36 us (plan 4, prefix 23, own
+// positions 3 more behind it, join 6); 256 rows of 16 / 4 heads in 8 groups over 4,096 and up to 1,024 of their own, bf16,
+// 64 us (5, 33, 21, 6); 4 rows over 1,024, 16 us (4, 9, 2, 3). The prefix kernel is bound by the chain QK, softmax, PV of a
+// half (2,200 cycles a unit; its MMAs alone are 900, the tensor pipe is busy for 24 to 35 %), and takes 5 us until its first
+// MMA; beside it one block of the other kernel fits an SM, so that large own parts run on behind it.
 #include <cuda.h>
 #include <float.h>
 #include <limits.h>
@@ -32,9 +39,9 @@ constexpr int PX_M = 128, PX_N = 64;       // rows of a half of a tile (an MMA's
 // Warps: four of the softmax for each half of a tile, the loaders of K and of V, one that issues the MMAs of each half, and
 // where the cache holds codes those that convert them.
 constexpr int PX_SOFT = 4, PX_LOADER = 8, PX_ISSUER = 10, PX_CONVERT = 12, PX_CONVERTERS = 4;
-// Registers of a thread: what the rows' own attention leaves of an SM with a block of its own there.
+// Registers of a thread: with 12 warps they leave room on the SM for a block of the rows' own attention on 16-bit pages.
 constexpr int PX_REGISTERS = 112;
-// Depth of what is kept per unit besides K and V. The loader is at most NS + RAW <= 6 halves ahead of the oldest one in use,
+// Depth of what is kept per unit besides K and V. The loaders are at most NS + RAW <= 6 halves ahead of the oldest one in use,
 // so at most four units ahead of the one whose weights are formed.
 constexpr int PX_TILES = 8;
 constexpr uint32_t PX_TMEM = 512;          // columns: for each half, S twice and O

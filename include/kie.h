@@ -380,7 +380,7 @@ int kie_paged_fork(const kie_paged_fork_args *a, void *stream);
 
 /* Pages copied inside a cache, K, V and scales of all layers: for each i, positions 0 .. rows[i] - 1 (rows NULL: all) of
  * page src[i] to page dst[i]. pages describes layer 0; the others follow k_layer_stride .. v_scale_layer_stride elements
- * apart (K and V: multiples of 16 bytes, from 0 to below 2^40; not read for one layer). A pair with a page outside [0,
+ * apart (above 0 and below 2^40, of K and V multiples of 16 bytes; not read for one layer). A pair with a page outside [0,
  * n_blocks), or of a page with itself, is left out. No page may be both a source and a destination, and no two
  * destinations may be the same. n_pairs * n_layers < 2^30. */
 typedef struct {

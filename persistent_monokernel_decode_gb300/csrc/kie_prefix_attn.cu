@@ -567,10 +567,11 @@ __device__ __forceinline__ void multiply_item(PxSmem<KIND, DH, SPLIT> &sm, uint3
         const uint64_t k = k0 + x.slot * SLOT;
         const uint32_t to = tmem + buf * PX_N;
 #pragma unroll
-        for (int p = 0; p < (SPLIT ? 2 : 1); ++p)
+        for (int p = SPLIT ? 1 : 0; p >= 0; --p)  // the second parts first: a large sum is cut off fewer times
 #pragma unroll
           for (int s = 0; s < DH / 16; ++s)
-            tc_mma(to, q0 + (p * KB + s / 4) * (PX_M * 8) + s % 4 * 2, k + s / 4 * (PX_N * 8) + s % 4 * 2, S_DESC, p || s ? 1u : 0u);
+            tc_mma(to, q0 + (p * KB + s / 4) * (PX_M * 8) + s % 4 * 2, k + s / 4 * (PX_N * 8) + s % 4 * 2, S_DESC,
+                   p < (SPLIT ? 1 : 0) || s ? 1u : 0u);
         tc_commit(&sm.s_full[w][buf]);
         tc_commit(&sm.empty[x.slot]);
         if (parts == 1) tc_commit(&sm.empty[x.slot]);

@@ -588,10 +588,10 @@ __device__ __forceinline__ void multiply_item(PxSmem<KIND, DH, SPLIT> &sm, uint3
         const uint64_t v = v0 + x.slot * SLOT;
         const uint32_t to = tmem + 2 * PX_N, p = tmem + buf * PX_N;
 #pragma unroll
-        for (int s = 0; s < PX_N / 16; ++s)
+        for (int part = 1; part >= 0; --part)  // as above
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
-            tc_mma_ts(to, p + s * 16 + part * 8, v + s * 128, O_DESC, j > 1 || s || part ? 1u : 0u);
+          for (int s = 0; s < PX_N / 16; ++s)
+            tc_mma_ts(to, p + s * 16 + part * 8, v + s * 128, O_DESC, j > 1 || s || !part ? 1u : 0u);
         tc_commit(&sm.pv_done[w][buf]);
         tc_commit(&sm.empty[x.slot]);
         if (parts == 1) tc_commit(&sm.empty[x.slot]);

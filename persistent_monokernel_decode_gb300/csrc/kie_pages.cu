@@ -22,10 +22,10 @@ namespace cg = cooperative_groups;
 
 constexpr int PS_THREADS = 1024, PS_WARPS = PS_THREADS / 32;
 constexpr int PS_CLUSTER = 8;  // the portable most
-// Up to these sizes (entries of the table, pages of the cache) one block does it all: a fork of 64 rows over a table of 4,672
-// entries takes 10.9 us so and 11.4 in two launches, of 128 rows over 16,512 entries 14.8 and 11.2; a compaction of 512 pages
-// 5.2 and 7.0, of 4,096 pages 7.8 and 7.5, of 16,384 17.9 and 8.8.
-constexpr int PS_SMALL_TABLE = 6144, PS_SMALL_CACHE = 4096;
+// Up to these sizes (entries of the table, pages of the cache) one block does it all: a fork of 32 rows over a table of 2,336
+// entries takes 8.5 us so and 9.9 in two launches, of 64 rows over 4,672 entries 10.8 and 10.6, of 128 over 16,512 14.6 and
+// 9.7; a compaction of 512 pages 5.1 and 6.9, of 4,096 pages 7.9 and 7.3, of 16,384 17.9 and 8.8.
+constexpr int PS_SMALL_TABLE = 4096, PS_SMALL_CACHE = 2048;
 
 // Exclusive prefix of the flags over the block's threads, in thread order; *all gets their number. Every thread calls.
 __device__ __forceinline__ int rank_of(bool flag, int *all) {

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(CLUSTER ? LP_FEW : LP_MANY, CLUSTER ? 4 : 10) 
     const float high = up.most();
     if (!(high <= most)) {
       next_most = most;
-      most = high;  // a NaN stays: whatever follows counts as more
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(high));  // a NaN stays, and from the next round on next_most is one too
       most_round = round;
     } else if (high > next_most) {
       next_most = high;

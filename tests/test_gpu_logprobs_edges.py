@@ -1,0 +1,51 @@
+"""Log probabilities at the limits of their numbers (NaN, a type's lowest value, large distances), in the form of a block to
+a row and in that of a cluster."""
+import math
+
+import pytest
+import torch
+
+import persistent_monokernel_decode_gb300 as kie
+from test_gpu_logprobs import draw
+from test_gpu_paged import BF16, F16, F32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    kie.build()
+    yield
+
+
+# Rows and vocabulary: a block to a row, two blocks, eight; each thread goes through several rounds of its row.
+FORMS = [(300, 32000), (63, 32003), (4, 262147)]
+
+
+def check_ids(got, x, rows, top):
+    """The ids of rows with NaN, which count above +inf, the lowest id first."""
+    want = torch.sort(x[rows].double(), dim=1, descending=True, stable=True).indices[:, :top]
+    assert torch.equal(got.top_ids[rows].long(), want)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("N,V", FORMS)
+@pytest.mark.parametrize("top", [0, 1, 20])
+def test_a_nan_anywhere_in_a_row(dtype, N, V, top):
+    """In the first round of a thread, in those between and in the last, alone and with others or +inf."""
+    at = [0, 1, 7, 3000, V // 3, V // 2 + 1, 5 * V // 8, V - 4097, V - 2, V - 1]
+    for i in range(0, len(at), 4):
+        x, tokens = draw(N, V, dtype, seed=i)
+        tokens[:] = torch.arange(N, device="cuda") % V
+        few = at[i:i + 4]
+        for r, k in enumerate(few):
+            x[r, k] = math.nan
+            if i:
+                x[r, (k + 12345) % V], x[r, (k + 777) % V] = math.nan, math.inf
+        rows = list(range(min(len(few), N)))
+        got = kie.token_logprobs(x, tokens, top=top)
+        assert torch.isnan(got.logprob[rows]).all() and torch.isnan(got.entropy[rows]).all()
+        assert torch.isnan(got.top_logprobs[rows]).all()
+        check_ids(got, x, rows, top)
+        if N > len(few):
+            assert not torch.isnan(got.logprob[len(few):]).any() and not torch.isnan(got.entropy[len(few):]).any()

@@ -82,7 +82,9 @@ struct Piece {
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  // The elements, two by two, none below a finite value whose weight is 0 (against a maximum above -10^37).
+  // Against a row's maximum from LOW up, what pair() makes of -inf has a weight of 0.
+  static constexpr float LOW = X == KIE_F16 ? -65000.f : -1e37f;
+  // The elements, two by two, none below a finite value.
   __device__ __forceinline__ float2 pair(int k) const {
     if (X == KIE_F32) return make_float2(fmaxf(get(2 * k), -1e38f), fmaxf(get(2 * k + 1), -1e38f));
     if (X == KIE_F16) return __half22float2(__hmax2(*reinterpret_cast<const __half2 *>(&w[k & 3]), __float2half2_rn(-65504.f)));
@@ -341,7 +343,8 @@ __global__ void __launch_bounds__(CLUSTER ? LP_FEW : LP_MANY, CLUSTER ? 4 : 10) 
   const float m = value_of(best), base_m = m == -INFINITY ? 0.f : m;
   // ---- the sums at the row's maximum
   float s = 0.f, t = 0.f;
-  if (!(fabsf(base_m) < 1e37f) || far) {  // differences may leave the range, or there is an infinity or NaN: once more
+  // once more where differences may leave the range, where there is an infinity or NaN, and where -inf has counted
+  if (!(base_m >= P::LOW && base_m < 1e37f) || far) {
 #pragma unroll 1
     for (int u = u0 + tid; u < u1; u += LP_THREADS) {
       const P x = fetch(u);

@@ -6,8 +6,8 @@ import pytest
 import torch
 
 import persistent_monokernel_decode_gb300 as kie
-from test_gpu_logprobs import draw
-from test_gpu_paged import BF16, F16, F32
+from test_gpu_logprobs import check, draw
+from test_gpu_paged import BF16, F16, F32, ints
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,32 @@ def test_a_nan_anywhere_in_a_row(dtype, N, V, top):
         check_ids(got, x, rows, top)
         if N > len(few):
             assert not torch.isnan(got.logprob[len(few):]).any() and not torch.isnan(got.entropy[len(few):]).any()
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("N,V", [(5, 10), (5, 1000), (300, 4097), *FORMS])
+def test_rows_at_the_lowest_value(dtype, N, V):
+    """Masked throughout, masked and ruled out, one token a little above the mask; with and without a piece cut off at either
+    end of a row."""
+    lowest = torch.finfo(dtype).min
+    for at, extra in ((0, 0), (3, 5)):
+        wide = torch.zeros((N, V + extra), device="cuda", dtype=dtype)
+        x = wide[:, at:at + V]
+        x[:] = draw(N, V, dtype)[0]
+        near = float(torch.tensor(lowest, dtype=torch.float64) * (1 - torch.finfo(dtype).eps))
+        x[0] = lowest
+        x[1], x[1, :10] = -math.inf, lowest
+        x[2], x[2, V // 2] = lowest, near
+        x[3], x[3, ::2] = lowest, -math.inf
+        for top in (0, min(V, 9)):
+            check(x, ints([1, 1, V // 2, 1] + [0] * (N - 4)), top)
+
+
+def test_fp16_rows_next_to_the_lowest_value():
+    """The largest logit steps of 32 above the lowest: what is at the lowest then counts in full, hardly, or not."""
+    x = torch.full((12, 1001), -65504.0, device="cuda").half()
+    for r in range(12):
+        x[r, r::50] = -65504.0 + 32 * r
+    x[6:, 500:] = -math.inf
+    check(x, ints([0, 1] * 6), 20)
+    check(x[:2].repeat(200, 1), ints([0, 1] * 200), 20)

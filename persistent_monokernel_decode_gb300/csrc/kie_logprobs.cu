@@ -243,7 +243,8 @@ __global__ void __launch_bounds__(CLUSTER ? LP_FEW : LP_MANY, CLUSTER ? 4 : 10) 
     if (!(high <= ref + LP_STEP) || !any) {  // seldom but for the first time
       far = far || (!(fabsf(high) < 1e37f) && high != -INFINITY);
       if (high != -INFINITY && !far) {
-        const float by = any ? ref - high : 0.f, f = ex2(by * LOG2E);  // t + s (old - new reference), s, both times f
+        // t + s (old - new reference), s, both times f. s times a distance whose f is 0 shall be finite
+        const float by = any ? fmaxf(ref - high, LP_LEAST) : 0.f, f = ex2(by * LOG2E);
         const unsigned long long f2 = two(f, f), by2 = two(by, by);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {

@@ -78,3 +78,17 @@ def test_fp16_rows_next_to_the_lowest_value():
     x[6:, 500:] = -math.inf
     check(x, ints([0, 1] * 6), 20)
     check(x[:2].repeat(200, 1), ints([0, 1] * 200), 20)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("N,V", [(300, 32000), (300, 262147), (4, 1000003)])
+@pytest.mark.parametrize("mask", [-9e36, -5e36, -1.5e36, -1e30, -3e38])
+def test_rows_that_begin_far_below_the_rest(dtype, N, V, mask):
+    """A thread whose first rounds hold a large negative mask, and a few ordinary logits behind: everywhere at the row's
+    beginning, and at that of each eighth."""
+    x, tokens = draw(N, V, dtype)
+    i = torch.arange(V, device="cuda")
+    x[0::2, : V * 7 // 8] = mask
+    x[1::2, i * 8 % V < V * 9 // 10] = mask
+    tokens[:] = V - 1
+    check(x, tokens, 4)

@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(CLUSTER ? LP_FEW : LP_MANY, CLUSTER ? 4 : 10) 
         for (int e = 0; e < P::N; ++e) {
           const int id = piece_of(u) * P::N - skew + e;
           const Key key = (Key)order_of(x.get(e)) << 32 | (uint32_t)~id;
-          if (key < last && key > next && id >= 0 && id < V) next = key;
+          if ((k == 0 || key < last) && key > next && id >= 0 && id < V) next = key;  // a NaN at id 0 is the largest key there is
         }
       }
 #pragma unroll

@@ -92,3 +92,16 @@ def test_rows_that_begin_far_below_the_rest(dtype, N, V, mask):
     x[1::2, i * 8 % V < V * 9 // 10] = mask
     tokens[:] = V - 1
     check(x, tokens, 4)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("N,V", [(5, 600), (300, 600), (300, 3000), *FORMS])
+def test_rows_of_nan_and_a_nan_ahead_of_ties(dtype, N, V):
+    """More candidates than a row's list holds, with a NaN at id 0 among them."""
+    x, tokens = torch.zeros((N, V), device="cuda", dtype=dtype), ints([0] * N)
+    x[0], x[1, 0], x[2, [0, V - 1]], x[3, 0], x[3, 1:] = math.nan, math.nan, math.nan, math.nan, -math.inf
+    for top in (1, 8, 32):
+        got = kie.token_logprobs(x, tokens, top=top)
+        check_ids(got, x, list(range(4)), top)
+        assert torch.isnan(got.logprob[:4]).all() and torch.isnan(got.top_logprobs[:4]).all()
+        check(x[4:], tokens[4:], top) if N > 4 else None

@@ -796,7 +796,7 @@ __device__ __forceinline__ void stage_queries(const PrefixArgs &a, PxSmem<KIND, 
         int e2 = 0;
         if (top > 0.f && top <= FLT_MAX) e2 = max(-120, min(120, 140 - (int)(__float_as_uint(top) >> 23)));
         up *= __int_as_float((127 + e2) << 23);
-        rs *= __int_as_float((127 - e2) << 23);
+        rs = fmaxf(rs * __int_as_float((127 - e2) << 23), FLT_MIN);  // not 0: the scores of masked positions stay -inf
       }
       const int half = r >= rows0, place = half ? r - rows0 : r;
       if (lane == 0) sm.rs[half][place] = rs;

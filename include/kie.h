@@ -484,6 +484,10 @@ int kie_paged_attention(const kie_paged_attention_args *a, void *stream);
  * KIE_PAGED_MAX_GROUPS; n_groups = 0 is kie_paged_attention. The limits and the treatment of infinities are those of
  * kie_paged_attention; a NaN or an infinity in a prefix concerns the rows of its group alone. K and V have to fit a tensor
  * map; INVALID where CUDA refuses to make one of their strides.
+ * Inside the call, blocks wait for their own loads and products, microseconds as a rule. A wait that takes longer than two
+ * seconds (kie_paged_set_timeout_ns; a GPU that is taken from the process for that long) ends its block's work: what the
+ * block had in hand and had still to do is NaN, in out and in lse, for every query head that it concerns. The call itself
+ * returned KIE_OK before.
  * a.workspace: kie_paged_prefix_attention_workspace bytes, 256-byte aligned, contents arbitrary before and after; calls
  * that may overlap need one each. */
 #define KIE_PAGED_MAX_GROUPS 4096
@@ -493,6 +497,15 @@ typedef struct {
   int n_groups;
 } kie_paged_prefix_attention_args;
 int kie_paged_prefix_attention(const kie_paged_prefix_attention_args *a, void *stream);
+
+/* How long a wait inside kie_paged_prefix_attention may take, in nanoseconds (2e9 at first): for all later calls of the
+ * process; a captured call keeps the limit of its capture. Errors: INVALID (0). */
+int kie_paged_set_timeout_ns(uint64_t ns);
+
+/* Test hook (fault injection on the host side of the contract): block `block` of the next kie_paged_prefix_attention call
+ * loads nothing from the half-th K or V of 64 positions on that it has to do with (0: nothing at all), so that its waits
+ * for them run out; -1: takes that back. No GPU fault, trap or unbounded wait is involved. */
+int kie_paged_debug_stop_loads(int block, int half);
 
 /* Bytes of kie_paged_prefix_attention's workspace on the current device (0: bad arguments or no device). */
 size_t kie_paged_prefix_attention_workspace(int n_seqs, int n_heads, int n_kv_heads, int head_dim);

@@ -291,6 +291,8 @@ SIGNATURES = {
     "kie_paged_attention_workspace": ([ctypes.c_int] * 3, ctypes.c_size_t),
     "kie_paged_prefix_attention": ([P, P], ctypes.c_int),
     "kie_paged_prefix_attention_workspace": ([ctypes.c_int] * 4, ctypes.c_size_t),
+    "kie_paged_set_timeout_ns": ([ctypes.c_uint64], ctypes.c_int),
+    "kie_paged_debug_stop_loads": ([ctypes.c_int, ctypes.c_int], ctypes.c_int),
     "kie_paged_fork": ([P, P], ctypes.c_int),
     "kie_paged_copy": ([P, P], ctypes.c_int),
     "kie_paged_compact": ([P, P], ctypes.c_int),
@@ -594,4 +596,4 @@ def rows_of_cta(M: int, n_cta: int, cta: int):
 # ---- paged K/V cache for a batch of sequences ----------------------------------------------------------------
 from .paged import (PagedCache, PagedFork, PagedMoves, PagedStep, TokenLogprobs, paged_append,  # noqa: E402,F401
                     paged_attention, paged_compact, paged_copy, paged_extend, paged_fork, paged_prefix_attention,
-                    paged_release, rope_table, token_logprobs)
+                    paged_release, paged_set_timeout_ns, rope_table, token_logprobs)

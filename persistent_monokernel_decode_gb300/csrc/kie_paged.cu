@@ -4,6 +4,7 @@
 #include <stdio.h>
 
 #include <algorithm>
+#include <atomic>
 #include <initializer_list>
 
 #include "kie_device.cuh"
@@ -510,6 +511,10 @@ const char *check_written_pages(const kie_pages &pg) {
   return nullptr;
 }
 
+// What the prefix kernel's waits are given: their limit, and a test's block and half from which on nothing is loaded.
+constexpr uint64_t NO_STOP = ~0ull;
+std::atomic<uint64_t> g_wait_ns{2000000000ull}, g_stop{NO_STOP};
+
 bool heads_fit(int n_heads, int n_kv_heads, int head_dim) {
   return n_kv_heads >= 1 && n_heads >= 1 && n_heads % n_kv_heads == 0 && n_heads / n_kv_heads <= PAGED_MAX_GROUP &&
          (head_dim == 64 || head_dim == 128);
@@ -658,6 +663,18 @@ size_t kie_paged_prefix_attention_workspace(int n_seqs, int n_heads, int n_kv_he
   return kie_paged_prefix_workspace_bytes(n_seqs, n_heads, n_kv_heads, head_dim, sms);
 }
 
+int kie_paged_set_timeout_ns(uint64_t ns) {
+  if (ns == 0) return refuse("the limit must be above 0");
+  g_wait_ns.store(ns, std::memory_order_relaxed);
+  return KIE_OK;
+}
+
+int kie_paged_debug_stop_loads(int block, int half) {
+  if (block >= 0 && half < 0) return refuse("half must be >= 0");
+  g_stop.store(block < 0 ? NO_STOP : (uint64_t)block << 32 | (uint32_t)half, std::memory_order_relaxed);
+  return KIE_OK;
+}
+
 int kie_paged_prefix_attention(const kie_paged_prefix_attention_args *p, void *stream) {
   if (!p) return refuse("the arguments are NULL");
   const kie_paged_attention_args &a = p->a;
@@ -672,7 +689,9 @@ int kie_paged_prefix_attention(const kie_paged_prefix_attention_args *p, void *s
   const size_t need = kie_paged_prefix_workspace_bytes(a.n_seqs, a.n_heads, a.pages.n_kv_heads, a.pages.head_dim, sms);
   if (!a.workspace || a.workspace_bytes < need || !aligned(a.workspace, 256))
     return refuse("the workspace is NULL, unaligned (256 bytes) or smaller than kie_paged_prefix_attention_workspace");
-  const cudaError_t e = p->n_groups ? kie_launch_paged_prefix(*p, dev, sms, (cudaStream_t)stream)
+  const uint64_t stop = g_stop.exchange(NO_STOP, std::memory_order_relaxed);
+  const cudaError_t e = p->n_groups ? kie_launch_paged_prefix(*p, g_wait_ns.load(std::memory_order_relaxed), (int)(stop >> 32),
+                                                              (int)(uint32_t)stop, dev, sms, (cudaStream_t)stream)
                                     : kie_launch_paged_attention(a, dev, sms, (cudaStream_t)stream);
   if (e == cudaErrorInvalidPitchValue) return refuse("no tensor map can be made of the pages' strides");
   return finish(e, "paged_prefix_attention");

@@ -118,6 +118,8 @@ struct PrefixArgs : kie_paged_attention_args {
   int32_t *row_lo;  // lo of each row
   float *prefix, *own;
   float2 *prefix_ml, *own_ml;
+  unsigned long long wait_ns;  // how long a wait may take
+  int stop_block, stop_half;   // a test's: this block (-1: none) loads nothing from its stop_half-th half of a unit on
 };
 
 // The kernels find the rows' ends in lens, be they lengths or a step's positions, and the number of table rows in n_table.
@@ -142,7 +144,8 @@ cudaError_t kie_launch_paged_compact(const kie_paged_compact_args &a, int dev, i
 cudaError_t kie_launch_paged_copy(const kie_paged_copy_args &a, cudaStream_t stream);
 cudaError_t kie_launch_token_logprobs(const kie_token_logprobs_args &a, int sms, cudaStream_t stream);
 cudaError_t kie_launch_paged_own(const kie::PrefixArgs &a, int dev, int sms, cudaStream_t stream);
-cudaError_t kie_launch_paged_prefix(const kie_paged_prefix_attention_args &a, int dev, int sms, cudaStream_t stream);
+cudaError_t kie_launch_paged_prefix(const kie_paged_prefix_attention_args &a, unsigned long long wait_ns, int stop_block,
+                                    int stop_half, int dev, int sms, cudaStream_t stream);
 size_t kie_paged_prefix_workspace_bytes(int n_seqs, int n_heads, int n_kv_heads, int head_dim, int sms);
 cudaError_t kie_launch_paged_attention(const kie_paged_attention_args &a, int dev, int sms, cudaStream_t stream);
 size_t kie_paged_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim, int sms);

@@ -45,7 +45,6 @@ constexpr int PX_REGISTERS = 112;
 // so at most four units ahead of the one whose weights are formed.
 constexpr int PX_TILES = 8;
 constexpr uint32_t PX_TMEM = 512;          // columns: for each half, S twice and O
-constexpr unsigned long long PX_TIMEOUT_NS = 2000000000ull;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float P_BIAS = 7.f, P_STEP = 8.f;  // weights are 2^7 2^(v - reference), below 2^15
 constexpr float MIN_LOG2_SCALE = -60.f, MAX_LOG2_SCALE = 127.f;  // of E4M3 values, as in kie_paged_attn.cu
@@ -60,6 +59,13 @@ struct PxShape {
   static constexpr int THREADS = 32 * (PX_CONVERT + (KIND == PG_E4M3 ? PX_CONVERTERS : 0));
 };
 
+// Of the block's waits: how long each may take, and whether one took longer. Then the barriers' phases no longer tell what
+// has happened, so that nothing that waits on them goes on: the block gives up (see prefix_kernel).
+struct Waits {
+  unsigned long long limit_ns;
+  int failed;
+};
+
 template <int KIND, int DH, bool SPLIT>
 struct PxSmem {
   using T = PxShape<KIND, DH, SPLIT>;
@@ -72,8 +78,9 @@ struct PxSmem {
   float rs[2][PX_M];             // score scale of a row, in log2 units
   uint64_t full[T::NS], empty[T::NS], unit[PX_TILES], s_full[2][2], p_full[2][2], pv_done[2][2], fix, raw_full[T::RAW], raw_empty[T::RAW];
   int reach;                     // positions of the prefix that the longest row of the group has
+  int sent[2];                   // units of K and of V that the loaders have brought for the item
   uint32_t tmem;
-  int failed;
+  Waits waits;
 };
 
 // 32 consecutive columns of the warp's 32 TMEM lanes, a lane's to each thread. Nothing waits for them here.
@@ -169,16 +176,16 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, in
 }
 __device__ __forceinline__ void fence_async_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Waits for a phase of a barrier of this block, two seconds at most; false if that ran out, here or in another wait.
-__device__ __forceinline__ bool px_wait(uint64_t *bar, uint32_t parity, int *failed) {
+// Waits for a phase of a barrier of this block, for a limited time; false if that ran out, here or in another wait.
+__device__ __forceinline__ bool px_wait(uint64_t *bar, uint32_t parity, Waits *waits) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
   for (int spins = 1;; ++spins) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((spins & 63) == 0) {
-      if (*static_cast<volatile int *>(failed)) return false;
-      if (globaltimer() - t0 > PX_TIMEOUT_NS) {
-        *static_cast<volatile int *>(failed) = 1;
+      if (*static_cast<volatile int *>(&waits->failed)) return false;
+      if (globaltimer() - t0 > waits->limit_ns) {
+        *static_cast<volatile int *>(&waits->failed) = 1;
         return false;
       }
     }
@@ -186,8 +193,15 @@ __device__ __forceinline__ bool px_wait(uint64_t *bar, uint32_t parity, int *fai
 }
 
 // The same for a whole warp at once.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int *failed) {
-  return __all_sync(0xffffffffu, px_wait(bar, parity, failed)) != 0;
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, Waits *waits) {
+  return __all_sync(0xffffffffu, px_wait(bar, parity, waits)) != 0;
+}
+
+// After a failure: for a copy or products that are under way, for the same time at most, whatever else has run out.
+__device__ __noinline__ void settle(uint64_t *bar, uint32_t parity, const Waits *waits) {
+  const uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer() - t0 > waits->limit_ns) return;
 }
 
 // K and V of the cache as tensors of four dimensions: dims, and three that order tells, two bits each (0 position, 1 head, 2
@@ -387,10 +401,12 @@ __device__ __forceinline__ int unit_of(int i, int n, bool *is_v) {
 }
 
 // The warp that loads K, or V. Finds the group's longest row (the first of them), through whose table row the prefix is read, and loads, without
-// waiting for the queries. Returns the number of units, all of them with positions.
+// waiting for the queries. Returns the number of units, all of them with positions. *mending: the last copy is one of V's end, and
+// did not come in time.
 template <int KIND, int DH, bool SPLIT>
 __device__ __forceinline__ int load_item(const PrefixArgs &a, const PrefixMaps &maps, PxSmem<KIND, DH, SPLIT> &sm, const Group &x,
-                                         bool is_v, int h, int u0, int u1, uint32_t tiles, uint32_t halves, uint32_t &fixes) {
+                                         bool is_v, int h, int u0, int u1, uint32_t tiles, uint32_t halves, uint32_t &fixes,
+                                         bool *mending) {
   using T = PxShape<KIND, DH, SPLIT>;
   constexpr bool CODES = KIND == PG_E4M3;
   constexpr int NS = CODES ? T::RAW : T::NS, KB = CODES ? 1 : DH / 64;
@@ -452,7 +468,8 @@ __device__ __forceinline__ int load_item(const PrefixArgs &a, const PrefixMaps &
     const uint32_t half = halves + half_of(u, n, is_v), slot = half % NS;
     turn_to(unit);
     const uint32_t live = __ballot_sync(0xffffffffu, page_a >= 0) >> ((unit - batch) * 4) & 15u;
-    if (!warp_wait(&empty[slot], (half / NS & 1u) ^ 1u, &sm.failed)) return false;
+    if (blockIdx.x == a.stop_block && half >= a.stop_half) return false;
+    if (!warp_wait(&empty[slot], (half / NS & 1u) ^ 1u, &sm.waits)) return false;
     // rows of V behind the end would meet weights of 0 as whatever they hold: they become zeros before the MMA may begin
     const int tail = reach - unit * PX_N;
     const bool mend = !CODES && is_v && tail < PX_N;
@@ -474,7 +491,7 @@ __device__ __forceinline__ int load_item(const PrefixArgs &a, const PrefixMaps &
     }
     __syncwarp();
     if (mend) {
-      if (!warp_wait(&sm.fix, fixes++ & 1u, &sm.failed)) return false;
+      if (!warp_wait(&sm.fix, fixes++ & 1u, &sm.waits)) return *mending = true, false;
       for (int k = tail * 8 + lane; k < PX_N * 8; k += 32)
 #pragma unroll
         for (int b = 0; b < KB; ++b)
@@ -505,10 +522,29 @@ __device__ __forceinline__ int load_item(const PrefixArgs &a, const PrefixMaps &
     }
     return true;
   };
+  int sent = 0;
 #pragma unroll 1
-  for (int u = 0; u < n; ++u)
-    if (!load(u)) break;
+  while (sent < n && load(sent)) ++sent;
+  if (lane == 0) sm.sent[is_v] = sent;
   return n;
+}
+
+// A loader, when the block has given up and every warp has stopped: waits for its copies that are under way. Slots that were
+// asked for again since have been read, so that it is the ring's last round at most.
+template <int KIND, int DH, bool SPLIT>
+__device__ __forceinline__ void settle_loads(PxSmem<KIND, DH, SPLIT> &sm, bool is_v, int n, uint32_t halves, uint32_t fixes,
+                                             bool mending) {
+  using T = PxShape<KIND, DH, SPLIT>;
+  constexpr bool CODES = KIND == PG_E4M3;
+  constexpr int NS = CODES ? T::RAW : T::NS;
+  const int k = sm.sent[0], v = sm.sent[1], own = is_v ? v : k;
+  const int last = max(k > 0 ? half_of(k - 1, n, false) : -1, v > 0 ? half_of(v - 1, n, true) : -1);
+  for (int u = max(0, own - NS); u < own; ++u) {
+    const int i = half_of(u, n, is_v);
+    const uint32_t half = halves + i;
+    if (i + NS > last) settle(CODES ? &sm.raw_full[half % NS] : &sm.full[half % NS], half / NS & 1u, &sm.waits);
+  }
+  if (mending) settle(&sm.fix, (fixes - 1) & 1u, &sm.waits);
 }
 
 // PX_CONVERTERS warps: codes of the raw ring into fp16 in the other one, positions from the prefix's end on as zeros.
@@ -521,8 +557,8 @@ __device__ __forceinline__ void convert_item(PxSmem<KIND, DH, SPLIT> &sm, int ct
     bool is_v;
     const int tail = reach - (u0 + unit_of(i, n, &is_v)) * PX_N;
     const uint32_t half = halves + i;
-    if (!warp_wait(&sm.raw_full[half % RAW], half / RAW & 1u, &sm.failed)) return;
-    if (!warp_wait(&sm.empty[half % NS], (half / NS & 1u) ^ 1u, &sm.failed)) return;
+    if (!warp_wait(&sm.raw_full[half % RAW], half / RAW & 1u, &sm.waits)) return;
+    if (!warp_wait(&sm.empty[half % NS], (half / NS & 1u) ^ 1u, &sm.waits)) return;
     const uint8_t *from = sm.raw[half % RAW] + chunk * 16;
     uint8_t *slot = sm.ring[half % NS] + (chunk >> 2) * (PX_N * 128);
 #pragma unroll
@@ -544,9 +580,10 @@ __device__ __forceinline__ void convert_item(PxSmem<KIND, DH, SPLIT> &sm, int ct
   }
 }
 
-// The warp that issues for half w of a tile, an elected lane of which does. parts: halves of the tile that have rows.
+// The warp that issues for half w of a tile, an elected lane of which does. parts: halves of the tile that have rows. Returns the
+// number of products that were issued: QK0, QK1, PV0, QK2, PV1, ..
 template <int KIND, int DH, bool SPLIT>
-__device__ __forceinline__ void multiply_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_t tmem, int w, int parts, int n,
+__device__ __forceinline__ int multiply_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_t tmem, int w, int parts, int n,
                                               uint32_t units, uint32_t halves) {
   using T = PxShape<KIND, DH, SPLIT>;
   constexpr int NS = T::NS, KB = DH / 64;
@@ -558,10 +595,10 @@ __device__ __forceinline__ void multiply_item(PxSmem<KIND, DH, SPLIT> &sm, uint3
 #pragma unroll 1
   for (int j = 0; j <= n; ++j) {
     if (j < n) {  // S = Q K^T
-      const Half<NS> x(half++);
+      const Half<NS> x(half);
       const uint32_t tile = units + j, buf = tile & 1u;
-      if (!warp_wait(&sm.full[x.slot], x.round, &sm.failed)) return;
-      if (j >= 2 && !warp_wait(&sm.pv_done[w][buf], (tile - 2) >> 1 & 1u, &sm.failed)) return;  // unit j - 2 is done with it
+      if (!warp_wait(&sm.full[x.slot], x.round, &sm.waits)) return half - halves;
+      if (j >= 2 && !warp_wait(&sm.pv_done[w][buf], (tile - 2) >> 1 & 1u, &sm.waits)) return half - halves;  // unit j - 2 is done with it
       tc_fence_after();
       if (elect_one()) {
         const uint64_t k = k0 + x.slot * SLOT;
@@ -577,12 +614,13 @@ __device__ __forceinline__ void multiply_item(PxSmem<KIND, DH, SPLIT> &sm, uint3
         if (parts == 1) tc_commit(&sm.empty[x.slot]);
       }
       __syncwarp();
+      ++half;
     }
     if (j > 0) {  // O += P V
-      const Half<NS> x(half++);
+      const Half<NS> x(half);
       const uint32_t tile = units + j - 1, buf = tile & 1u;
-      if (!warp_wait(&sm.full[x.slot], x.round, &sm.failed)) return;
-      if (!warp_wait(&sm.p_full[w][buf], tile >> 1 & 1u, &sm.failed)) return;
+      if (!warp_wait(&sm.full[x.slot], x.round, &sm.waits)) return half - halves;
+      if (!warp_wait(&sm.p_full[w][buf], tile >> 1 & 1u, &sm.waits)) return half - halves;
       tc_fence_after();
       if (elect_one()) {
         const uint64_t v = v0 + x.slot * SLOT;
@@ -597,7 +635,20 @@ __device__ __forceinline__ void multiply_item(PxSmem<KIND, DH, SPLIT> &sm, uint3
         if (parts == 1) tc_commit(&sm.empty[x.slot]);
       }
       __syncwarp();
+      ++half;
     }
+  }
+  return half - halves;
+}
+
+// An issuer, when the block has given up and every warp has stopped: waits for the products that are under way, the last of
+// which are of two units at most.
+template <int KIND, int DH, bool SPLIT>
+__device__ __forceinline__ void settle_products(PxSmem<KIND, DH, SPLIT> &sm, int w, int n, uint32_t units, int issued) {
+  for (int i = max(0, issued - 4); i < issued; ++i) {
+    bool is_pv;
+    const uint32_t tile = units + unit_of(i, n, &is_pv);
+    settle(is_pv ? &sm.pv_done[w][tile & 1u] : &sm.s_full[w][tile & 1u], tile >> 1 & 1u, &sm.waits);
   }
 }
 
@@ -643,8 +694,8 @@ __device__ __forceinline__ bool soften_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_
   for (int j = 0; j < n; ++j) {
     const uint32_t place = (tiles + j) % PX_TILES, tile = units + j, t_s = tmem + (tile & 1u) * PX_N;
     const int left = lim - (u0 + j) * PX_N;  // positions of the unit that the row attends to
-    if (!warp_wait(&sm.unit[place], (tiles + j) / PX_TILES & 1u, &sm.failed)) return false;
-    if (!warp_wait(&sm.s_full[w][tile & 1u], tile >> 1 & 1u, &sm.failed)) return false;
+    if (!warp_wait(&sm.unit[place], (tiles + j) / PX_TILES & 1u, &sm.waits)) return false;
+    if (!warp_wait(&sm.s_full[w][tile & 1u], tile >> 1 & 1u, &sm.waits)) return false;
     tc_fence_after();
     if (rows) {
       const uint32_t live = sm.live[place];
@@ -685,7 +736,7 @@ __device__ __forceinline__ bool soften_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_
         m = mn;
         l *= f;
         if (j > 0) {
-          if (!warp_wait(&sm.pv_done[w][(tile - 1) & 1u], (tile - 1) >> 1 & 1u, &sm.failed)) return false;
+          if (!warp_wait(&sm.pv_done[w][(tile - 1) & 1u], (tile - 1) >> 1 & 1u, &sm.waits)) return false;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < DH; c += 16) {
@@ -731,7 +782,7 @@ __device__ __forceinline__ bool soften_item(PxSmem<KIND, DH, SPLIT> &sm, uint32_
     __syncwarp();
     if (lane == 0) mbar_arrive(&sm.p_full[w][tile & 1u]);
   }
-  if (n > 0 && !warp_wait(&sm.pv_done[w][(units + n - 1) & 1u], (units + n - 1) >> 1 & 1u, &sm.failed)) return false;
+  if (n > 0 && !warp_wait(&sm.pv_done[w][(units + n - 1) & 1u], (units + n - 1) >> 1 & 1u, &sm.waits)) return false;
   *m_out = m;
   *l_out = l;
   return true;
@@ -857,7 +908,7 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ PrefixMaps maps) {
       mbar_init(&sm.s_full[i / 2][i % 2], 1), mbar_init(&sm.p_full[i / 2][i % 2], PX_SOFT), mbar_init(&sm.pv_done[i / 2][i % 2], 1);
     mbar_init(&sm.fix, 1);
     fence_barrier_init();
-    sm.failed = 0;
+    sm.waits = {a.wait_ns, 0};
     asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.k) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.v) : "memory");
   }
@@ -883,17 +934,20 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ PrefixMaps maps) {
   int g = begin.g, item = begin.item;  // the item is the group's item-th: tile * heads + head
   Group x = group_of(a, g, begin.start, begin.end);
   long long place = begin.place;
+  bool lost = false;  // a wait has run out: this item's results, and those of whatever the block still has to do, are NaN
   for (;;) {
     // ---- an item, or this block's part of it: units [u0, u1)
     const int t = item / heads, h = item % heads, first = x.start + t * members;
     const int rows = min(members, x.end - first) * group, rows0 = min(rows, members / 2 * group);
     const int u0 = (int)max(0ll, v0 - place - PX_ITEM_COST), u1 = (int)min((long long)x.units, v1 - place - PX_ITEM_COST);
-    if (u1 > u0) {
-      int n;
+    const int mine = part < 2 && in_part < (part ? rows - rows0 : rows0) ? in_part + part * rows0 : -1;  // the row, of the tile
+    const int64_t slot = (int64_t)first * a.n_heads + h * rows + (int64_t)PX_TILE * blockIdx.x;
+    if (u1 > u0 && !lost) {
+      int n, issued = 0;
+      bool mending = false;
       if (warp == PX_LOADER || warp == PX_LOADER + 1) {
-        n = load_item<KIND, DH, SPLIT>(a, maps, sm, x, warp != PX_LOADER, h, u0, u1, tiles, halves, fixes);
+        n = load_item<KIND, DH, SPLIT>(a, maps, sm, x, warp != PX_LOADER, h, u0, u1, tiles, halves, fixes, &mending);
       } else {
-        const int mine = part < 2 && in_part < (part ? rows - rows0 : rows0) ? in_part + part * rows0 : -1;  // the row, of the tile
         const int lim = mine >= 0 ? min(x.prefix, length_of(a, first + mine / group)) : 0;
         stage_queries<KIND, DH, SPLIT>(a, sm, first, h, group, rows0, rows);
         fence_async_proxy();
@@ -903,7 +957,7 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ PrefixMaps maps) {
         if (warp == PX_ISSUER || warp == PX_ISSUER + 1) {
           const int w = warp - PX_ISSUER;
           if (w == 0 || rows > rows0)
-            multiply_item<KIND, DH, SPLIT>(sm, tmem + w * (PX_TMEM / 2), w, rows > rows0 ? 2 : 1, n, w ? units[1] : units[0], halves);
+            issued = multiply_item<KIND, DH, SPLIT>(sm, tmem + w * (PX_TMEM / 2), w, rows > rows0 ? 2 : 1, n, w ? units[1] : units[0], halves);
         } else if (part >= 2) {
           if constexpr (KIND == PG_E4M3) convert_item<KIND, DH, SPLIT>(sm, tid - 32 * PX_CONVERT, reach, u0, n, halves);
         } else if (part == 0 || rows > rows0) {
@@ -911,7 +965,6 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ PrefixMaps maps) {
           const bool some = __any_sync(0xffffffffu, mine >= 0);
           const bool ok = soften_item<KIND, DH, SPLIT>(sm, my_tmem, part, in_part, some, lim, u0, n, tiles, part ? units[1] : units[0], &m, &l);
           // the piece: eight dimensions of a row at a time, rows side by side
-          const int64_t slot = (int64_t)first * a.n_heads + h * rows + (int64_t)PX_TILE * blockIdx.x;
           float *to = a.prefix + slot * DH + 8 * mine;
           tc_fence_after();
           if (some) {
@@ -931,18 +984,27 @@ prefix_kernel(const PrefixArgs a, const __grid_constant__ PrefixMaps maps) {
               }
             }
           }
-          // a wait that ran out shows as NaN in every result that it concerns
-          if (mine >= 0) a.prefix_ml[slot + mine] = make_float2(ok ? m - P_BIAS : 0.f, ok ? l : __int_as_float(0x7fc00000));
+          if (mine >= 0) a.prefix_ml[slot + mine] = make_float2(m - P_BIAS, l);
           tc_fence_before();
         }
+      }
+      lost = __syncthreads_or(*static_cast<volatile int *>(&sm.waits.failed)) != 0;  // whoever gave up sees its own mark
+      tc_fence_after();
+      if (lost) {  // no copy may land, and no product be formed, when the block has ended
+        if (warp == PX_LOADER || warp == PX_LOADER + 1)
+          settle_loads(sm, warp != PX_LOADER, n, halves, fixes, mending);
+        else if (warp == PX_ISSUER || warp == PX_ISSUER + 1)
+          settle_products(sm, warp - PX_ISSUER, n, warp == PX_ISSUER ? units[0] : units[1], issued);
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
       }
       tiles += n;
       units[0] += n;
       if (rows > rows0) units[1] += n;
       halves += 2 * n;
-      __syncthreads();
-      tc_fence_after();
     }
+    if (lost && u1 > u0 && mine >= 0) a.prefix_ml[slot + mine] = make_float2(0.f, __int_as_float(0x7fc00000));
     // ---- the next item
     if (place + PX_ITEM_COST + x.units >= v1) break;
     place += x.units + PX_ITEM_COST;
@@ -1146,7 +1208,8 @@ size_t kie_paged_prefix_workspace_bytes(int n_seqs, int n_heads, int n_kv_heads,
   return kie::Parts(n_seqs, n_heads, n_kv_heads, head_dim, sms).all;
 }
 
-cudaError_t kie_launch_paged_prefix(const kie_paged_prefix_attention_args &args, int dev, int sms, cudaStream_t stream) {
+cudaError_t kie_launch_paged_prefix(const kie_paged_prefix_attention_args &args, unsigned long long wait_ns, int stop_block,
+                                    int stop_half, int dev, int sms, cudaStream_t stream) {
   kie::PrefixArgs a;
   static_cast<kie_paged_attention_args &>(a) = kie::rows_in_lens(args.a);
   a.group_start = args.group_start;
@@ -1162,5 +1225,8 @@ cudaError_t kie_launch_paged_prefix(const kie_paged_prefix_attention_args &args,
   a.own_ml = reinterpret_cast<float2 *>(at + p.own_ml);
   a.own = reinterpret_cast<float *>(at + p.own);
   a.prefix = reinterpret_cast<float *>(at + p.prefix);
+  a.wait_ns = wait_ns;
+  a.stop_block = stop_block;
+  a.stop_half = stop_half;
   return a.pages.head_dim == 64 ? kie::launch_all<64>(a, dev, sms, stream) : kie::launch_all<128>(a, dev, sms, stream);
 }

@@ -154,6 +154,14 @@ def paged_prefix_attention(q, k_cache, v_cache, block_table, lens, group_start, 
                                                   return_lse, seqs, positions, group_start, prefix_lens)
 
 
+def paged_set_timeout_ns(ns: int) -> None:
+    """How long a wait inside paged_prefix_attention may take (2 seconds at first), for all later calls of the process: what
+    a wait that runs out concerns is NaN (kie_paged_set_timeout_ns)."""
+    if not 0 < ns < 1 << 64:
+        raise ValueError("ns must be above 0 and fit 64 bits")
+    lib().kie_paged_set_timeout_ns(ns)
+
+
 def rope_table(theta: float, head_dim: int, n_pos: int, device=None):
     """(cos, sin) of p * theta^(-2i / head_dim) for positions p < n_pos, in fp64 rounded to fp32 [n_pos, head_dim/2, 2]:
     the table that the decoder builds for itself."""

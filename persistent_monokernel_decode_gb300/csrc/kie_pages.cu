@@ -23,8 +23,8 @@ namespace cg = cooperative_groups;
 constexpr int PS_THREADS = 1024, PS_WARPS = PS_THREADS / 32;
 constexpr int PS_CLUSTER = 8;  // the portable most
 // Up to these sizes (entries of the table, pages of the cache) one block does it all: a fork of 32 rows over a table of 2,336
-// entries takes 8.5 us so and 9.9 in two launches, of 64 rows over 4,672 entries 10.8 and 10.6, of 128 over 16,512 14.6 and
-// 9.7; a compaction of 512 pages 5.1 and 6.9, of 4,096 pages 7.9 and 7.3, of 16,384 17.9 and 8.8.
+// entries takes 8.2 us so and 8.8 in two launches, of 64 rows over 4,672 entries 9.9 and 9.8, of 128 over 16,512 13.9 and
+// 8.9; a compaction of 512 pages 4.6 and 6.2, of 4,096 pages 6.7 and 7.2, of 16,384 16.0 and 8.2.
 constexpr int PS_SMALL_TABLE = 4096, PS_SMALL_CACHE = 2048;
 
 // Exclusive prefix of the flags over the block's threads, in thread order; *all gets their number. Every thread calls.
@@ -442,6 +442,8 @@ cudaError_t kie_launch_paged_fork(const kie::ForkArgs &a, int dev, int sms, cuda
     return e != cudaSuccess ? e : launch_after_previous(paged_fork_kernel, 1, PS_THREADS, smem, stream, a);
   }
   cudaError_t e = allow_smem(paged_fork_plan_kernel, &ready[1], dev, most);
+  // A block for every eight rows, though its warps take 32 neighbouring ones: three of four blocks only plan, or find nothing
+  // to do. Spreading the rows over all of them has not been measured.
   const int blocks = std::max(1, std::min(sms, (a.n_seqs + PS_WARPS / 4 - 1) / (PS_WARPS / 4)));
   if (e == cudaSuccess) e = launch_after_previous(paged_fork_plan_kernel, blocks, PS_THREADS, smem, stream, a);
   return e != cudaSuccess ? e : launch_clusters(paged_fork_finish_kernel, std::max(1, blocks / PS_CLUSTER), 0, stream, a);
